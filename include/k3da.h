@@ -283,6 +283,140 @@ int k3da_qk_norm_rope_yarn(void *qkv, int num_tokens, int num_q_heads, int num_k
                            const void *q_norm_w, const void *k_norm_w, float eps, float rope_base,
                            const k3da_yarn *yarn, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The paged cache of a running model: writing a chunk's K and V into it
+ * (plain or quantised), reading cached tokens back, and the attention of
+ * chunks of new tokens over it.  These calls serve what surrounds the
+ * drafter's block attention: filling the contexts k3da_attn reads (prefill),
+ * the target's check of drafted tokens, and decoding one token at a time.
+ * They have no counterpart on the page cited above.
+ *
+ * A batch is R requests, 1 <= R <= K3DA_MAX_CHUNK_REQUESTS.  Request r brings
+ * n_r >= 0 tokens, rows cu_seqlens[r] .. cu_seqlens[r+1] of the packed
+ * [num_tokens, ...] tensors (cu_seqlens: R + 1 int32, rising from 0); its
+ * token i is token ctx_lens[r] + i of its cache.  Rows from cu_seqlens[R] on
+ * belong to nobody: they are not read and what is written is left as it was
+ * there.  Any number of query heads per kv head from 1 to 16, at most 64 kv
+ * heads, head_dim 64.
+ *
+ * Every pointer is device memory of the current device.  As above: nothing
+ * is allocated or synchronised, lengths and pages are read by the kernels (a
+ * captured graph replays with them rewritten), and a violation only they can
+ * see sets a K3DA_STATUS_* bit and skips the access: a token past its page
+ * table row's page_stride * 64 (or before 0) BAD_LENGTH, a page id out of
+ * range BAD_PAGE.  The first call on a device should come before any stream
+ * capture.  num_tokens 0 is a call that does nothing.
+ */
+#define K3DA_MAX_CHUNK_REQUESTS 1024
+
+/* What a pool holds.  E4M3: kv_pool is [num_pages, 2, Hkv, 64, 64] e4m3
+ * codes and kv_scales [num_pages, 2, Hkv, 64] e8m0 bytes b, one for each
+ * token's K or V of one head; the row's values are code * 2^(b - 127).
+ * BF16: kv_scales is NULL. */
+typedef enum { K3DA_CACHE_BF16 = 0, K3DA_CACHE_E4M3 = 1 } k3da_cache_dtype;
+
+/* Cache tokens that token i of a request's chunk sees. */
+typedef enum {
+    K3DA_MASK_CAUSAL = 0,  /* c <= ctx_len + i */
+    K3DA_MASK_FULL = 1,    /* c < ctx_len + n: the whole chunk too, as a draft block */
+    K3DA_MASK_CONTEXT = 2  /* c < ctx_len: the chunk's own tokens are in no cache yet */
+} k3da_mask;
+
+/*
+ * k3da_kv_append -- write the k and v head rows of qkv into the cache.
+ *
+ *   kv_pool      [num_pages, 2, Hkv, 64, 64], written at the chunk's tokens
+ *                only.  16-byte aligned.  cache_dtype, kv_scales: above.
+ *   qkv          [num_tokens, (Hq + 2*Hkv)*64] bf16, k already normalised
+ *                and roped.  16-byte aligned.  Must not overlap kv_pool.
+ *   others       as for k3da_attn.
+ *
+ * bf16: the bits are copied.  e4m3: 2^(b - 127) is the smallest power of two
+ * that brings the row's largest magnitude to at most 448 (b = 0 for rows
+ * below 448 * 2^-127), codes are rounded to nearest even; a row with an
+ * infinity or a NaN gets b = 255 and reads back as NaN.  Two tokens of a
+ * call that share a cache slot (a page listed twice) leave one of the two.
+ */
+int k3da_kv_append(void *kv_pool, int cache_dtype, void *kv_scales, int64_t num_pages,
+                   const int32_t *page_table, int page_stride, const int32_t *ctx_lens,
+                   const int32_t *cu_seqlens, int num_requests, const void *qkv, int num_tokens,
+                   int num_q_heads, int num_kv_heads, int head_dim, int32_t *status, void *stream);
+
+/*
+ * k3da_kv_append_qknorm -- as k3da_kv_append, but k is raw: each k head row
+ * is normalised and roped (as by k3da_qk_norm_rope, same arithmetic) on its
+ * way into the cache, rounded once, and the q head rows, treated alike, go
+ * to q_out.  qkv itself is only read.  With a bf16 cache this leaves the
+ * bits of k3da_qk_norm_rope followed by k3da_kv_append.
+ *
+ *   positions, pos_dtype, q_norm_w, k_norm_w, eps, rope_base
+ *                as for k3da_qk_norm_rope; positions of rows behind the last
+ *                sequence are read and not used.
+ *   yarn         YaRN RoPE, or NULL for plain NeoX RoPE.
+ *   q_out        [num_tokens, Hq*64] bf16, 16-byte aligned, or NULL: no q
+ *                wanted.  Must not overlap qkv or kv_pool.
+ */
+int k3da_kv_append_qknorm(void *kv_pool, int cache_dtype, void *kv_scales, int64_t num_pages,
+                          const int32_t *page_table, int page_stride, const int32_t *ctx_lens,
+                          const int32_t *cu_seqlens, int num_requests, const void *qkv,
+                          int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                          const void *positions, int pos_dtype, const void *q_norm_w,
+                          const void *k_norm_w, float eps, float rope_base,
+                          const k3da_yarn *yarn, void *q_out, int32_t *status, void *stream);
+
+/*
+ * k3da_kv_gather -- read cached tokens back as dense bf16 rows: row
+ * cu_seqlens[r] + i of k_out and v_out ([num_tokens, Hkv*64] each, 16-byte
+ * aligned, not overlapping) becomes token starts[r] + i of request r's
+ * cache.  Exact for both cache types (a quantised value has 4 significant
+ * bits), but for values below bf16's smallest normal, which round.  Tokens
+ * that fail a device check read as zeros.
+ */
+int k3da_kv_gather(void *k_out, void *v_out, const void *kv_pool, int cache_dtype,
+                   const void *kv_scales, int64_t num_pages, const int32_t *page_table,
+                   int page_stride, const int32_t *starts, const int32_t *cu_seqlens,
+                   int num_requests, int num_tokens, int num_kv_heads, int head_dim,
+                   int32_t *status, void *stream);
+
+/*
+ * Bytes of device workspace a k3da_chunk_attn call with these sizes needs;
+ * 0 when they are out of contract.  Depends on nothing else, so one buffer
+ * serves every replay of a captured graph.
+ */
+size_t k3da_chunk_workspace_bytes(int num_tokens, int num_requests, int num_q_heads,
+                                  int num_kv_heads, int page_stride);
+
+/*
+ * k3da_chunk_attn -- attention of every new token over its request's cache:
+ *   out[t, h] = sum_c softmax_c(softmax_scale * q[t, h] . K_c) V_c
+ *   lse[t, h] = log sum_c exp(softmax_scale * q[t, h] . K_c)
+ * over the cache tokens c that `mask` shows (the chunk's own K and V were
+ * appended before; with K3DA_MASK_CONTEXT they need not be).  A row that
+ * sees nothing gets out = 0 and lse = -inf.  Chunks of any length from a
+ * single decoded token on, mixed in one call.
+ *
+ *   out          [num_tokens, Hq*64] bf16, written; 16-byte aligned; must
+ *                not overlap q or kv_pool.
+ *   lse          [num_tokens, Hq] fp32, or NULL.
+ *   q            [num_tokens, Hq*64] bf16 rows q_row_stride elements apart
+ *                (>= Hq*64, a multiple of 8, at most 2^31): the q heads of
+ *                qkv rows, or k3da_kv_append_qknorm's q_out.  16-byte aligned.
+ *   workspace    at least k3da_chunk_workspace_bytes(), 256-byte aligned;
+ *                contents on entry are irrelevant.  Calls that may overlap
+ *                on the GPU need one each.
+ *   others       as for k3da_attn; a context length whose chunk does not fit
+ *                the page table row is flagged, and the keys past the row's
+ *                end are not seen.  A page id out of range serves zeros.
+ *
+ * The same call on the same inputs gives the same bits every time.
+ */
+int k3da_chunk_attn(void *out, float *lse, const void *q, int64_t q_row_stride, int num_tokens,
+                    const void *kv_pool, int cache_dtype, const void *kv_scales, int64_t num_pages,
+                    const int32_t *page_table, int page_stride, const int32_t *ctx_lens,
+                    const int32_t *cu_seqlens, int num_requests, int num_q_heads,
+                    int num_kv_heads, int head_dim, int mask, float softmax_scale,
+                    void *workspace, size_t workspace_bytes, int32_t *status, void *stream);
+
 /* Static description of a k3da_error or K3DA_STATUS_* bit set. */
 const char *k3da_error_string(int code);
 

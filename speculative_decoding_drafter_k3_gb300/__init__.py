@@ -26,6 +26,8 @@ import torch
 __all__ = [
     "K3daError", "library_path", "load_library", "workspace_bytes", "k3da_attn",
     "k3da_attn_qknorm", "STATUS_BAD_LENGTH", "STATUS_BAD_PAGE", "STATUS_TIMEOUT",
+    "k3da_kv_append", "k3da_kv_append_qknorm", "k3da_kv_gather", "k3da_chunk_attn",
+    "chunk_workspace_bytes", "alloc_chunk_workspace", "alloc_cache",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -36,10 +38,14 @@ _lib = None
 OK, EINVAL, EUNSUPPORTED, ECUDA, EWORKSPACE = 0, -1, -2, -3, -4
 STATUS_BAD_LENGTH, STATUS_BAD_PAGE, STATUS_TIMEOUT = 1, 2, 4
 POS_I32, POS_I64 = 0, 1
+CACHE_BF16, CACHE_E4M3 = 0, 1
+MASKS = {"causal": 0, "full": 1, "context": 2}
+MAX_CHUNK_REQUESTS = 1024
 EXPORTED = ["k3da_workspace_bytes", "k3da_attn", "k3da_attn_qknorm", "k3da_attn_qknorm_noalloc",
             "k3da_noalloc_scratch_bytes", "k3da_split_grid", "k3da_set_phase_event",
             "k3da_error_string", "k3da_version", "k3da_qk_norm_rope", "k3da_attn_qknorm_yarn",
-            "k3da_qk_norm_rope_yarn", "k3da_selftest_wait_timeout"]
+            "k3da_qk_norm_rope_yarn", "k3da_selftest_wait_timeout", "k3da_kv_append",
+            "k3da_kv_append_qknorm", "k3da_kv_gather", "k3da_chunk_workspace_bytes", "k3da_chunk_attn"]
 
 
 class Yarn(ctypes.Structure):
@@ -107,6 +113,19 @@ def load_library():
         lib.k3da_qk_norm_rope_yarn.restype = c_int
         lib.k3da_selftest_wait_timeout.argtypes = [vp, ctypes.c_ulonglong, vp]
         lib.k3da_selftest_wait_timeout.restype = c_int
+        cache = [vp, c_int, vp, c_i64, vp, c_int, vp, vp, c_int]
+        lib.k3da_kv_append.argtypes = cache + [vp, c_int, c_int, c_int, c_int, vp, vp]
+        lib.k3da_kv_append.restype = c_int
+        lib.k3da_kv_append_qknorm.argtypes = cache + [vp, c_int, c_int, c_int, c_int, vp, c_int, vp, vp, c_f, c_f,
+                                                      yp, vp, vp, vp]
+        lib.k3da_kv_append_qknorm.restype = c_int
+        lib.k3da_kv_gather.argtypes = [vp, vp] + cache + [c_int, c_int, c_int, vp, vp]
+        lib.k3da_kv_gather.restype = c_int
+        lib.k3da_chunk_workspace_bytes.argtypes = [c_int, c_int, c_int, c_int, c_int]
+        lib.k3da_chunk_workspace_bytes.restype = c_sz
+        lib.k3da_chunk_attn.argtypes = [vp, vp, vp, c_i64, c_int] + cache + [c_int, c_int, c_int, c_int, c_f, vp, c_sz,
+                                                                             vp, vp]
+        lib.k3da_chunk_attn.restype = c_int
         _lib = lib
         return lib
 
@@ -321,4 +340,177 @@ def k3da_attn_qknorm_noalloc(out, qkv, kv_pool, page_table, ctx_lens, positions,
                                       _ptr(k_norm_w), float(eps), float(rope_base), _ptr(status),
                                       _stream(stream))
     _check(rc, "k3da_attn_qknorm_noalloc")
+    return out
+
+
+# ---- the paged cache: append, gather, chunk attention ----------------------
+
+def alloc_cache(num_pages: int, num_kv_heads: int, *, quantised: bool = False, device=None):
+    """(kv_pool, kv_scales): a zeroed paged cache, bf16 (kv_scales None) or
+    e4m3 codes with e8m0 scales."""
+    device = torch.device("cuda") if device is None else torch.device(device)
+    shape = (num_pages, 2, num_kv_heads, 64)
+    if not quantised:
+        return torch.zeros(*shape, 64, dtype=torch.bfloat16, device=device), None
+    pool = torch.zeros(*shape, 64, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+    return pool, torch.zeros(*shape, dtype=torch.uint8, device=device).view(torch.float8_e8m0fnu)
+
+
+def _on(device, **tensors):
+    """Every tensor is contiguous and on the cache's device."""
+    for name, t in tensors.items():
+        if t is not None and (t.device != device or not t.is_contiguous()):
+            raise K3daError(f"{name} must be contiguous and on the cache's device ({device})")
+
+
+def _cache_args(kv_pool, kv_scales, page_table, lens, cu_seqlens, num_kv_heads, status):
+    """Checks a cache call's common tensors; returns the C arguments from
+    kv_pool to num_requests."""
+    if kv_pool.device.type != "cuda":
+        raise K3daError("kv_pool must be a CUDA tensor")
+    _on(kv_pool.device, kv_pool=kv_pool, kv_scales=kv_scales, page_table=page_table, lengths=lens,
+        cu_seqlens=cu_seqlens, status=status)
+    if kv_pool.dim() != 5 or tuple(kv_pool.shape[1:4]) != (2, num_kv_heads, 64):
+        raise K3daError("kv_pool must be [pages, 2, Hkv, 64, 64]")
+    if kv_pool.dtype == torch.bfloat16:
+        code = CACHE_BF16
+        if kv_scales is not None:
+            raise K3daError("a bf16 cache has no scales")
+    elif kv_pool.dtype == torch.float8_e4m3fn:
+        code = CACHE_E4M3
+        if kv_scales is None or kv_scales.dtype != torch.float8_e8m0fnu or kv_scales.shape != kv_pool.shape[:-1]:
+            raise K3daError("an e4m3 cache needs kv_scales [pages, 2, Hkv, 64] float8_e8m0fnu")
+    else:
+        raise K3daError("kv_pool must be bfloat16 or float8_e4m3fn")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2:
+        raise K3daError("page_table must be [R, S] int32")
+    R, S = page_table.shape
+    if lens.dtype != torch.int32 or lens.numel() != R or cu_seqlens.dtype != torch.int32 or cu_seqlens.numel() != R + 1:
+        raise K3daError("lengths must be [R] and cu_seqlens [R + 1], both int32")
+    if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
+        raise K3daError("status must be an int32 CUDA tensor")
+    return [_ptr(kv_pool), code, _ptr(kv_scales), kv_pool.shape[0], _ptr(page_table), S, _ptr(lens),
+            _ptr(cu_seqlens), R]
+
+
+def _device_stream(device, stream):
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise K3daError("stream must be one of the cache's device")
+    return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _qkv_rows(qkv, num_q_heads, num_kv_heads, D):
+    if qkv.dtype != torch.bfloat16 or qkv.dim() != 2 or qkv.shape[1] != (num_q_heads + 2 * num_kv_heads) * D:
+        raise K3daError("qkv must be [T, (Hq+2Hkv)*64] bf16")
+    return qkv.shape[0]
+
+
+def k3da_kv_append(kv_pool, qkv, page_table, ctx_lens, cu_seqlens, *, num_q_heads: int, num_kv_heads: int,
+                   kv_scales=None, status=None, stream=None):
+    """Write the k and v heads of the packed rows ``qkv`` (k already
+    normalised and roped) into the paged cache at tokens ``ctx_lens[r] + i``
+    (C: k3da_kv_append).  Returns ``kv_pool``."""
+    args = _cache_args(kv_pool, kv_scales, page_table, ctx_lens, cu_seqlens, num_kv_heads, status)
+    D = kv_pool.shape[-1]
+    T = _qkv_rows(qkv, num_q_heads, num_kv_heads, D)
+    _on(kv_pool.device, qkv=qkv)
+    with torch.cuda.device(kv_pool.device):
+        rc = load_library().k3da_kv_append(*args, _ptr(qkv), T, num_q_heads, num_kv_heads, D, _ptr(status),
+                                           _device_stream(kv_pool.device, stream))
+    _check(rc, "k3da_kv_append")
+    return kv_pool
+
+
+def k3da_kv_append_qknorm(kv_pool, qkv, page_table, ctx_lens, cu_seqlens, positions, q_norm_w, k_norm_w, *,
+                          num_q_heads: int, num_kv_heads: int, q_out=None, eps: float = 1e-5,
+                          rope_base: float = 10000.0, yarn=None, kv_scales=None, status=None, stream=None):
+    """``k3da_kv_append`` of raw k: RMSNorm + NeoX RoPE (with ``yarn``, YaRN
+    RoPE) on the way into the cache, and of q into ``q_out`` [T, Hq*64] when
+    given (C: k3da_kv_append_qknorm).  Returns ``kv_pool``."""
+    args = _cache_args(kv_pool, kv_scales, page_table, ctx_lens, cu_seqlens, num_kv_heads, status)
+    D = kv_pool.shape[-1]
+    T = _qkv_rows(qkv, num_q_heads, num_kv_heads, D)
+    _on(kv_pool.device, qkv=qkv, positions=positions, q_norm_w=q_norm_w, k_norm_w=k_norm_w, q_out=q_out)
+    if positions.dtype not in (torch.int32, torch.int64) or positions.numel() != T:
+        raise K3daError("positions must be [T] int32 or int64")
+    if q_norm_w.dtype != torch.bfloat16 or k_norm_w.dtype != torch.bfloat16 or \
+            q_norm_w.numel() != D or k_norm_w.numel() != D:
+        raise K3daError("norm weights must be [64] bf16")
+    if q_out is not None and (q_out.dtype != torch.bfloat16 or tuple(q_out.shape) != (T, num_q_heads * D)):
+        raise K3daError("q_out must be [T, Hq*64] bf16")
+    with torch.cuda.device(kv_pool.device):
+        rc = load_library().k3da_kv_append_qknorm(
+            *args, _ptr(qkv), T, num_q_heads, num_kv_heads, D, _ptr(positions),
+            POS_I64 if positions.dtype == torch.int64 else POS_I32, _ptr(q_norm_w), _ptr(k_norm_w), float(eps),
+            float(rope_base), None if yarn is None else ctypes.byref(yarn), _ptr(q_out), _ptr(status),
+            _device_stream(kv_pool.device, stream))
+    _check(rc, "k3da_kv_append_qknorm")
+    return kv_pool
+
+
+def k3da_kv_gather(k_out, v_out, kv_pool, page_table, starts, cu_seqlens, *, num_kv_heads: int, kv_scales=None,
+                   status=None, stream=None):
+    """Read cache tokens ``starts[r] + i`` back into the packed rows of
+    ``k_out`` and ``v_out`` [T, Hkv*64] bf16 (C: k3da_kv_gather).  Returns
+    both."""
+    args = _cache_args(kv_pool, kv_scales, page_table, starts, cu_seqlens, num_kv_heads, status)
+    D = kv_pool.shape[-1]
+    _on(kv_pool.device, k_out=k_out, v_out=v_out)
+    T = k_out.shape[0]
+    for t in (k_out, v_out):
+        if t.dtype != torch.bfloat16 or tuple(t.shape) != (T, num_kv_heads * D):
+            raise K3daError("k_out and v_out must be [T, Hkv*64] bf16")
+    with torch.cuda.device(kv_pool.device):
+        rc = load_library().k3da_kv_gather(_ptr(k_out), _ptr(v_out), *args, T, num_kv_heads, D, _ptr(status),
+                                           _device_stream(kv_pool.device, stream))
+    _check(rc, "k3da_kv_gather")
+    return k_out, v_out
+
+
+def chunk_workspace_bytes(num_tokens: int, num_requests: int, num_q_heads: int, num_kv_heads: int,
+                          page_stride: int) -> int:
+    n = load_library().k3da_chunk_workspace_bytes(num_tokens, num_requests, num_q_heads, num_kv_heads, page_stride)
+    if n == 0:
+        raise K3daError("chunk_workspace_bytes: sizes out of contract")
+    return int(n)
+
+
+def alloc_chunk_workspace(num_tokens: int, num_requests: int, num_q_heads: int, num_kv_heads: int,
+                          page_stride: int, device=None) -> torch.Tensor:
+    """A workspace tensor for ``k3da_chunk_attn`` calls of these sizes."""
+    device = torch.device("cuda") if device is None else torch.device(device)
+    n = chunk_workspace_bytes(num_tokens, num_requests, num_q_heads, num_kv_heads, page_stride)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def k3da_chunk_attn(out, q, kv_pool, page_table, ctx_lens, cu_seqlens, *, num_q_heads: int, num_kv_heads: int,
+                    softmax_scale: float = 0.125, mask: str = "causal", kv_scales=None, lse=None, workspace,
+                    status=None, stream=None):
+    """Attention of ragged chunks of new tokens over the paged cache (C:
+    k3da_chunk_attn).  ``q`` [T, Hq*64] bf16 may be a view whose rows are
+    further apart (``qkv[:, :Hq*64]``); ``mask`` is "causal", "full" or
+    "context"; ``lse`` [T, Hq] fp32 is optional.  Returns ``out``."""
+    args = _cache_args(kv_pool, kv_scales, page_table, ctx_lens, cu_seqlens, num_kv_heads, status)
+    D = kv_pool.shape[-1]
+    device = kv_pool.device
+    if q.dtype != torch.bfloat16 or q.dim() != 2 or q.shape[1] != num_q_heads * D or q.device != device or \
+            (q.shape[0] and q.stride(1) != 1):
+        raise K3daError("q must be [T, Hq*64] bf16 on the cache's device, each row contiguous")
+    T = q.shape[0]
+    _on(device, out=out, lse=lse, workspace=workspace)
+    if out.dtype != torch.bfloat16 or tuple(out.shape) != (T, num_q_heads * D):
+        raise K3daError("out must be [T, Hq*64] bf16")
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (T, num_q_heads)):
+        raise K3daError("lse must be [T, Hq] fp32")
+    if mask not in MASKS:
+        raise K3daError(f"mask must be one of {', '.join(MASKS)}")
+    row_stride = q.stride(0) if T > 1 else num_q_heads * D
+    with torch.cuda.device(device):
+        rc = load_library().k3da_chunk_attn(
+            _ptr(out), _ptr(lse), _ptr(q), row_stride, T, *args, num_q_heads, num_kv_heads, D, MASKS[mask],
+            float(softmax_scale), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
+            _device_stream(device, stream))
+    _check(rc, "k3da_chunk_attn")
     return out

@@ -12,8 +12,10 @@ import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SOURCES = [os.path.join(PKG, "csrc", "k3da.cu"), os.path.join(PKG, "csrc", "k3da_norm_rope.cu")]
-HEADERS = [os.path.join(ROOT, "include", "k3da.h"), os.path.join(PKG, "csrc", "rope_table.h")]
+SOURCES = [os.path.join(PKG, "csrc", f) for f in
+           ("k3da.cu", "k3da_norm_rope.cu", "k3da_cache.cu", "k3da_chunk.cu")]
+HEADERS = [os.path.join(ROOT, "include", "k3da.h"), os.path.join(PKG, "csrc", "rope_table.h"),
+           os.path.join(PKG, "csrc", "cache_common.cuh")]
 LIB = os.path.join(PKG, "libk3da.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -36,7 +38,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if not force and up_to_date():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
+    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "--threads", "0", "-Xcompiler", "-fPIC",
            "-shared", "-I", os.path.join(ROOT, "include"), "-o", tmp, *SOURCES,
            "-cudart", "static", *extra]
     if verbose:

@@ -1,0 +1,496 @@
+// k3da_cache.cu -- writing a chunk's K and V into the paged cache and reading
+// cached tokens back (sm_103a): k3da_kv_append, k3da_kv_append_qknorm and
+// k3da_kv_gather.
+//
+// The cache is the pool the attention calls read ([page][K=0,V=1][kv head]
+// [slot][64]), in bf16 or quantised.  A quantised row (one token's K or V of
+// one head) is 64 e4m3 codes and one e8m0 byte b: the values are
+// code * 2^(b - 127), with 2^(b - 127) the smallest power of two that brings
+// the row's largest magnitude to at most 448 (e4m3's largest).  A power of
+// two costs a floating-point code nothing but range, makes the scaling and
+// the reading back exact (every value is a bf16), and lets each row be
+// written as soon as its token is known: no statistics over other tokens.
+// A row that holds an infinity or a NaN gets b = 255 (e8m0's NaN): it reads
+// back as NaN, and no other row is touched.
+//
+// Rounding: bf16 inputs are widened exactly, norm and RoPE run in fp32, and
+// each value is rounded once, to bf16 or (from fp32) to its e4m3 code.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "cache_common.cuh"
+#include "k3da.h"
+#include "rope_table.h"
+
+namespace {
+
+using namespace k3da_cache;
+
+// -------------------------------------------------------------- quantising --
+
+// e8m0 byte of a row whose largest magnitude has these fp32 bits: 448 is
+// 1.75 * 2^8, so the exponent field less 8, one more above 1.75; 255 for a
+// row that is not finite.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
+    if (top >= 0x7f800000u) return 255u;
+    const int b = static_cast<int>(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return b < 0 ? 0u : static_cast<uint32_t>(b);
+}
+
+// Two values, scaled, as e4m3 codes (round to nearest even), the first in
+// the low byte.
+__device__ __forceinline__ uint32_t codes2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint4 codes16(const float (&x)[16], float mul) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        w[k] = codes2(x[4 * k] * mul, x[4 * k + 1] * mul) | codes2(x[4 * k + 2] * mul, x[4 * k + 3] * mul) << 16;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// 2^(b - 127), 2^-127 (a subnormal) included; NaN for 255.
+__device__ __forceinline__ float scale_of(uint32_t b) {
+    return b == 255u ? __uint_as_float(0x7fffffffu) : b == 0u ? 0x1p-127f : __uint_as_float(b << 23);
+}
+
+// Four codes as two pairs of bf16 (exact: code * 2^e has 4 significant bits).
+__device__ __forceinline__ uint2 values4(uint32_t c, float mul) {
+    uint32_t a, b;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(a), "=r"(b)
+        : "r"(c));
+    float f[4];
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+        : "=f"(f[0]), "=f"(f[1])
+        : "r"(a));
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+        : "=f"(f[2]), "=f"(f[3])
+        : "r"(b));
+    return make_uint2(pack2(f[0] * mul, f[1] * mul), pack2(f[2] * mul, f[3] * mul));
+}
+
+// ------------------------------------------------------------------ append --
+//
+// Two threads per head row, as in the norm+RoPE cell (and with its
+// arithmetic, operation for operation, so appending to a bf16 cache gives
+// the bits of that call followed by a plain append): thread hp of a row
+// holds the pairs (j, j + 32), 16 hp <= j < 16 hp + 16, read with 16-byte
+// loads that are issued before anything they do not depend on: the search
+// for the row's request, its page, the angles.  A CTA takes 128 rows' worth
+// of whole tokens.  Bound by memory: each row is read and written once.
+constexpr int kAppendThreads = 256;
+constexpr int kAppendRows = kAppendThreads / 2;
+constexpr int kAppendTokens = 64;  // most tokens of a CTA
+
+struct AppendParams {
+    const __nv_bfloat16 *qkv;
+    uint8_t *pool;
+    uint8_t *scales;
+    __nv_bfloat16 *q_out;
+    const int32_t *page_table;
+    const int32_t *ctx_lens;
+    const int32_t *cu_seqlens;
+    const void *positions;
+    const __nv_bfloat16 *q_w;
+    const __nv_bfloat16 *k_w;
+    int32_t *status;
+    long long num_pages;
+    int page_stride, R, T, Hq, Hkv;
+    int rows;            // head rows handled per token: (q,) k and v heads
+    int tokens_per_cta;
+    int pos_i64;
+    float eps;
+    float mscale;
+    unsigned long long turn_rate[kD / 2];
+};
+
+template <bool NORM, bool QUANT>
+__global__ void __launch_bounds__(kAppendThreads) k3da_kv_append_kernel(const __grid_constant__ AppendParams p) {
+    __shared__ float2 trig[NORM ? kAppendTokens * (kD / 2) : 1];
+    __shared__ float wsm[NORM ? 2 * kD : 1];
+    __shared__ int32_t cu[kMaxRequests + 1];
+    __shared__ long long slot[kAppendTokens];  // page * 64 + slot of the token, or -1: nothing is written
+    __shared__ bool real[kAppendTokens];       // the token is some request's
+    const int tid = threadIdx.x;
+    const int t0 = blockIdx.x * p.tokens_per_cta;
+    const int ntok = min(p.T - t0, p.tokens_per_cta);
+    const int heads = p.Hq + 2 * p.Hkv;
+    const int skip = heads - p.rows;  // head rows of a token that are left alone (q heads nobody asks for)
+    const int hp = tid & 1;
+
+    uint4 a0, a1, b0, b1;
+    auto load = [&](int rl) {
+        a0 = a1 = b0 = b1 = make_uint4(0, 0, 0, 0);
+        if (rl >= ntok * p.rows) return;
+        const int tl = rl / p.rows, h = skip + rl - tl * p.rows;
+        const uint4 *x = reinterpret_cast<const uint4 *>(p.qkv + (static_cast<long long>(t0 + tl) * heads + h) * kD);
+        a0 = __ldg(x + 2 * hp);
+        a1 = __ldg(x + 2 * hp + 1);
+        b0 = __ldg(x + 4 + 2 * hp);
+        b1 = __ldg(x + 4 + 2 * hp + 1);
+    };
+    load(tid >> 1);
+    if (NORM) {
+        unsigned long long rate = 0;  // read with constant indices: a lane-dependent one would serialise the warp
+#pragma unroll
+        for (int j = 0; j < kD / 2; ++j)
+            if ((tid & 31) == j) rate = p.turn_rate[j];
+        for (int e = tid; e < ntok * (kD / 2); e += kAppendThreads) {
+            const int t = t0 + (e >> 5);
+            const long long pos = p.pos_i64 ? reinterpret_cast<const long long *>(p.positions)[t]
+                                            : reinterpret_cast<const int *>(p.positions)[t];
+            const unsigned long long turns = static_cast<unsigned long long>(pos) * rate;
+            const float half_turns = static_cast<float>(static_cast<int>(turns >> 32)) * 0x1p-31f;
+            float sn, cs;
+            sincospif(half_turns, &sn, &cs);
+            trig[e] = make_float2(__fmul_rn(cs, p.mscale), __fmul_rn(sn, p.mscale));
+        }
+        if (tid < 2 * kD) wsm[tid] = __bfloat162float(tid < kD ? p.q_w[tid] : p.k_w[tid - kD]);
+    }
+    for (int e = tid; e <= p.R; e += kAppendThreads) cu[e] = __ldg(p.cu_seqlens + e);
+    __syncthreads();
+    if (tid < ntok) {
+        const int t = t0 + tid;
+        const int r = request_of(cu, p.R, t);
+        long long at = -1;
+        const bool mine = t >= cu[r] && t < cu[r + 1];
+        if (mine) {
+            const long long c = static_cast<long long>(__ldg(p.ctx_lens + r)) + (t - cu[r]);
+            if (c < t - cu[r] || c >= static_cast<long long>(p.page_stride) * kP) {
+                if (p.status) atomicOr(p.status, K3DA_STATUS_BAD_LENGTH);
+            } else {
+                const long long page = page_of(p.page_table, p.page_stride, p.num_pages, r, static_cast<int>(c));
+                if (page >= 0) at = page * kP + c % kP;
+                else if (p.status) atomicOr(p.status, K3DA_STATUS_BAD_PAGE);
+            }
+        }
+        slot[tid] = at;
+        real[tid] = mine;
+    }
+    __syncthreads();
+
+    for (int base = 0; base < ntok * p.rows; base += kAppendRows) {
+        const int rl = base + (tid >> 1);
+        if (base > 0) load(rl);
+        const bool valid = rl < ntok * p.rows;
+        const int tl = valid ? rl / p.rows : 0;
+        const int h = valid ? skip + rl - tl * p.rows : heads - 1;
+        float lo[16], hi[16];
+        {
+            const uint32_t av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+            const uint32_t bv[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                lo[2 * e] = bf16_lo(av[e]);
+                lo[2 * e + 1] = bf16_hi(av[e]);
+                hi[2 * e] = bf16_lo(bv[e]);
+                hi[2 * e + 1] = bf16_hi(bv[e]);
+            }
+        }
+        if (NORM) {
+            float ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) ss = __fmaf_rn(lo[e], lo[e], __fmaf_rn(hi[e], hi[e], ss));
+            ss = __fadd_rn(ss, __shfl_xor_sync(kFull, ss, 1));
+            if (h < p.Hq + p.Hkv) {
+                const float inv = rsqrtf(__fmaf_rn(ss, 1.0f / kD, p.eps));
+                const float *w = wsm + (h < p.Hq ? 0 : kD);
+                const float2 *tr = trig + tl * (kD / 2);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int jp = 16 * hp + e;
+                    const float n_lo = __fmul_rn(__fmul_rn(lo[e], inv), w[jp]);
+                    const float n_hi = __fmul_rn(__fmul_rn(hi[e], inv), w[jp + 32]);
+                    const float2 cs = tr[jp];
+                    lo[e] = __fmaf_rn(n_lo, cs.x, -__fmul_rn(n_hi, cs.y));
+                    hi[e] = __fmaf_rn(n_hi, cs.x, __fmul_rn(n_lo, cs.y));
+                }
+            }
+        }
+        uint32_t top = 0;  // the row's largest magnitude, as fp32 bits (a NaN's are above all)
+        if (QUANT) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                top = max(top, max(__float_as_uint(lo[e]) & 0x7fffffffu, __float_as_uint(hi[e]) & 0x7fffffffu));
+            top = max(top, __shfl_xor_sync(kFull, top, 1));
+        }
+        if (!valid) continue;
+        uint4 *dst = nullptr;
+        if (h < p.Hq) {
+            if (real[tl]) dst = reinterpret_cast<uint4 *>(p.q_out + (static_cast<long long>(t0 + tl) * p.Hq + h) * kD);
+        } else if (slot[tl] >= 0) {
+            const int kv = h >= p.Hq + p.Hkv;
+            const int head = h - p.Hq - kv * p.Hkv;
+            const long long row = ((slot[tl] / kP * 2 + kv) * p.Hkv + head) * kP + slot[tl] % kP;
+            if (QUANT) {
+                const uint32_t b = scale_byte(top);
+                const float mul = b == 255u ? 0.f : __uint_as_float((254u - b) << 23);  // 2^(127 - b)
+                uint4 *codes = reinterpret_cast<uint4 *>(p.pool + row * kD);
+                const uint4 zero = make_uint4(0, 0, 0, 0);
+                codes[hp] = b == 255u ? zero : codes16(lo, mul);
+                codes[2 + hp] = b == 255u ? zero : codes16(hi, mul);
+                if (hp == 0) p.scales[row] = static_cast<uint8_t>(b);
+            } else {
+                dst = reinterpret_cast<uint4 *>(p.pool + row * (kD * 2));
+            }
+        }
+        if (dst != nullptr) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                dst[2 * hp + c] = make_uint4(pack2(lo[8 * c], lo[8 * c + 1]), pack2(lo[8 * c + 2], lo[8 * c + 3]),
+                                             pack2(lo[8 * c + 4], lo[8 * c + 5]), pack2(lo[8 * c + 6], lo[8 * c + 7]));
+                dst[4 + 2 * hp + c] =
+                    make_uint4(pack2(hi[8 * c], hi[8 * c + 1]), pack2(hi[8 * c + 2], hi[8 * c + 3]),
+                               pack2(hi[8 * c + 4], hi[8 * c + 5]), pack2(hi[8 * c + 6], hi[8 * c + 7]));
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ gather --
+//
+// Four threads per (token, K or V, head) row, 16 dims each: 32 bytes (bf16)
+// or 16 codes and the row's scale in, 32 bytes out.  A thread issues the
+// loads of all its rows before it stores any.  Bound by memory.
+constexpr int kGatherThreads = 256;
+constexpr int kGatherTokens = 64;  // most tokens of a CTA
+constexpr int kGatherItems = 4;    // row quarters of a thread in flight
+
+struct GatherParams {
+    __nv_bfloat16 *k_out;
+    __nv_bfloat16 *v_out;
+    const uint8_t *pool;
+    const uint8_t *scales;
+    const int32_t *page_table;
+    const int32_t *starts;
+    const int32_t *cu_seqlens;
+    int32_t *status;
+    long long num_pages;
+    int page_stride, R, T, Hkv;
+    int tokens_per_cta;
+};
+
+template <bool QUANT>
+__global__ void __launch_bounds__(kGatherThreads) k3da_kv_gather_kernel(const __grid_constant__ GatherParams p) {
+    __shared__ int32_t cu[kMaxRequests + 1];
+    __shared__ long long slot[kGatherTokens];  // page * 64 + slot, -1: zeros, -2: the row is left alone
+    const int tid = threadIdx.x;
+    const int t0 = blockIdx.x * p.tokens_per_cta;
+    const int ntok = min(p.T - t0, p.tokens_per_cta);
+    for (int e = tid; e <= p.R; e += kGatherThreads) cu[e] = __ldg(p.cu_seqlens + e);
+    __syncthreads();
+    if (tid < ntok) {
+        const int t = t0 + tid;
+        const int r = request_of(cu, p.R, t);
+        long long at = -2;
+        if (t >= cu[r] && t < cu[r + 1]) {
+            at = -1;
+            const long long c = static_cast<long long>(__ldg(p.starts + r)) + (t - cu[r]);
+            if (c < t - cu[r] || c >= static_cast<long long>(p.page_stride) * kP) {
+                if (p.status) atomicOr(p.status, K3DA_STATUS_BAD_LENGTH);
+            } else {
+                const long long page = page_of(p.page_table, p.page_stride, p.num_pages, r, static_cast<int>(c));
+                if (page >= 0) at = page * kP + c % kP;
+                else if (p.status) atomicOr(p.status, K3DA_STATUS_BAD_PAGE);
+            }
+        }
+        slot[tid] = at;
+    }
+    __syncthreads();
+    const int per_token = p.Hkv * 8;  // row quarters of a token
+    const int items = ntok * per_token;
+    for (int base = 0; base < items; base += kGatherThreads * kGatherItems) {
+        uint4 x[kGatherItems], y[kGatherItems];
+        uint32_t sc[kGatherItems];
+#pragma unroll
+        for (int k = 0; k < kGatherItems; ++k) {
+            const int e = base + k * kGatherThreads + tid;
+            x[k] = y[k] = make_uint4(0, 0, 0, 0);
+            sc[k] = 127u;
+            if (e >= items) continue;
+            const int tl = e / per_token, rest = e - tl * per_token;
+            const int kv = rest >= p.Hkv * 4, head = (rest >> 2) - kv * p.Hkv, quarter = rest & 3;
+            if (slot[tl] < 0) continue;
+            const long long row = ((slot[tl] / kP * 2 + kv) * p.Hkv + head) * kP + slot[tl] % kP;
+            if (QUANT) {
+                x[k] = __ldg(reinterpret_cast<const uint4 *>(p.pool + row * kD) + quarter);
+                sc[k] = __ldg(p.scales + row);
+            } else {
+                const uint4 *src = reinterpret_cast<const uint4 *>(p.pool + row * (kD * 2)) + 2 * quarter;
+                x[k] = __ldg(src);
+                y[k] = __ldg(src + 1);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kGatherItems; ++k) {
+            const int e = base + k * kGatherThreads + tid;
+            if (e >= items) continue;
+            const int tl = e / per_token, rest = e - tl * per_token;
+            const int kv = rest >= p.Hkv * 4, head = (rest >> 2) - kv * p.Hkv, quarter = rest & 3;
+            if (slot[tl] == -2) continue;
+            if (QUANT) {
+                const float mul = scale_of(sc[k]);
+                const uint2 v0 = values4(x[k].x, mul), v1 = values4(x[k].y, mul), v2 = values4(x[k].z, mul),
+                            v3 = values4(x[k].w, mul);
+                x[k] = make_uint4(v0.x, v0.y, v1.x, v1.y);
+                y[k] = make_uint4(v2.x, v2.y, v3.x, v3.y);
+            }
+            uint4 *dst = reinterpret_cast<uint4 *>((kv ? p.v_out : p.k_out) +
+                                                   (static_cast<long long>(t0 + tl) * p.Hkv + head) * kD) +
+                         2 * quarter;
+            dst[0] = x[k];
+            dst[1] = y[k];
+        }
+    }
+}
+
+// -------------------------------------------------------------------- host --
+
+int launch_append(void *kv_pool, int cache_dtype, void *kv_scales, int64_t num_pages, const int32_t *page_table,
+                  int page_stride, const int32_t *ctx_lens, const int32_t *cu_seqlens, int R, const void *qkv,
+                  int T, int Hq, int Hkv, int head_dim, bool norm, const void *positions, int pos_dtype,
+                  const void *q_norm_w, const void *k_norm_w, float eps, float rope_base, const k3da_yarn *yarn,
+                  void *q_out, int32_t *status, void *stream) {
+    const int rc = check_cache(kv_pool, cache_dtype, kv_scales, num_pages, page_table, page_stride, ctx_lens,
+                               cu_seqlens, R, T, Hkv, head_dim, status);
+    if (rc != K3DA_OK) return rc;
+    if (!heads_ok(Hq, Hkv)) return K3DA_EUNSUPPORTED;
+    if (T > 0 && !qkv) return K3DA_EINVAL;
+    if (!aligned_to(qkv, 16)) return K3DA_EINVAL;
+    if (norm) {
+        if ((T > 0 && !positions) || !q_norm_w || !k_norm_w) return K3DA_EINVAL;
+        if (pos_dtype != K3DA_POS_I32 && pos_dtype != K3DA_POS_I64) return K3DA_EINVAL;
+        if (!aligned_to(positions, pos_dtype == K3DA_POS_I64 ? 8 : 4) || !aligned_to(q_norm_w, 2) ||
+            !aligned_to(k_norm_w, 2) || !aligned_to(q_out, 16))
+            return K3DA_EINVAL;
+        if (!(eps >= 0.f) || !std::isfinite(eps) || !(rope_base > 1.f) || !std::isfinite(rope_base)) return K3DA_EINVAL;
+        if (yarn != nullptr && !k3da_host::yarn_valid(yarn)) return K3DA_EINVAL;
+    }
+    if (T == 0) return K3DA_OK;
+    // Nothing that is written may overlap what other threads still read.
+    const size_t in_bytes = static_cast<size_t>(T) * (Hq + 2 * Hkv) * kD * 2;
+    const size_t q_bytes = static_cast<size_t>(T) * Hq * kD * 2;
+    const size_t cache_bytes = pool_bytes(num_pages, Hkv, cache_dtype);
+    if (overlap(qkv, in_bytes, kv_pool, cache_bytes)) return K3DA_EINVAL;
+    if (q_out && (overlap(qkv, in_bytes, q_out, q_bytes) || overlap(kv_pool, cache_bytes, q_out, q_bytes)))
+        return K3DA_EINVAL;
+
+    AppendParams prm;
+    std::memset(&prm, 0, sizeof prm);
+    prm.qkv = static_cast<const __nv_bfloat16 *>(qkv);
+    prm.pool = static_cast<uint8_t *>(kv_pool);
+    prm.scales = static_cast<uint8_t *>(kv_scales);
+    prm.q_out = static_cast<__nv_bfloat16 *>(q_out);
+    prm.page_table = page_table;
+    prm.ctx_lens = ctx_lens;
+    prm.cu_seqlens = cu_seqlens;
+    prm.positions = positions;
+    prm.q_w = static_cast<const __nv_bfloat16 *>(q_norm_w);
+    prm.k_w = static_cast<const __nv_bfloat16 *>(k_norm_w);
+    prm.status = status;
+    prm.num_pages = num_pages;
+    prm.page_stride = page_stride;
+    prm.R = R;
+    prm.T = T;
+    prm.Hq = Hq;
+    prm.Hkv = Hkv;
+    prm.rows = 2 * Hkv + (norm && q_out ? Hq : 0);
+    prm.tokens_per_cta = kAppendRows / prm.rows;
+    if (prm.tokens_per_cta < 1) prm.tokens_per_cta = 1;
+    if (prm.tokens_per_cta > kAppendTokens) prm.tokens_per_cta = kAppendTokens;
+    prm.pos_i64 = pos_dtype == K3DA_POS_I64;
+    prm.eps = eps;
+    prm.mscale = 1.0f;
+    if (norm) {
+        double inv_freq[kD / 2];
+        k3da_host::rope_frequencies(inv_freq, kD / 2, rope_base, yarn);
+        for (int j = 0; j < kD / 2; ++j) prm.turn_rate[j] = k3da_host::turn_rate_fixed64(inv_freq[j]);
+        if (yarn != nullptr) prm.mscale = k3da_host::yarn_mscale(yarn);
+    }
+    const unsigned ctas = static_cast<unsigned>((static_cast<long long>(T) + prm.tokens_per_cta - 1) / prm.tokens_per_cta);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool quant = cache_dtype == K3DA_CACHE_E4M3;
+    if (norm && quant) k3da_kv_append_kernel<true, true><<<ctas, kAppendThreads, 0, st>>>(prm);
+    else if (norm) k3da_kv_append_kernel<true, false><<<ctas, kAppendThreads, 0, st>>>(prm);
+    else if (quant) k3da_kv_append_kernel<false, true><<<ctas, kAppendThreads, 0, st>>>(prm);
+    else k3da_kv_append_kernel<false, false><<<ctas, kAppendThreads, 0, st>>>(prm);
+    return cudaGetLastError() == cudaSuccess ? K3DA_OK : K3DA_ECUDA;
+}
+
+}  // namespace
+
+extern "C" int k3da_kv_append(void *kv_pool, int cache_dtype, void *kv_scales, int64_t num_pages,
+                              const int32_t *page_table, int page_stride, const int32_t *ctx_lens,
+                              const int32_t *cu_seqlens, int num_requests, const void *qkv, int num_tokens,
+                              int num_q_heads, int num_kv_heads, int head_dim, int32_t *status, void *stream) {
+    return launch_append(kv_pool, cache_dtype, kv_scales, num_pages, page_table, page_stride, ctx_lens, cu_seqlens,
+                         num_requests, qkv, num_tokens, num_q_heads, num_kv_heads, head_dim, false, nullptr, 0,
+                         nullptr, nullptr, 0.f, 0.f, nullptr, nullptr, status, stream);
+}
+
+extern "C" int k3da_kv_append_qknorm(void *kv_pool, int cache_dtype, void *kv_scales, int64_t num_pages,
+                                     const int32_t *page_table, int page_stride, const int32_t *ctx_lens,
+                                     const int32_t *cu_seqlens, int num_requests, const void *qkv, int num_tokens,
+                                     int num_q_heads, int num_kv_heads, int head_dim, const void *positions,
+                                     int pos_dtype, const void *q_norm_w, const void *k_norm_w, float eps,
+                                     float rope_base, const k3da_yarn *yarn, void *q_out, int32_t *status,
+                                     void *stream) {
+    return launch_append(kv_pool, cache_dtype, kv_scales, num_pages, page_table, page_stride, ctx_lens, cu_seqlens,
+                         num_requests, qkv, num_tokens, num_q_heads, num_kv_heads, head_dim, true, positions,
+                         pos_dtype, q_norm_w, k_norm_w, eps, rope_base, yarn, q_out, status, stream);
+}
+
+extern "C" int k3da_kv_gather(void *k_out, void *v_out, const void *kv_pool, int cache_dtype, const void *kv_scales,
+                              int64_t num_pages, const int32_t *page_table, int page_stride, const int32_t *starts,
+                              const int32_t *cu_seqlens, int num_requests, int num_tokens, int num_kv_heads,
+                              int head_dim, int32_t *status, void *stream) {
+    const int rc = check_cache(kv_pool, cache_dtype, kv_scales, num_pages, page_table, page_stride, starts,
+                               cu_seqlens, num_requests, num_tokens, num_kv_heads, head_dim, status);
+    if (rc != K3DA_OK) return rc;
+    if (!aligned_to(k_out, 16) || !aligned_to(v_out, 16)) return K3DA_EINVAL;
+    if (num_tokens == 0) return K3DA_OK;
+    if (!k_out || !v_out) return K3DA_EINVAL;
+    const size_t out_bytes = static_cast<size_t>(num_tokens) * num_kv_heads * kD * 2;
+    const size_t cache_bytes = pool_bytes(num_pages, num_kv_heads, cache_dtype);
+    if (overlap(k_out, out_bytes, v_out, out_bytes) || overlap(k_out, out_bytes, kv_pool, cache_bytes) ||
+        overlap(v_out, out_bytes, kv_pool, cache_bytes))
+        return K3DA_EINVAL;
+    GatherParams prm;
+    std::memset(&prm, 0, sizeof prm);
+    prm.k_out = static_cast<__nv_bfloat16 *>(k_out);
+    prm.v_out = static_cast<__nv_bfloat16 *>(v_out);
+    prm.pool = static_cast<const uint8_t *>(kv_pool);
+    prm.scales = static_cast<const uint8_t *>(kv_scales);
+    prm.page_table = page_table;
+    prm.starts = starts;
+    prm.cu_seqlens = cu_seqlens;
+    prm.status = status;
+    prm.num_pages = num_pages;
+    prm.page_stride = page_stride;
+    prm.R = num_requests;
+    prm.T = num_tokens;
+    prm.Hkv = num_kv_heads;
+    // Four row quarters a thread for the long calls; one where that leaves
+    // SMs without work.
+    const long long items = static_cast<long long>(num_tokens) * num_kv_heads * 8;
+    const int per_cta = items >= 304LL * kGatherThreads * kGatherItems ? kGatherThreads * kGatherItems : kGatherThreads;
+    prm.tokens_per_cta = per_cta / (num_kv_heads * 8);
+    if (prm.tokens_per_cta < 1) prm.tokens_per_cta = 1;
+    if (prm.tokens_per_cta > kGatherTokens) prm.tokens_per_cta = kGatherTokens;
+    const unsigned ctas =
+        static_cast<unsigned>((static_cast<long long>(num_tokens) + prm.tokens_per_cta - 1) / prm.tokens_per_cta);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (cache_dtype == K3DA_CACHE_E4M3) k3da_kv_gather_kernel<true><<<ctas, kGatherThreads, 0, st>>>(prm);
+    else k3da_kv_gather_kernel<false><<<ctas, kGatherThreads, 0, st>>>(prm);
+    return cudaGetLastError() == cudaSuccess ? K3DA_OK : K3DA_ECUDA;
+}
