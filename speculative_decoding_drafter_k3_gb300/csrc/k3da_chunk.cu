@@ -1,119 +1,1168 @@
 // k3da_chunk.cu -- attention of ragged chunks of new tokens over the paged
 // cache (sm_103a): k3da_chunk_attn.
 //
-// For row i of request r's chunk and query head h (kv head g = h / (Hq/Hkv)):
+// For row i of request r's chunk and query head h (kv head g = h / G):
 //   o = sum_c softmax_c(scale * q . k_c) v_c,   lse = log sum_c exp(scale * q . k_c)
 // over the cache tokens c the mask shows: c <= ctx_r + i (causal), all
 // ctx_r + n_r (full), or the ctx_r before the chunk (context).  A row that
 // sees nothing gets o = 0 and lse = -inf.
 //
-// One warp per (row, query head): lane l takes the keys l, l + 32, ... with
-// a running maximum, sum and output of its own in fp32; the lanes merge at
-// the end.
+// Work.  An item is a request, a kv head and 2 * tpt consecutive tokens of
+// the chunk, tpt = floor(128 / G): two slots of up to 128 query rows (token
+// major, the G heads of a token together), each one M = 128 accumulator.  An
+// item's keys come in tiles of 128 (two pages).  All items are laid on one
+// line, request by request, head by head, each as long as the keys its last
+// row sees plus a constant, and the line is cut into equal slices, one a
+// CTA: every CTA has the same number of key tiles to within one, whatever
+// the lengths.  An item that a cut falls into leaves partial results, which
+// the combine kernel folds in order.  Each CTA finds its slice by itself: a
+// scan over the requests, then closed forms.
+//
+// Both slots of an item read the same K/V tiles (shared).  An item whose
+// tokens fit one slot (a decode step, a draft block, a chunk's tail) gives
+// its tiles to the two slots in turn (alternate), both with the same rows,
+// and the two halves are merged at the end: the softmax of one tile overlaps
+// the products and loads of the next either way.
+//
+// Roles of a CTA's 16 warps: two softmax warpgroups (a slot each, one thread
+// a row), one warpgroup that prepares tiles (below), a K/V loader, one MMA
+// issuer for each slot, and a Q loader.  S (128 x 128 fp32) and P (bf16) have
+// tensor memory of their own, so that a slot's next Q K^T runs while its
+// softmax works on the last: S is free as soon as it is in registers.
+//
+// The preparing warpgroup zeroes the V rows past an item's last key (stale
+// slots may hold anything, and 0 * NaN is NaN), and where only some of an
+// item's rows see a key, it takes infinities and NaN out of that V row and
+// records the first key that had one for each dim: what a row sees is always
+// a prefix of the keys, so the epilogue puts them back for just the rows that
+// see them.  Quantised tiles it widens to bf16 on the way (the scale is a
+// power of two, so the bf16 are exact); both cache types share all the rest.
+//
+// Rounding: scores, softmax statistics and O are fp32 throughout (partials
+// too); P is rounded to bf16 once for the P V product, the output once.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include <cmath>
 #include <cstring>
+#include <mutex>
 
 #include "cache_common.cuh"
 #include "k3da.h"
+#include "sm103.cuh"
 
 namespace {
 
 using namespace k3da_cache;
+using namespace sm103;
+
+constexpr int kThreads = 512;
+constexpr int kCtas = 152;         // slices of the line at most: one CTA an SM
+constexpr int kTile = 128;         // keys of a tile: two pages
+constexpr int kSlotRows = 128;     // query rows of a slot
+constexpr int kOverhead = 128;     // an item's fixed cost, in keys
+constexpr int kMinSlice = 256;     // shortest slice, in keys
+constexpr int kRecords = 8;        // pieces whose non-finite records are alive at once
+constexpr float kRescale = 8.0f;   // log2 units the running maximum may lag behind
+// Warps.
+constexpr int kPrepWarp = 8, kLoadWarp = 12, kMmaWarp = 13, kQWarp = 15;
+// Registers a thread: 2 x 128 x 192 + 2 x 128 x 64 = 512 x 128.
+constexpr int kSoftmaxRegs = 192, kOtherRegs = 64;
+// Tensor memory columns of slot s.
+__device__ __forceinline__ uint32_t col_s(int s) { return 128u * s; }
+__device__ __forceinline__ uint32_t col_p(int s) { return 256u + 64u * s; }
+__device__ __forceinline__ uint32_t col_o(int s) { return 384u + 64u * s; }
+constexpr uint32_t kTmemCols = 512u;
+constexpr uint32_t kIdescQK = idesc_f16(128, kTile, false);
+constexpr uint32_t kIdescPV = idesc_f16(128, kD, true);
 
 struct ChunkParams {
     __nv_bfloat16 *out;
     float *lse;
-    const __nv_bfloat16 *q;
-    const uint8_t *pool;
     const uint8_t *scales;
     const int32_t *page_table;
     const int32_t *ctx_lens;
     const int32_t *cu_seqlens;
     int32_t *status;
-    long long q_stride;
+    struct Cut *cuts;
+    float2 *part_ml;  // [kCtas][2][256] (m in log2 units, l)
+    float *part_o;    // [kCtas][2][256][64]
     long long num_pages;
     int page_stride, R, T, Hq, Hkv;
+    int G;    // query heads per kv head
+    int tpt;  // tokens of a slot
     int mask;
     float scale_log2;
 };
 
-constexpr int kWarps = 4;
+// What a CTA leaves for the combine kernel.  part 0: the piece it began with
+// belongs to an item begun before; part 1: the item it ended with goes on in
+// later CTAs, up to `last`.
+struct Cut {
+    int has[2];
+    int row;     // first row of the item that goes on
+    int tokens;  // its tokens
+    int head;    // its kv head
+    int last;
+    int pad[2];
+};
+static_assert(sizeof(Cut) == 32, "cuts are 32 bytes");
+constexpr size_t kCutBytes = 8192;
+static_assert(kCtas * sizeof(Cut) <= kCutBytes, "room for the cuts");
+constexpr size_t kPartRows = static_cast<size_t>(kCtas) * 2 * 2 * kSlotRows;
+constexpr size_t kWorkspace = kCutBytes + kPartRows * (sizeof(float2) + kD * sizeof(float));
 
-__device__ __forceinline__ float e4m3_value(uint32_t c) {
-    uint32_t h;
-    asm("{\n\t.reg .b16 l;\n\tcvt.u16.u32 l, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(h) : "r"(c & 0xffu));
-    float f;
-    asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.f32.f16 %0, l;\n\t}" : "=f"(f) : "r"(h));
-    return f;
+// -------------------------------------------------------------- the line --
+
+struct Plan {
+    long long prefix[kMaxRequests + 1];  // where request r's items begin on the line
+    int32_t row[kMaxRequests];           // its first row
+    int32_t n[kMaxRequests];             // its new tokens
+    int32_t ctx[kMaxRequests];           // its cached tokens
+    long long warp_sum[kThreads / 32];
+};
+
+// Length of the first `pairs` items of one head: each sees `base` keys (and,
+// causal, its own tokens and the ones before) and costs kOverhead.
+__device__ __forceinline__ long long line_of(const ChunkParams &p, long long base, long long pairs) {
+    const long long own = p.mask == K3DA_MASK_CAUSAL ? p.tpt * pairs * (pairs + 1) : 0;  // 2 tpt (1 + 2 + ... + pairs)
+    return pairs * (base + kOverhead) + own;
 }
 
-template <bool QUANT>
-__device__ __forceinline__ float cached(const ChunkParams &p, long long row, int d) {
-    if (!QUANT) return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p.pool)[row * kD + d]);
-    const uint32_t b = p.scales[row];
-    const float s = b == 255u ? __uint_as_float(0x7fffffffu) : b == 0u ? 0x1p-127f : __uint_as_float(b << 23);
-    return e4m3_value(p.pool[row * kD + d]) * s;
-}
-
-template <bool QUANT>
-__global__ void __launch_bounds__(32 * kWarps) k3da_chunk_simple_kernel(const __grid_constant__ ChunkParams p) {
-    __shared__ int32_t cu[kMaxRequests + 1];
-    for (int e = threadIdx.x; e <= p.R; e += 32 * kWarps) cu[e] = p.cu_seqlens[e];
-    __syncthreads();
-    const int lane = threadIdx.x & 31;
-    const long long w = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    if (w >= static_cast<long long>(p.T) * p.Hq) return;
-    const int t = static_cast<int>(w / p.Hq), h = static_cast<int>(w % p.Hq);
-    const int r = request_of(cu, p.R, t);
-    if (t < cu[r] || t >= cu[r + 1]) return;
-    const int n = cu[r + 1] - cu[r];
+// All threads; syncs.  Lengths the kernel cannot use are clamped and flagged.
+__device__ void build_plan(const ChunkParams &p, Plan *pl, bool report) {
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int cap = p.page_stride * kP;
-    int ctx = p.ctx_lens[r];
-    if (ctx < 0 || static_cast<long long>(ctx) + n > cap) {
-        if (lane == 0 && p.status) atomicOr(p.status, K3DA_STATUS_BAD_LENGTH);
-        ctx = ctx < 0 ? 0 : ctx > cap ? cap : ctx;
-    }
-    long long limit = p.mask == K3DA_MASK_CAUSAL ? static_cast<long long>(ctx) + (t - cu[r]) + 1
-                      : p.mask == K3DA_MASK_FULL ? static_cast<long long>(ctx) + n
-                                                 : ctx;
-    if (limit > cap) limit = cap;
-    const __nv_bfloat16 *q = p.q + t * p.q_stride + h * kD;
-    const int g = h / (p.Hq / p.Hkv);
-    float m = -INFINITY, l = 0.f, o[kD];
+    static_assert(kMaxRequests == 2 * kThreads, "two requests a thread");
+    long long cost[2] = {0, 0};
 #pragma unroll
-    for (int d = 0; d < kD; ++d) o[d] = 0.f;
-    for (int c = lane; c < limit; c += 32) {
-        const long long page = page_of(p.page_table, p.page_stride, p.num_pages, r, c);
-        if (page < 0 && p.status) atomicOr(p.status, K3DA_STATUS_BAD_PAGE);
-        const long long krow = ((page * 2) * p.Hkv + g) * kP + c % kP, vrow = krow + static_cast<long long>(p.Hkv) * kP;
-        float s = 0.f;
-        if (page >= 0)
-            for (int d = 0; d < kD; ++d) s += __bfloat162float(q[d]) * cached<QUANT>(p, krow, d);
-        s *= p.scale_log2;
-        const float mn = fmaxf(m, s), f = exp2f(m - mn), e = exp2f(s - mn);
-        l = l * f + e;
-#pragma unroll
-        for (int d = 0; d < kD; ++d) o[d] = o[d] * f + (page >= 0 ? e * cached<QUANT>(p, vrow, d) : 0.f);
-        m = mn;
+    for (int k = 0; k < 2; ++k) {
+        const int r = 2 * t + k;
+        if (r >= p.R) continue;
+        const int a = __ldg(p.cu_seqlens + r), b = __ldg(p.cu_seqlens + r + 1), c = __ldg(p.ctx_lens + r);
+        const int begin = min(max(a, 0), p.T), end = min(max(b, begin), p.T), n = end - begin;
+        const int ctx = min(max(c, 0), cap);
+        const bool fits = p.mask == K3DA_MASK_CONTEXT || static_cast<long long>(ctx) + n <= cap;
+        if (report && p.status && (a != begin || b != end || (n > 0 && (c != ctx || !fits))))
+            atomicOr(p.status, K3DA_STATUS_BAD_LENGTH);
+        pl->row[r] = begin;
+        pl->n[r] = n;
+        pl->ctx[r] = ctx;
+        const long long base = static_cast<long long>(ctx) + (p.mask == K3DA_MASK_FULL ? n : 0);
+        cost[k] = p.Hkv * line_of(p, base, (n + 2 * p.tpt - 1) / (2 * p.tpt));
     }
-    float mt = m;
-    for (int x = 16; x > 0; x >>= 1) mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, x));
-    const float f = m == -INFINITY ? 0.f : exp2f(m - mt);
-    l *= f;
-    for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(kFull, l, x);
-    __nv_bfloat16 *dst = p.out + (static_cast<long long>(t) * p.Hq + h) * kD;
+    long long sum = cost[0] + cost[1];
 #pragma unroll
-    for (int d = 0; d < kD; ++d) {
-        float v = f == 0.f ? 0.f : o[d] * f;
-        for (int x = 16; x > 0; x >>= 1) v += __shfl_xor_sync(kFull, v, x);
-        if (lane == (d & 31)) dst[d] = __float2bfloat16_rn(limit > 0 ? v / l : 0.f);
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long up = __shfl_up_sync(kFull, sum, off);
+        if (lane >= off) sum += up;
     }
-    if (lane == 0 && p.lse)
-        p.lse[static_cast<long long>(t) * p.Hq + h] = limit > 0 ? (mt + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    if (lane == 31) pl->warp_sum[warp] = sum;
+    __syncthreads();
+    long long before = 0;
+    for (int w = 0; w < warp; ++w) before += pl->warp_sum[w];
+    const long long begin = before + sum - cost[0] - cost[1];
+    if (2 * t <= p.R) pl->prefix[2 * t] = begin;
+    if (2 * t + 1 <= p.R) pl->prefix[2 * t + 1] = begin + cost[0];
+    if (t == kThreads - 1 && p.R == kMaxRequests) pl->prefix[kMaxRequests] = begin + cost[0] + cost[1];
+    __syncthreads();
+}
+
+// A piece: the tiles [t0, t1) of one item that fall into this CTA's slice.
+struct Piece {
+    long long start, length;  // the item on the line
+    int r, h;
+    int tok0;    // its first token in the chunk
+    int tokens;
+    int ctx, n;  // its request's
+    int row;     // its first row
+    int limit;   // keys its last row sees
+    int nt;      // tiles of the item
+    int t0, t1;
+    bool alt;    // one slot's worth of rows: the slots take the tiles in turn
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == nt; }
+    // Tiles that slot s works on: [from, to) in steps of `step`.
+    __device__ __forceinline__ int from(int s) const { return alt ? t0 + s : t0; }
+    __device__ __forceinline__ int step() const { return alt ? 2 : 1; }
+};
+
+// Keys that the chunk's token i sees.
+__device__ __forceinline__ int keys_seen(const ChunkParams &p, int ctx, int n, int i) {
+    const long long c = p.mask == K3DA_MASK_CAUSAL ? static_cast<long long>(ctx) + i + 1
+                        : p.mask == K3DA_MASK_FULL ? static_cast<long long>(ctx) + n
+                                                   : ctx;
+    const int cap = p.page_stride * kP;
+    return c < cap ? static_cast<int>(c) : cap;
+}
+
+// The CTA's pieces, in order.  Every warp walks them for itself, with the
+// state in shared memory: the softmax's registers are for scores.
+struct Walk {
+    long long lo, hi;         // the slice
+    long long total, slices;
+    long long at;             // where the next item begins
+    int r, h, pair;
+
+    // Start of slice c: ceil(c * total / slices), without a wide product.
+    __device__ __forceinline__ long long slice(long long c) const {
+        const long long q = total / slices, rem = total - q * slices;
+        return c * q + (c * rem + slices - 1) / slices;
+    }
+    __device__ __forceinline__ static long long base(const ChunkParams &p, const Plan *pl, int rr) {
+        return static_cast<long long>(pl->ctx[rr]) + (p.mask == K3DA_MASK_FULL ? pl->n[rr] : 0);
+    }
+    __device__ __forceinline__ static int pairs(const ChunkParams &p, const Plan *pl, int rr) {
+        return (pl->n[rr] + 2 * p.tpt - 1) / (2 * p.tpt);
+    }
+
+    __device__ void begin(const ChunkParams &p, const Plan *pl, int cta) {
+        total = pl->prefix[p.R];
+        slices = total / kMinSlice;
+        slices = slices < 1 ? 1 : slices > kCtas ? kCtas : slices;
+        lo = hi = at = 0;
+        r = h = pair = 0;
+        if (cta >= slices || total == 0) return;
+        lo = slice(cta);
+        hi = slice(cta + 1);
+        int a = 0, b = p.R;
+        while (b - a > 1) {
+            const int mid = (a + b) >> 1;
+            if (pl->prefix[mid] <= lo) a = mid;
+            else b = mid;
+        }
+        r = a;
+        const long long keys = base(p, pl, r);
+        const long long head = line_of(p, keys, pairs(p, pl, r));
+        long long rest = lo - pl->prefix[r];
+        h = static_cast<int>(rest / head);
+        rest -= h * head;
+        int x = 0, y = pairs(p, pl, r);
+        while (y - x > 1) {
+            const int mid = (x + y) >> 1;
+            if (line_of(p, keys, mid) <= rest) x = mid;
+            else y = mid;
+        }
+        pair = x;
+        at = pl->prefix[r] + h * head + line_of(p, keys, pair);
+    }
+
+    // First tile of an item's part from `offset` (in the item) on.
+    __device__ __forceinline__ static int tile_at(long long offset, int nt) {
+        const long long t = (offset - kOverhead + kTile - 1) / kTile;
+        return offset <= kOverhead ? 0 : t < nt ? static_cast<int>(t) : nt;
+    }
+
+    __device__ bool next(const ChunkParams &p, const Plan *pl, Piece &it) {
+        while (at < hi) {
+            it.r = r;
+            it.h = h;
+            it.ctx = pl->ctx[r];
+            it.n = pl->n[r];
+            it.tok0 = pair * 2 * p.tpt;
+            it.tokens = min(2 * p.tpt, it.n - it.tok0);
+            it.row = pl->row[r] + it.tok0;
+            it.alt = it.tokens <= p.tpt;
+            it.limit = keys_seen(p, it.ctx, it.n, it.tok0 + it.tokens - 1);
+            it.nt = static_cast<int>((static_cast<long long>(it.limit) + kTile - 1) / kTile);
+            it.start = at;
+            const int count = pairs(p, pl, r);
+            const long long keys = base(p, pl, r);
+            it.length = line_of(p, keys, pair + 1) - line_of(p, keys, pair);
+            it.t0 = lo <= at ? 0 : tile_at(lo - at, it.nt);
+            it.t1 = hi >= at + it.length ? it.nt : tile_at(hi - at, it.nt);
+            at += it.length;
+            if (++pair == count) {
+                pair = 0;
+                if (++h == p.Hkv) {
+                    h = 0;
+                    do ++r;
+                    while (r < p.R && pl->n[r] == 0);
+                }
+            }
+            if (it.t0 < it.t1 || (it.nt == 0 && it.start >= lo)) return true;
+        }
+        return false;
+    }
+
+    // The slice that holds this position of the line.
+    __device__ int slice_of(long long pos) const {
+        int a = 0, b = static_cast<int>(slices);
+        while (b - a > 1) {
+            const int mid = (a + b) >> 1;
+            if (slice(mid) <= pos) a = mid;
+            else b = mid;
+        }
+        return a;
+    }
+};
+
+struct WarpState {
+    Walk walk;
+    Piece it;
+    int more;
+    int pad;
+};
+
+// The warp's next piece (in ws->it), false after the last.
+__device__ __forceinline__ bool next_piece(const ChunkParams &p, const Plan *pl, WarpState *ws) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) ws->more = ws->walk.next(p, pl, ws->it);
+    __syncwarp();
+    return *const_cast<volatile int *>(&ws->more) != 0;
+}
+
+// ----------------------------------------------------------- shared memory --
+
+// What was taken out of a piece's V: for +inf, -inf and NaN and each dim,
+// ~piece (24 bits) over the first key that had one, counted from the keys
+// every row sees (8 bits: an item has at most 256 tokens).  atomicMin then
+// lets a later piece's entries replace an earlier one's: nothing is reset.
+struct Records {
+    uint32_t first[3][kD];
+    int piece;  // the last piece that left something here
+    int pad[3];
+};
+
+template <bool QUANT>
+struct Smem {
+    static constexpr int kStages = QUANT ? 3 : 5;  // bf16 K/V tiles
+    static constexpr int kRaw = QUANT ? 4 : 0;     // quantised tiles: K codes, V codes, K scales, V scales
+    static constexpr int kRawBytes = 2 * kTile * kD + 2 * kTile;
+    static constexpr int kStageBytes = 2 * kTile * kD * 2;
+    static constexpr int kVOff = kTile * kD * 2;
+    static constexpr int kQ = 0;
+    static constexpr int kKv = kQ + 2 * kSlotRows * kD * 2;
+    static constexpr int kRawOff = kKv + kStages * kStageBytes;
+    static constexpr int kPlan = kRawOff + kRaw * kRawBytes;
+    static constexpr int kRec = kPlan + static_cast<int>(sizeof(Plan));
+    static constexpr int kXch = kRec + kRecords * static_cast<int>(sizeof(Records));
+    static constexpr int kWarps = kXch + kSlotRows * 8;
+    static constexpr int kBars = kWarps + kThreads / 32 * static_cast<int>(sizeof(WarpState));
+    static constexpr int kNumBars = 3 * kStages + 2 * kRaw + 2 + 5 * 2 + 2;
+    static constexpr int kTail = kBars + kNumBars * 8;  // TMEM address, abort flag
+    static constexpr int kBytes = kTail + 16 + 1024;
+    static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
+    static_assert(kKv % 1024 == 0 && kRawOff % 128 == 0 && kPlan % 16 == 0 && kRec % 8 == 0 && kBars % 8 == 0, "alignment");
+};
+
+// Byte of 16-byte chunk `chunk` of a 128-byte row in a 128B-swizzled tile.
+__device__ __forceinline__ uint32_t swz(int row, int chunk) {
+    return static_cast<uint32_t>(row * 128 + ((chunk ^ (row & 7)) << 4));
+}
+
+// Keeps uses of loaded tensor memory behind the wait for it.
+__device__ __forceinline__ void pin32(uint32_t *r) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 8)
+        asm volatile("" : "+r"(r[j]), "+r"(r[j + 1]), "+r"(r[j + 2]), "+r"(r[j + 3]), "+r"(r[j + 4]), "+r"(r[j + 5]),
+                     "+r"(r[j + 6]), "+r"(r[j + 7]));
+}
+
+__device__ __forceinline__ void pin16(uint32_t *r) {
+#pragma unroll
+    for (int j = 0; j < 16; j += 8)
+        asm volatile("" : "+r"(r[j]), "+r"(r[j + 1]), "+r"(r[j + 2]), "+r"(r[j + 3]), "+r"(r[j + 4]), "+r"(r[j + 5]),
+                     "+r"(r[j + 6]), "+r"(r[j + 7]));
+}
+
+// Two e4m3 codes (the top bytes of the halves of h) as bf16 times 2^-120:
+// the sign, and the other seven bits moved to where bf16's exponent ends.
+__device__ __forceinline__ uint32_t widen2(uint32_t h) { return (h & 0x80008000u) | ((h >> 4) & 0x07f007f0u); }
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+template <bool QUANT>
+__global__ void __launch_bounds__(kThreads, 1)
+    k3da_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap q_map,
+                      const __grid_constant__ ChunkParams p) {
+    using L = Smem<QUANT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem =
+        reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    Plan *pl = reinterpret_cast<Plan *>(smem + L::kPlan);
+    Records *recs = reinterpret_cast<Records *>(smem + L::kRec);
+    float2 *xch = reinterpret_cast<float2 *>(smem + L::kXch);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kTail + 8);
+    uint32_t *taddr_slot = reinterpret_cast<uint32_t *>(smem + L::kTail);
+    const uint32_t bars = smem_u32(smem + L::kBars);
+    const uint32_t bar_full = bars;                        // [kStages] bf16 tile loaded (QUANT: unused)
+    const uint32_t bar_prep = bar_full + 8 * L::kStages;   // [kStages] tile prepared
+    const uint32_t bar_empty = bar_prep + 8 * L::kStages;  // [kStages] both slots are done with the tile
+    const uint32_t bar_rfull = bar_empty + 8 * L::kStages; // [kRaw] quantised tile loaded
+    const uint32_t bar_rempty = bar_rfull + 8 * L::kRaw;   // [kRaw] ... and widened
+    const uint32_t bar_qfull = bar_rempty + 8 * L::kRaw, bar_qempty = bar_qfull + 8;
+    const uint32_t bar_sfull = bar_qempty + 8;   // [2] S written
+    const uint32_t bar_sfree = bar_sfull + 16;   // [2] S read
+    const uint32_t bar_pfull = bar_sfree + 16;   // [2] P written
+    const uint32_t bar_pvdone = bar_pfull + 16;  // [2] P V complete
+    const uint32_t bar_ofree = bar_pvdone + 16;  // [2] an item's O read
+    const uint32_t bar_xch = bar_ofree + 16;     // slot 1's half of an alternate item is ready
+    const uint32_t bar_done = bar_xch + 8;       // both issuers' products are complete
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        *abort_flag = 0;
+        for (int s = 0; s < L::kStages; ++s) {
+            mbar_init(bar_full + 8 * s, 1);
+            mbar_init(bar_prep + 8 * s, 4);
+            mbar_init(bar_empty + 8 * s, 2);
+        }
+        for (int s = 0; s < L::kRaw; ++s) {
+            mbar_init(bar_rfull + 8 * s, 1);
+            mbar_init(bar_rempty + 8 * s, 4);
+        }
+        mbar_init(bar_qfull, 1);
+        mbar_init(bar_qempty, 2);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(bar_sfull + 8 * s, 1);
+            mbar_init(bar_sfree + 8 * s, 4);
+            mbar_init(bar_pfull + 8 * s, 4);
+            mbar_init(bar_pvdone + 8 * s, 1);
+            mbar_init(bar_ofree + 8 * s, 4);
+        }
+        mbar_init(bar_xch, 4);
+        mbar_init(bar_done, 2);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    for (int e = threadIdx.x; e < kRecords; e += kThreads) recs[e].piece = -1;
+    for (int e = threadIdx.x; e < kRecords * 3 * kD; e += kThreads)
+        (&recs[e / (3 * kD)].first[0][0])[e % (3 * kD)] = 0xffffffffu;
+    if (warp == kLoadWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(taddr_slot)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    build_plan(p, pl, blockIdx.x == 0);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = *taddr_slot;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    WarpState *ws = reinterpret_cast<WarpState *>(smem + L::kWarps) + warp;
+    const Piece &it = ws->it;
+    if (lane == 0) ws->walk.begin(p, pl, blockIdx.x);
+    bool alive = true;
+
+    if (warp < kPrepWarp) regs_raise<kSoftmaxRegs>();
+    else regs_lower<kOtherRegs>();
+    if (warp < kPrepWarp) {
+        // ------------------------------------------------------ softmax --
+        const int s = warp >> 2;
+        const int rho = threadIdx.x & (kSlotRows - 1);  // this thread's row of the slot
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const int ti = rho / p.G, gi = rho - ti * p.G;
+        int k = 0;       // tiles of this slot so far
+        int pieces = 0;  // pieces with tiles so far
+        int merges = 0;  // alternate pieces with tiles for both slots so far
+        while (alive && next_piece(p, pl, ws)) {
+            const int token = (it.alt ? 0 : s * p.tpt) + ti;  // in the item
+            const bool row_valid = ti < p.tpt && token < it.tokens;
+            const bool warp_valid = __any_sync(kFull, row_valid);
+            const int sees = row_valid ? keys_seen(p, it.ctx, it.n, it.tok0 + token) : 0;
+            const int least = keys_seen(p, it.ctx, it.n, it.tok0 + (it.alt ? 0 : s * p.tpt));  // ... of the slot's rows
+            // The slot's own last tile: in a shared item slot 0 sees fewer keys.
+            const int slot_keys =
+                it.alt || s == 1 ? it.limit : keys_seen(p, it.ctx, it.n, it.tok0 + p.tpt - 1);
+            const int t_end = min(it.t1, (slot_keys + kTile - 1) / kTile);
+            float m = -INFINITY, l = 0.f;
+            int mine = 0;
+            for (int t = it.from(s); t < t_end; t += it.step()) {
+                if (!mbar_wait(bar_sfull + 8 * s, k & 1, abort_flag, p.status)) {
+                    alive = false;
+                    break;
+                }
+                fence_after();
+                if (!warp_valid) {
+                    // No row of this warp's: it only keeps step.
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_sfree + 8 * s);
+                    if (k > 0 && !mbar_wait(bar_pvdone + 8 * s, (k - 1) & 1, abort_flag, p.status)) {
+                        alive = false;
+                        break;
+                    }
+                    fence_after();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_pfull + 8 * s);
+                    ++k;
+                    ++mine;
+                    continue;
+                }
+                uint32_t x[kTile];
+#pragma unroll
+                for (int j = 0; j < kTile; j += 32) tmem_ld32(tmem + lanes + col_s(s) + j, x + j);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < kTile; j += 32) pin32(x + j);
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_sfree + 8 * s);
+                unsigned long long sum[2] = {0ull, 0ull};
+                const int lim = sees - t * kTile;
+                if ((t + 1) * static_cast<long long>(kTile) > least) {
+#pragma unroll
+                    for (int j = 0; j < kTile; ++j) x[j] = j < lim ? x[j] : 0xff800000u;
+                }
+                float mx[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mx[j] = fmaxf(__uint_as_float(x[j]), __uint_as_float(x[j + 4]));
+#pragma unroll
+                for (int j = 8; j < kTile; j += 8)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        mx[q] = fmax3(mx[q], __uint_as_float(x[j + q]), __uint_as_float(x[j + 4 + q]));
+                const float rmax = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
+                // The base of the exponents follows the row's maximum only
+                // when that passes it by 2^8: P up to 256 is as exact, and O
+                // is left alone.
+                const bool need = mine > 0 && rmax > m + kRescale;
+                const float m_new = mine == 0 || need ? rmax : m;
+                const float m_eff = m_new == -INFINITY ? 0.f : m_new;  // a row that has seen nothing yet
+                const float f = need ? exp2_approx(m - m_eff) : 1.f;
+                m = m_new;
+                const unsigned long long sl2 = pack_f32x2(p.scale_log2, p.scale_log2);
+                const unsigned long long nm2 = pack_f32x2(-m_eff, -m_eff);
+                // P of 32 keys from column j on, 16 columns of bf16 pairs.
+                auto weights = [&](int j, uint32_t *pk) {
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) {
+                        const float2 e = unpack_f32x2(fma_f32x2(
+                            pack_f32x2(__uint_as_float(x[j + 2 * q]), __uint_as_float(x[j + 2 * q + 1])), sl2, nm2));
+                        const float p0 = exp2_approx(e.x), p1 = exp2_approx(e.y);
+                        sum[q & 1] = add_f32x2(sum[q & 1], pack_f32x2(p0, p1));
+                        pk[q] = pack2(p0, p1);
+                    }
+                };
+                uint32_t pk0[16], pk1[16];
+                weights(0, pk0);
+                weights(32, pk1);
+                // P's room is free, and O at rest, once the last P V is complete.
+                if (k > 0) {
+                    if (!mbar_wait(bar_pvdone + 8 * s, (k - 1) & 1, abort_flag, p.status)) {
+                        alive = false;
+                        break;
+                    }
+                    fence_after();
+                }
+                if (__any_sync(kFull, need)) {
+#pragma unroll
+                    for (int part = 0; part < 4; ++part) {
+                        uint32_t o[16];
+                        tmem_ld16(tmem + lanes + col_o(s) + 16 * part, o);
+                        tmem_wait_ld();
+                        pin16(o);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                        tmem_st16(tmem + lanes + col_o(s) + 16 * part, o);
+                    }
+                }
+                tmem_st16(tmem + lanes + col_p(s), pk0);
+                tmem_st16(tmem + lanes + col_p(s) + 16, pk1);
+                weights(64, pk0);
+                tmem_st16(tmem + lanes + col_p(s) + 32, pk0);
+                weights(96, pk1);
+                tmem_st16(tmem + lanes + col_p(s) + 48, pk1);
+                const float2 tot = unpack_f32x2(add_f32x2(sum[0], sum[1]));
+                l = l * f + (tot.x + tot.y);
+                tmem_wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_pfull + 8 * s);
+                ++k;
+                ++mine;
+            }
+            if (!alive) break;
+            // ------------------------------------------------- epilogue --
+            const int piece = pieces;
+            if (it.t0 < it.t1) ++pieces;
+            const bool both = it.alt && it.t1 - it.t0 > 1;  // slot 1 has tiles of an alternate item
+            if (mine > 0) {
+                if (!mbar_wait(bar_pvdone + 8 * s, (k - 1) & 1, abort_flag, p.status)) {
+                    alive = false;
+                    break;
+                }
+                fence_after();
+            }
+            if (it.alt && s == 1) {
+                // Slot 0 merges: it owns the same tensor memory lanes.
+                if (both) {
+                    xch[rho] = make_float2(m, l);
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_xch);
+                }
+                continue;
+            }
+            float wa = 1.f, wb = 0.f;
+            if (both) {
+                if (!mbar_wait(bar_xch, merges & 1, abort_flag, p.status)) {
+                    alive = false;
+                    break;
+                }
+                fence_after();
+                ++merges;
+                const float2 o = xch[rho];
+                const float mt = fmaxf(m, o.x);
+                const float me = mt == -INFINITY ? 0.f : mt;
+                wa = exp2_approx(m - me);
+                wb = exp2_approx(o.x - me);
+                l = l * wa + o.y * wb;
+                m = mt;
+            }
+            const bool whole = it.whole();
+            const float norm = whole ? 1.f / l : 1.f;
+            const int row = it.row + token;
+            const int head = it.h * p.G + gi;
+            const int part = (blockIdx.x * 2 + (it.t0 > 0 ? 0 : 1)) * 2 * kSlotRows + s * kSlotRows + rho;
+            const Records &rec = recs[piece % kRecords];
+            const bool dirty = mine > 0 && rec.piece == piece;
+            const int common = keys_seen(p, it.ctx, it.n, it.tok0);  // keys every row of the item sees
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t o[32], ob[32];
+                if (mine > 0) {
+                    tmem_ld32(tmem + lanes + col_o(s) + 32 * half, o);
+                    if (both) tmem_ld32(tmem + lanes + col_o(1) + 32 * half, ob);
+                    tmem_wait_ld();
+                    pin32(o);
+                    if (both) {
+                        pin32(ob);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            o[j] = __float_as_uint(__uint_as_float(o[j]) * wa + __uint_as_float(ob[j]) * wb);
+                    }
+                }
+                if (half == 1) {
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0 && mine > 0) mbar_arrive(bar_ofree + 8 * s);
+                    if (lane == 0 && both) mbar_arrive(bar_ofree + 8);
+                }
+                if (!row_valid) continue;
+                float v[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = l == 0.f ? 0.f : __uint_as_float(o[j]) * norm;
+                if (dirty) {
+                    const uint32_t tag = ~static_cast<uint32_t>(piece) << 8;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const int d = 32 * half + j;
+                        bool seen[3];
+#pragma unroll
+                        for (int q = 0; q < 3; ++q) {
+                            const uint32_t e = rec.first[q][d];
+                            seen[q] = (e & 0xffffff00u) == tag && common + static_cast<int>(e & 0xffu) < sees;
+                        }
+                        if (seen[0]) v[j] += INFINITY;
+                        if (seen[1]) v[j] -= INFINITY;
+                        if (seen[2]) v[j] = __uint_as_float(0x7fffffffu);
+                    }
+                }
+                if (whole) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + (static_cast<long long>(row) * p.Hq + head) * kD + 32 * half);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        dst[j] = make_uint4(pack2(v[8 * j], v[8 * j + 1]), pack2(v[8 * j + 2], v[8 * j + 3]),
+                                            pack2(v[8 * j + 4], v[8 * j + 5]), pack2(v[8 * j + 6], v[8 * j + 7]));
+                    if (half == 0 && p.lse)
+                        p.lse[static_cast<long long>(row) * p.Hq + head] =
+                            l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+                } else {
+                    float4 *dst = reinterpret_cast<float4 *>(p.part_o + static_cast<long long>(part) * kD + 32 * half);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) dst[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    if (half == 0) p.part_ml[part] = make_float2(m, l);
+                }
+            }
+        }
+    } else if (warp < kLoadWarp) {
+        // -------------------------------------------------- preparation --
+        const int tid = threadIdx.x - 32 * kPrepWarp;
+        int x = 0, pieces = 0;
+        while (alive && next_piece(p, pl, ws)) {
+            if (it.t0 >= it.t1) continue;
+            const int piece = pieces++;
+            Records *rec = recs + piece % kRecords;
+            const uint32_t tag = ~static_cast<uint32_t>(piece) << 8;
+            const int least = keys_seen(p, it.ctx, it.n, it.tok0);  // keys that every row of the item sees
+            for (int t = it.t0; t < it.t1; ++t, ++x) {
+                const int st = x % L::kStages;
+                uint8_t *kt = smem + L::kKv + st * L::kStageBytes;
+                uint8_t *vt = kt + L::kVOff;
+                const uint32_t ph = (x / L::kStages) & 1;
+                const uint8_t *raw = smem + L::kRawOff;
+                if (QUANT) {
+                    const int rs = x % (L::kRaw ? L::kRaw : 1);
+                    raw += rs * L::kRawBytes;
+                    if (!mbar_wait(bar_rfull + 8 * rs, (x / (L::kRaw ? L::kRaw : 1)) & 1, abort_flag, p.status) ||
+                        !mbar_wait(bar_empty + 8 * st, ph ^ 1, abort_flag, p.status)) {
+                        alive = false;
+                        break;
+                    }
+                } else if (!mbar_wait(bar_full + 8 * st, ph, abort_flag, p.status)) {
+                    alive = false;
+                    break;
+                }
+                if (QUANT) {
+                    // Four threads a row, 16 codes each.
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const bool is_v = e >= 4;
+                        const int c = (e & 3) * 128 + tid, row = c >> 2, quarter = c & 3;
+                        const uint4 w = *reinterpret_cast<const uint4 *>(raw + (is_v ? kTile * kD : 0) + c * 16);
+                        const uint32_t b = raw[2 * kTile * kD + (is_v ? kTile : 0) + row];
+                        const int key = t * kTile + row;
+                        // 2^120 times the scale, in two factors where it
+                        // passes bf16's range (rows above 448 * 2^7).
+                        const uint32_t e1 = b <= 134u ? b + 120u : 254u;
+                        const uint32_t mul = e1 << 7 | e1 << 23;
+                        uint4 o[2];
+                        uint32_t *ov = reinterpret_cast<uint32_t *>(o);
+                        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            ov[2 * q] = mul_bf16x2(widen2(__byte_perm(in[q], 0, 0x1404)), mul);
+                            ov[2 * q + 1] = mul_bf16x2(widen2(__byte_perm(in[q], 0, 0x3424)), mul);
+                        }
+                        if (b > 134u) {
+                            const uint32_t mul2 = (b - 7u) << 7 | (b - 7u) << 23;
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) ov[q] = b == 255u ? 0x7fff7fffu : mul_bf16x2(ov[q], mul2);
+                        }
+                        if (is_v && (key >= it.limit || (b == 255u && key >= least))) {
+                            if (key < it.limit) {
+#pragma unroll
+                                for (int d = 0; d < 16; ++d) atomicMin(&rec->first[2][quarter * 16 + d], tag | (key - least));
+                                rec->piece = piece;
+                            }
+                            o[0] = o[1] = make_uint4(0, 0, 0, 0);
+                        }
+                        uint8_t *dst = is_v ? vt : kt;
+                        *reinterpret_cast<uint4 *>(dst + swz(row, 2 * quarter)) = o[0];
+                        *reinterpret_cast<uint4 *>(dst + swz(row, 2 * quarter + 1)) = o[1];
+                    }
+                    fence_proxy_async();
+                } else if ((t + 1) * static_cast<long long>(kTile) > least) {
+                    const int key = t * kTile + tid;  // this thread's V row
+                    if (key >= it.limit) {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(vt + swz(tid, c)) = make_uint4(0, 0, 0, 0);
+                    } else if (key >= least) {
+                        for (int c = 0; c < 8; ++c) {
+                            uint4 *at = reinterpret_cast<uint4 *>(vt + swz(tid, c));
+                            const uint4 w = *at;
+                            uint32_t v[4] = {w.x, w.y, w.z, w.w};
+                            bool bad = false;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                bad |= (v[q] & 0x7f80u) == 0x7f80u || (v[q] & 0x7f800000u) == 0x7f800000u;
+                            if (!bad) continue;
+                            for (int q = 0; q < 8; ++q) {
+                                const uint32_t e = v[q >> 1] >> (16 * (q & 1)) & 0xffffu;
+                                if ((e & 0x7f80u) != 0x7f80u) continue;
+                                const int kind = e & 0x7fu ? 2 : e >> 15;
+                                atomicMin(&rec->first[kind][8 * c + q], tag | (key - least));
+                                v[q >> 1] &= q & 1 ? 0x0000ffffu : 0xffff0000u;
+                            }
+                            *at = make_uint4(v[0], v[1], v[2], v[3]);
+                            rec->piece = piece;
+                        }
+                    }
+                    fence_proxy_async();
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar_prep + 8 * st);
+                    if (QUANT) mbar_arrive(bar_rempty + 8 * (x % (L::kRaw ? L::kRaw : 1)));
+                }
+            }
+        }
+    } else if (warp == kLoadWarp) {
+        // ------------------------------------------------------ K/V loads --
+        constexpr int S = QUANT ? L::kRaw : L::kStages;
+        const uint32_t full = QUANT ? bar_rfull : bar_full, empty = QUANT ? bar_rempty : bar_empty;
+        constexpr int kPageTile = kP * kD * (QUANT ? 1 : 2);  // bytes of a page's K or V of one head
+        uint64_t policy;  // pages are read again by the items of other token pairs
+        asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
+        int x = 0;
+        Cut cut = {};
+        while (alive && next_piece(p, pl, ws)) {
+            if (it.t0 > 0) cut.has[0] = 1;
+            if (it.t0 == 0 && it.t1 < it.nt) {
+                cut.has[1] = 1;
+                cut.row = it.row;
+                cut.tokens = it.tokens;
+                cut.head = it.h;
+                cut.last = ws->walk.slice_of(it.start + it.length - 1);
+            }
+            const int pages = (it.limit + kP - 1) / kP;
+            int mine = -2;
+            for (int t = it.t0; t < it.t1; ++t, ++x) {
+                const int ahead = (t - it.t0) & 15;
+                if (ahead == 0) {
+                    // The next 32 pages, one a lane: row of its K, -1 where
+                    // the id is no page, -2 past the item's last key.
+                    const int pg = 2 * t + lane;
+                    mine = -2;
+                    if (pg < pages && pg < 2 * it.t1) {
+                        const long long page = page_of(p.page_table, p.page_stride, p.num_pages, it.r, pg * kP);
+                        mine = page < 0 ? -1 : static_cast<int>((page * 2 * p.Hkv + it.h) * kP);
+                    }
+                }
+                const int st = x % S;
+                if (!mbar_wait(empty + 8 * st, ((x / S) & 1) ^ 1, abort_flag, p.status)) {
+                    alive = false;
+                    break;
+                }
+                uint8_t *dst = smem + (QUANT ? L::kRawOff + st * L::kRawBytes : L::kKv + st * L::kStageBytes);
+                uint32_t bytes = 0;
+                int krow[2];
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    krow[half] = __shfl_sync(kFull, mine, 2 * ahead + half);
+                    if (krow[half] >= 0) bytes += 2 * kPageTile + (QUANT ? 2 * kP : 0);
+                    if (krow[half] == -1) {
+                        if (lane == 0 && p.status) atomicOr(p.status, K3DA_STATUS_BAD_PAGE);
+                        for (int e = lane; e < kPageTile / 16; e += 32) {
+                            reinterpret_cast<uint4 *>(dst + half * kPageTile)[e] = make_uint4(0, 0, 0, 0);
+                            reinterpret_cast<uint4 *>(dst + (2 + half) * kPageTile)[e] = make_uint4(0, 0, 0, 0);
+                        }
+                        if (QUANT)
+                            for (int e = lane; e < kP; e += 32)
+                                dst[4 * kPageTile + half * kP + e] = dst[4 * kPageTile + (2 + half) * kP + e] = 0;
+                        fence_proxy_async();
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    const uint32_t bar = full + 8 * st;
+                    if (bytes > 0) mbar_arrive_expect_tx(bar, bytes);
+                    else mbar_arrive(bar);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        if (krow[half] < 0) continue;
+                        const int vrow = krow[half] + p.Hkv * kP;
+                        tma_load_2d(smem_u32(dst + half * kPageTile), &kv_map, 0, krow[half], bar, policy);
+                        tma_load_2d(smem_u32(dst + (2 + half) * kPageTile), &kv_map, 0, vrow, bar, policy);
+                        if (QUANT) {
+                            bulk_load(smem_u32(dst + 4 * kPageTile + half * kP), p.scales + krow[half], kP, bar);
+                            bulk_load(smem_u32(dst + 4 * kPageTile + (2 + half) * kP), p.scales + vrow, kP, bar);
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        if (lane == 0) p.cuts[blockIdx.x] = cut;
+        // Loads in flight land before the CTA leaves (a wait that gave up).
+        if (!alive) {
+            for (int j = x > S ? x - S : 0; j < x; ++j) {
+                const unsigned long long t0 = global_ns();
+                while (!mbar_try_wait(full + 8 * (j % S), (j / S) & 1) && global_ns() - t0 < kWaitLimitNs) {
+                }
+            }
+        }
+    } else if (warp == kQWarp) {
+        // -------------------------------------------------------- Q loads --
+        int j = 0;
+        if (lane == 0) {
+            const uint32_t box = static_cast<uint32_t>(p.G) * p.tpt * 128;
+            while (alive && ws->walk.next(p, pl, ws->it)) {
+                if (it.t0 >= it.t1) continue;
+                if (!mbar_wait(bar_qempty, (j & 1) ^ 1, abort_flag, p.status)) {
+                    alive = false;
+                    break;
+                }
+                mbar_arrive_expect_tx(bar_qfull, it.alt ? box : 2 * box);
+                tma_load_3d(smem_u32(smem + L::kQ), &q_map, 0, it.h * p.G, it.row, bar_qfull);
+                if (!it.alt)
+                    tma_load_3d(smem_u32(smem + L::kQ + kSlotRows * 128), &q_map, 0, it.h * p.G, it.row + p.tpt, bar_qfull);
+                ++j;
+            }
+            if (!alive && j > 0) {
+                const unsigned long long t0 = global_ns();
+                while (!mbar_try_wait(bar_qfull, (j - 1) & 1) && global_ns() - t0 < kWaitLimitNs) {
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        // --------------------------------------------------- MMA issuers --
+        // One thread a slot.  Q K^T of the slot's next tile needs K and a
+        // free S, P V of its last needs P: whichever has its operands is
+        // issued first, with at most two P V outstanding.
+        const int s = warp - kMmaWarp;
+        if (lane == 0) {
+            int x = 0;      // the CTA's tiles
+            int k = 0;      // Q K^T issued
+            int kp = 0;     // P V issued
+            int j = 0;      // pieces with tiles
+            int items = 0;  // ... of them, with tiles for this slot
+            // The tiles whose P V is outstanding, the older first: stage,
+            // tile count, and the number of the slot's item (from 1) at its
+            // first tile, else 0.
+            int st_a = 0, x_a = 0, item_a = 0, st_b = 0, x_b = 0, item_b = 0;
+            auto pv_ready = [&]() -> bool {
+                return mbar_test(bar_pfull + 8 * s, kp & 1) &&
+                       mbar_test(bar_prep + 8 * st_a, (x_a / L::kStages) & 1) &&
+                       (item_a < 2 || mbar_test(bar_ofree + 8 * s, item_a & 1));
+            };
+            auto issue_pv = [&]() {
+                const uint64_t v = desc_sw128(smem_u32(smem + L::kKv + st_a * L::kStageBytes + L::kVOff));
+#pragma unroll
+                for (int kk = 0; kk < kTile / 16; ++kk)
+                    mma_ts(tmem + col_o(s), tmem + col_p(s) + 8 * kk, v + ((kk * 2048) >> 4), kIdescPV,
+                           (kk > 0 || item_a == 0) ? 1u : 0u);
+                mma_commit(bar_pvdone + 8 * s);
+                mma_commit(bar_empty + 8 * st_a);
+                st_a = st_b;
+                x_a = x_b;
+                item_a = item_b;
+                ++kp;
+            };
+            unsigned long long t0 = global_ns();
+            unsigned spins = 0;
+            // Whether to go on waiting: not past the limit, nor after
+            // another warp gave up.
+            auto patient = [&]() -> bool {
+                if ((++spins & 255u) != 0) return true;
+                if (*abort_flag) return false;
+                if (global_ns() - t0 < kWaitLimitNs) return true;
+                *abort_flag = 1;
+                if (p.status) atomicOr(p.status, K3DA_STATUS_TIMEOUT);
+                return false;
+            };
+            while (alive && ws->walk.next(p, pl, ws->it)) {
+                if (it.t0 >= it.t1) continue;
+                const int slot_keys = it.alt || s == 1 ? it.limit : keys_seen(p, it.ctx, it.n, it.tok0 + p.tpt - 1);
+                const int t_end = min(it.t1, (slot_keys + kTile - 1) / kTile);
+                const int t_from = it.from(s);
+                const int last = t_from >= t_end ? -1 : it.alt ? t_from + ((t_end - 1 - t_from) & ~1) : t_end - 1;
+                if (last >= 0) ++items;
+                const uint64_t qd = desc_sw128(smem_u32(smem + L::kQ + (it.alt ? 0 : s * kSlotRows * 128)));
+                for (int t = it.t0; t < it.t1 && alive; ++t, ++x) {
+                    const int st = x % L::kStages;
+                    const uint32_t ready = QUANT ? bar_prep + 8 * st : bar_full + 8 * st;
+                    const uint32_t ph = (x / L::kStages) & 1;
+                    const bool mine = t >= t_from && t <= last && (!it.alt || ((t - t_from) & 1) == 0);
+                    t0 = global_ns();
+                    bool taken = false;
+                    while (!taken && alive) {
+                        if (k > kp && pv_ready()) {
+                            fence_after();
+                            issue_pv();
+                        }
+                        if (!mine) {
+                            taken = mbar_test(ready, ph);
+                            if (taken) mbar_arrive(bar_empty + 8 * st);
+                        } else if (k - kp < 2 && mbar_test(ready, ph) &&
+                                   (k == 0 || mbar_test(bar_sfree + 8 * s, (k - 1) & 1)) &&
+                                   (t != t_from || mbar_test(bar_qfull, j & 1))) {
+                            fence_after();
+                            const uint64_t kd = desc_sw128(smem_u32(smem + L::kKv + st * L::kStageBytes));
+#pragma unroll
+                            for (int kk = 0; kk < kD / 16; ++kk)
+                                mma_ss(tmem + col_s(s), qd + ((kk * 32) >> 4), kd + ((kk * 32) >> 4), kIdescQK,
+                                       kk > 0 ? 1u : 0u);
+                            mma_commit(bar_sfull + 8 * s);
+                            if (t == last) mma_commit(bar_qempty);
+                            st_b = st;
+                            x_b = x;
+                            item_b = t == t_from ? items : 0;
+                            if (k == kp) {
+                                st_a = st_b;
+                                x_a = x_b;
+                                item_a = item_b;
+                            }
+                            ++k;
+                            taken = true;
+                        }
+                        if (!taken) alive = patient();
+                    }
+                }
+                if (last < 0) {
+                    // Nothing of this piece for the slot: Q is not needed.
+                    // An outstanding P V is issued meanwhile (the other
+                    // slot's way to this Q may lead through it).
+                    t0 = global_ns();
+                    while (alive && !mbar_test(bar_qfull, j & 1)) {
+                        if (k > kp && pv_ready()) {
+                            fence_after();
+                            issue_pv();
+                        }
+                        alive = patient();
+                    }
+                    if (alive) mbar_arrive(bar_qempty);
+                }
+                ++j;
+            }
+            t0 = global_ns();
+            while (k > kp && alive) {
+                if (pv_ready()) {
+                    fence_after();
+                    issue_pv();
+                } else {
+                    alive = patient();
+                }
+            }
+            // Every product and its signals complete before the CTA leaves.
+            fence_after();
+            mma_commit(bar_done);
+            t0 = global_ns();
+            while (!mbar_try_wait(bar_done, 0) && global_ns() - t0 < kWaitLimitNs) {
+            }
+        }
+        __syncwarp();
+    }
+
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == kLoadWarp)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+}
+
+// ----------------------------------------------------------------- combine --
+//
+// Folds the partial results of the items that a cut of the line fell into,
+// in the order of their pieces.  CTA (x, y) takes rows [y * rows, (y + 1) *
+// rows) of the x-th such item: 16 threads a row (4 dims each) times `lanes`
+// piece lanes, lane i folding the pieces i, i + lanes, ...; one lane where
+// there are few pieces (a long chunk: many rows, two or three pieces), eight
+// where one item spreads over many CTAs.  A programmatic dependent of the
+// main kernel: its launch overlaps that kernel's end.
+constexpr int kCombineThreads = 256;
+
+__global__ void __launch_bounds__(kCombineThreads)
+    k3da_chunk_combine_kernel(const __grid_constant__ ChunkParams p, int rows) {
+    __shared__ int votes[kCombineThreads / 32];
+    __shared__ int owner;
+    __shared__ float4 part[8][32];
+    __shared__ float2 part_ml[8][2];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // The x-th CTA that left an item unfinished.
+    static_assert(kCtas <= kCombineThreads, "one CTA a thread");
+    const bool cut_here = tid < kCtas && p.cuts[tid].has[1];
+    const unsigned vote = __ballot_sync(kFull, cut_here);
+    if (lane == 0) votes[warp] = __popc(vote);
+    if (tid == 0) owner = -1;
+    __syncthreads();
+    int rank = __popc(vote & ((1u << lane) - 1u));
+    for (int w = 0; w < warp; ++w) rank += votes[w];
+    if (cut_here && rank == static_cast<int>(blockIdx.x)) owner = tid;
+    __syncthreads();
+    const int a = owner;
+    if (a < 0) return;
+    const Cut cut = p.cuts[a];
+    const int pieces = cut.last - a + 1;
+    const int lanes = pieces > 8 ? 8 : 1;
+    const int dim = tid & 15;
+    const int pl = lanes == 8 ? (tid >> 4) & 7 : 0;
+    const int per_pass = kCombineThreads / 16 / lanes;
+    const int slot_rows = p.tpt * p.G;
+    for (int base = 0; base < rows; base += per_pass) {
+        const int local = lanes == 8 ? tid >> 7 : tid >> 4;
+        const int rho = blockIdx.y * rows + base + local;  // the item's row, slot by slot
+        const int s = rho / kSlotRows, in_slot = rho % kSlotRows;
+        const int token = s * p.tpt + in_slot / p.G;
+        const bool valid = base + local < rows && rho < 2 * kSlotRows && in_slot < slot_rows && token < cut.tokens;
+        float m = -INFINITY, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (valid) {
+            constexpr int kFold = 4;  // pieces whose loads are in flight together
+            for (int j = pl; j < pieces; j += lanes * kFold) {
+                float2 ml[kFold];
+                float4 v[kFold];
+#pragma unroll
+                for (int q = 0; q < kFold; ++q) {
+                    const int i = j + q * lanes;
+                    ml[q] = make_float2(-INFINITY, 0.f);
+                    v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (i >= pieces || (i > 0 && !p.cuts[a + i].has[0])) continue;
+                    const long long at = (static_cast<long long>(a + i) * 2 + (i == 0 ? 1 : 0)) * 2 * kSlotRows + rho;
+                    ml[q] = p.part_ml[at];
+                    v[q] = reinterpret_cast<const float4 *>(p.part_o + at * kD)[dim];
+                }
+#pragma unroll
+                for (int q = 0; q < kFold; ++q) {
+                    const float mt = fmaxf(m, ml[q].x);
+                    const float me = mt == -INFINITY ? 0.f : mt;
+                    const float f = exp2_approx(m - me), g = exp2_approx(ml[q].x - me);
+                    l = l * f + ml[q].y * g;
+                    o.x = o.x * f + v[q].x * g;
+                    o.y = o.y * f + v[q].y * g;
+                    o.z = o.z * f + v[q].z * g;
+                    o.w = o.w * f + v[q].w * g;
+                    m = mt;
+                }
+            }
+        }
+        if (lanes == 8) {
+            part[pl][tid & 15 | (tid >> 7) << 4] = o;
+            if (dim == 0) part_ml[pl][tid >> 7] = make_float2(m, l);
+            __syncthreads();
+            if (pl == 0) {
+                for (int q = 1; q < 8; ++q) {
+                    const float2 ml = part_ml[q][tid >> 7];
+                    const float4 v = part[q][tid & 15 | (tid >> 7) << 4];
+                    const float mt = fmaxf(m, ml.x);
+                    const float me = mt == -INFINITY ? 0.f : mt;
+                    const float f = exp2_approx(m - me), g = exp2_approx(ml.x - me);
+                    l = l * f + ml.y * g;
+                    o.x = o.x * f + v.x * g;
+                    o.y = o.y * f + v.y * g;
+                    o.z = o.z * f + v.z * g;
+                    o.w = o.w * f + v.w * g;
+                    m = mt;
+                }
+            }
+            __syncthreads();
+        }
+        if (valid && pl == 0) {
+            const float norm = 1.f / l;
+            const long long at = static_cast<long long>(cut.row + token) * p.Hq + cut.head * p.G + in_slot % p.G;
+            uint2 w = make_uint2(0, 0);
+            if (l != 0.f) w = make_uint2(pack2(o.x * norm, o.y * norm), pack2(o.z * norm, o.w * norm));
+            reinterpret_cast<uint2 *>(p.out + at * kD)[dim] = w;
+            if (dim == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        }
+    }
+}
+
+// -------------------------------------------------------------------- host --
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static std::mutex mutex;
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    std::lock_guard<std::mutex> lock(mutex);
+    if (fn == nullptr) {
+        cudaDriverEntryPointQueryResult q;
+        void *f = nullptr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    }
+    return fn;
+}
+
+template <bool QUANT>
+int launch_chunk(const CUtensorMap &kv_map, const CUtensorMap &q_map, const ChunkParams &prm, cudaStream_t st) {
+    // Set at every call: a context has its own copy of the attribute.
+    if (cudaFuncSetAttribute(k3da_chunk_kernel<QUANT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Smem<QUANT>::kBytes) != cudaSuccess)
+        return K3DA_ECUDA;
+    k3da_chunk_kernel<QUANT><<<kCtas, kThreads, Smem<QUANT>::kBytes, st>>>(kv_map, q_map, prm);
+    return cudaGetLastError() == cudaSuccess ? K3DA_OK : K3DA_ECUDA;
 }
 
 }  // namespace
@@ -123,7 +1172,7 @@ extern "C" size_t k3da_chunk_workspace_bytes(int num_tokens, int num_requests, i
     if (num_tokens < 0 || num_requests < 1 || num_requests > kMaxRequests || !heads_ok(num_q_heads, num_kv_heads) ||
         page_stride < 1 || page_stride > kMaxPageStride)
         return 0;
-    return 256;
+    return kWorkspace;
 }
 
 extern "C" int k3da_chunk_attn(void *out, float *lse, const void *q, int64_t q_row_stride, int num_tokens,
@@ -141,9 +1190,7 @@ extern "C" int k3da_chunk_attn(void *out, float *lse, const void *q, int64_t q_r
     if (!aligned_to(out, 16) || !aligned_to(q, 16) || !aligned_to(lse, 4)) return K3DA_EINVAL;
     const int64_t width = static_cast<int64_t>(num_q_heads) * kD;
     if (q_row_stride < width || q_row_stride % 8 != 0 || q_row_stride > (1LL << 31)) return K3DA_EINVAL;
-    if (!workspace || !aligned_to(workspace, 256)) return K3DA_EWORKSPACE;
-    if (workspace_bytes < k3da_chunk_workspace_bytes(num_tokens, num_requests, num_q_heads, num_kv_heads, page_stride))
-        return K3DA_EWORKSPACE;
+    if (!workspace || !aligned_to(workspace, 256) || workspace_bytes < kWorkspace) return K3DA_EWORKSPACE;
     if (num_tokens == 0) return K3DA_OK;
     if (!out || !q) return K3DA_EINVAL;
     const size_t out_bytes = static_cast<size_t>(num_tokens) * width * 2;
@@ -151,30 +1198,78 @@ extern "C" int k3da_chunk_attn(void *out, float *lse, const void *q, int64_t q_r
     if (overlap(out, out_bytes, q, q_bytes) ||
         overlap(out, out_bytes, kv_pool, pool_bytes(num_pages, num_kv_heads, cache_dtype)))
         return K3DA_EINVAL;
+
     ChunkParams prm;
     std::memset(&prm, 0, sizeof prm);
     prm.out = static_cast<__nv_bfloat16 *>(out);
     prm.lse = lse;
-    prm.q = static_cast<const __nv_bfloat16 *>(q);
-    prm.pool = static_cast<const uint8_t *>(kv_pool);
     prm.scales = static_cast<const uint8_t *>(kv_scales);
     prm.page_table = page_table;
     prm.ctx_lens = ctx_lens;
     prm.cu_seqlens = cu_seqlens;
     prm.status = status;
-    prm.q_stride = q_row_stride;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    prm.cuts = reinterpret_cast<Cut *>(ws);
+    prm.part_ml = reinterpret_cast<float2 *>(ws + kCutBytes);
+    prm.part_o = reinterpret_cast<float *>(ws + kCutBytes + kPartRows * sizeof(float2));
     prm.num_pages = num_pages;
     prm.page_stride = page_stride;
     prm.R = num_requests;
     prm.T = num_tokens;
     prm.Hq = num_q_heads;
     prm.Hkv = num_kv_heads;
+    prm.G = num_q_heads / num_kv_heads;
+    prm.tpt = kSlotRows / prm.G;
     prm.mask = mask;
     prm.scale_log2 = softmax_scale * 1.4426950408889634f;
-    const long long warps = static_cast<long long>(num_tokens) * num_q_heads;
-    const unsigned ctas = static_cast<unsigned>((warps + kWarps - 1) / kWarps);
+
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (encode == nullptr) return K3DA_ECUDA;
+    const bool quant = cache_dtype == K3DA_CACHE_E4M3;
+    CUtensorMap kv_map, q_map;
+    {
+        const cuuint64_t dims[2] = {kD, static_cast<cuuint64_t>(num_pages) * 2 * num_kv_heads * kP};
+        const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kD) * (quant ? 1 : 2)};
+        const cuuint32_t box[2] = {kD, kP}, estrides[2] = {1, 1};
+        if (encode(&kv_map, quant ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                   const_cast<void *>(kv_pool), dims, strides, box, estrides, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   quant ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return K3DA_ECUDA;
+    }
+    {
+        const cuuint64_t dims[3] = {kD, static_cast<cuuint64_t>(num_q_heads), static_cast<cuuint64_t>(num_tokens)};
+        const cuuint64_t strides[2] = {kD * 2, static_cast<cuuint64_t>(q_row_stride) * 2};
+        const cuuint32_t box[3] = {kD, static_cast<cuuint32_t>(prm.G), static_cast<cuuint32_t>(prm.tpt)};
+        const cuuint32_t estrides[3] = {1, 1, 1};
+        if (encode(&q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box, estrides,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return K3DA_ECUDA;
+    }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (cache_dtype == K3DA_CACHE_E4M3) k3da_chunk_simple_kernel<true><<<ctas, 32 * kWarps, 0, st>>>(prm);
-    else k3da_chunk_simple_kernel<false><<<ctas, 32 * kWarps, 0, st>>>(prm);
-    return cudaGetLastError() == cudaSuccess ? K3DA_OK : K3DA_ECUDA;
+    const int launched = quant ? launch_chunk<true>(kv_map, q_map, prm, st) : launch_chunk<false>(kv_map, q_map, prm, st);
+    if (launched != K3DA_OK) return launched;
+
+    // Items a cut can fall into, rows one can have: a grid of about 1200
+    // CTAs over both.
+    const long long items =
+        ((static_cast<long long>(num_tokens) + 2 * prm.tpt - 1) / (2 * prm.tpt) + num_requests) * num_kv_heads;
+    const unsigned gx = static_cast<unsigned>(items < kCtas ? items : kCtas);
+    const long long bound = static_cast<long long>(num_tokens) * prm.G < 2 * kSlotRows
+                                ? (num_tokens <= prm.tpt ? num_tokens * prm.G : 2 * kSlotRows)
+                                : 2 * kSlotRows;
+    int rows = static_cast<int>((bound * gx + 1215) / 1216);
+    rows = rows < 2 ? 2 : rows;
+    cudaLaunchConfig_t lc;
+    std::memset(&lc, 0, sizeof lc);
+    lc.gridDim = dim3(gx, static_cast<unsigned>((bound + rows - 1) / rows));
+    lc.blockDim = dim3(kCombineThreads);
+    lc.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelEx(&lc, k3da_chunk_combine_kernel, prm, rows) == cudaSuccess ? K3DA_OK : K3DA_ECUDA;
 }
