@@ -625,84 +625,83 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Records &rec = recs[piece % kRecords];
             const bool dirty = mine > 0 && rec.piece == piece;
             const int common = keys_seen(p, it.ctx, it.n, it.tok0);  // keys every row of the item sees
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t o[32], ob[32];
+            if (row_valid && whole && p.lse)
+                p.lse[static_cast<long long>(row) * p.Hq + head] =
+                    l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+            if (row_valid && !whole) p.part_ml[part] = make_float2(m, l);
+            // 16 dims at a time: the registers are the main loop's.
+#pragma unroll 1
+            for (int d0 = 0; d0 < kD; d0 += 16) {
+                uint32_t o[16], ob[16];
                 if (mine > 0) {
-                    tmem_ld32(tmem + lanes + col_o(s) + 32 * half, o);
-                    if (both) tmem_ld32(tmem + lanes + col_o(1) + 32 * half, ob);
+                    tmem_ld16(tmem + lanes + col_o(s) + d0, o);
+                    if (both) tmem_ld16(tmem + lanes + col_o(1) + d0, ob);
                     tmem_wait_ld();
-                    pin32(o);
+                    pin16(o);
                     if (both) {
-                        pin32(ob);
+                        pin16(ob);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
+                        for (int j = 0; j < 16; ++j)
                             o[j] = __float_as_uint(__uint_as_float(o[j]) * wa + __uint_as_float(ob[j]) * wb);
                     }
                 }
-                if (half == 1) {
+                if (d0 == kD - 16) {
                     fence_before();
                     __syncwarp();
                     if (lane == 0 && mine > 0) mbar_arrive(bar_ofree + 8 * s);
                     if (lane == 0 && both) mbar_arrive(bar_ofree + 8);
                 }
                 if (!row_valid) continue;
-                float v[32];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = l == 0.f ? 0.f : __uint_as_float(o[j]) * norm;
+                for (int j = 0; j < 16; ++j) o[j] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[j]) * norm);
                 if (dirty) {
                     const uint32_t tag = ~static_cast<uint32_t>(piece) << 8;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const int d = 32 * half + j;
+                    for (int j = 0; j < 16; ++j) {
                         bool seen[3];
 #pragma unroll
                         for (int q = 0; q < 3; ++q) {
-                            const uint32_t e = rec.first[q][d];
+                            const uint32_t e = rec.first[q][d0 + j];
                             seen[q] = (e & 0xffffff00u) == tag && common + static_cast<int>(e & 0xffu) < sees;
                         }
-                        if (seen[0]) v[j] += INFINITY;
-                        if (seen[1]) v[j] -= INFINITY;
-                        if (seen[2]) v[j] = __uint_as_float(0x7fffffffu);
+                        float v = __uint_as_float(o[j]);
+                        if (seen[0]) v += INFINITY;
+                        if (seen[1]) v -= INFINITY;
+                        if (seen[2]) v = __uint_as_float(0x7fffffffu);
+                        o[j] = __float_as_uint(v);
                     }
                 }
                 if (whole) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + (static_cast<long long>(row) * p.Hq + head) * kD + 32 * half);
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + (static_cast<long long>(row) * p.Hq + head) * kD + d0);
+                    uint32_t w[8];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        dst[j] = make_uint4(pack2(v[8 * j], v[8 * j + 1]), pack2(v[8 * j + 2], v[8 * j + 3]),
-                                            pack2(v[8 * j + 4], v[8 * j + 5]), pack2(v[8 * j + 6], v[8 * j + 7]));
-                    if (half == 0 && p.lse)
-                        p.lse[static_cast<long long>(row) * p.Hq + head] =
-                            l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+                    for (int j = 0; j < 8; ++j) w[j] = pack2(__uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1]));
+                    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
                 } else {
-                    float4 *dst = reinterpret_cast<float4 *>(p.part_o + static_cast<long long>(part) * kD + 32 * half);
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.part_o + static_cast<long long>(part) * kD + d0);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) dst[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-                    if (half == 0) p.part_ml[part] = make_float2(m, l);
+                    for (int j = 0; j < 4; ++j) dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
                 }
             }
         }
     } else if (warp < kLoadWarp) {
         // -------------------------------------------------- preparation --
         const int tid = threadIdx.x - 32 * kPrepWarp;
-        int x = 0, pieces = 0;
+        int st = 0, rs = 0, pieces = 0;
+        uint32_t ph = 0, rph = 0;  // rounds of the stages, mod 2
         while (alive && next_piece(p, pl, ws)) {
             if (it.t0 >= it.t1) continue;
             const int piece = pieces++;
             Records *rec = recs + piece % kRecords;
             const uint32_t tag = ~static_cast<uint32_t>(piece) << 8;
             const int least = keys_seen(p, it.ctx, it.n, it.tok0);  // keys that every row of the item sees
-            for (int t = it.t0; t < it.t1; ++t, ++x) {
-                const int st = x % L::kStages;
+            for (int t = it.t0; t < it.t1; ++t) {
                 uint8_t *kt = smem + L::kKv + st * L::kStageBytes;
                 uint8_t *vt = kt + L::kVOff;
-                const uint32_t ph = (x / L::kStages) & 1;
-                const uint8_t *raw = smem + L::kRawOff;
+                const uint8_t *raw = smem + L::kRawOff + rs * L::kRawBytes;
                 if (QUANT) {
-                    const int rs = x % (L::kRaw ? L::kRaw : 1);
-                    raw += rs * L::kRawBytes;
-                    if (!mbar_wait(bar_rfull + 8 * rs, (x / (L::kRaw ? L::kRaw : 1)) & 1, abort_flag, p.status) ||
+                    if (!mbar_wait(bar_rfull + 8 * rs, rph, abort_flag, p.status) ||
                         !mbar_wait(bar_empty + 8 * st, ph ^ 1, abort_flag, p.status)) {
                         alive = false;
                         break;
@@ -713,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (QUANT) {
                     // Four threads a row, 16 codes each.
-#pragma unroll
+#pragma unroll 2
                     for (int e = 0; e < 8; ++e) {
                         const bool is_v = e >= 4;
                         const int c = (e & 3) * 128 + tid, row = c >> 2, quarter = c & 3;
@@ -781,7 +780,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(bar_prep + 8 * st);
-                    if (QUANT) mbar_arrive(bar_rempty + 8 * (x % (L::kRaw ? L::kRaw : 1)));
+                    if (QUANT) mbar_arrive(bar_rempty + 8 * rs);
+                }
+                if (++st == L::kStages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+                if (QUANT && ++rs == L::kRaw) {
+                    rs = 0;
+                    rph ^= 1;
                 }
             }
         }
@@ -901,30 +908,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         // issued first, with at most two P V outstanding.
         const int s = warp - kMmaWarp;
         if (lane == 0) {
-            int x = 0;      // the CTA's tiles
+            int st = 0;     // the tile's stage
+            uint32_t ph = 0;  // ... and how often the stages have come round, mod 2
             int k = 0;      // Q K^T issued
             int kp = 0;     // P V issued
             int j = 0;      // pieces with tiles
             int items = 0;  // ... of them, with tiles for this slot
             // The tiles whose P V is outstanding, the older first: stage,
-            // tile count, and the number of the slot's item (from 1) at its
-            // first tile, else 0.
-            int st_a = 0, x_a = 0, item_a = 0, st_b = 0, x_b = 0, item_b = 0;
+            // round (bit 8), and the number of the slot's item (from 1) at
+            // its first tile, else 0.
+            uint32_t at_a = 0, at_b = 0;
+            int item_a = 0, item_b = 0;
             auto pv_ready = [&]() -> bool {
-                return mbar_test(bar_pfull + 8 * s, kp & 1) &&
-                       mbar_test(bar_prep + 8 * st_a, (x_a / L::kStages) & 1) &&
+                return mbar_test(bar_pfull + 8 * s, kp & 1) && mbar_test(bar_prep + 8 * (at_a & 255u), at_a >> 8) &&
                        (item_a < 2 || mbar_test(bar_ofree + 8 * s, item_a & 1));
             };
             auto issue_pv = [&]() {
-                const uint64_t v = desc_sw128(smem_u32(smem + L::kKv + st_a * L::kStageBytes + L::kVOff));
+                const uint64_t v = desc_sw128(smem_u32(smem + L::kKv) + (at_a & 255u) * L::kStageBytes + L::kVOff);
 #pragma unroll
                 for (int kk = 0; kk < kTile / 16; ++kk)
                     mma_ts(tmem + col_o(s), tmem + col_p(s) + 8 * kk, v + ((kk * 2048) >> 4), kIdescPV,
                            (kk > 0 || item_a == 0) ? 1u : 0u);
                 mma_commit(bar_pvdone + 8 * s);
-                mma_commit(bar_empty + 8 * st_a);
-                st_a = st_b;
-                x_a = x_b;
+                mma_commit(bar_empty + 8 * (at_a & 255u));
+                at_a = at_b;
                 item_a = item_b;
                 ++kp;
             };
@@ -948,10 +955,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int last = t_from >= t_end ? -1 : it.alt ? t_from + ((t_end - 1 - t_from) & ~1) : t_end - 1;
                 if (last >= 0) ++items;
                 const uint64_t qd = desc_sw128(smem_u32(smem + L::kQ + (it.alt ? 0 : s * kSlotRows * 128)));
-                for (int t = it.t0; t < it.t1 && alive; ++t, ++x) {
-                    const int st = x % L::kStages;
-                    const uint32_t ready = QUANT ? bar_prep + 8 * st : bar_full + 8 * st;
-                    const uint32_t ph = (x / L::kStages) & 1;
+                for (int t = it.t0; t < it.t1 && alive; ++t) {
+                    const uint32_t ready = (QUANT ? bar_prep : bar_full) + 8 * st;
                     const bool mine = t >= t_from && t <= last && (!it.alt || ((t - t_from) & 1) == 0);
                     t0 = global_ns();
                     bool taken = false;
@@ -967,25 +972,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                                    (k == 0 || mbar_test(bar_sfree + 8 * s, (k - 1) & 1)) &&
                                    (t != t_from || mbar_test(bar_qfull, j & 1))) {
                             fence_after();
-                            const uint64_t kd = desc_sw128(smem_u32(smem + L::kKv + st * L::kStageBytes));
+                            const uint64_t kd = desc_sw128(smem_u32(smem + L::kKv) + st * L::kStageBytes);
 #pragma unroll
                             for (int kk = 0; kk < kD / 16; ++kk)
                                 mma_ss(tmem + col_s(s), qd + ((kk * 32) >> 4), kd + ((kk * 32) >> 4), kIdescQK,
                                        kk > 0 ? 1u : 0u);
                             mma_commit(bar_sfull + 8 * s);
                             if (t == last) mma_commit(bar_qempty);
-                            st_b = st;
-                            x_b = x;
+                            at_b = static_cast<uint32_t>(st) | ph << 8;
                             item_b = t == t_from ? items : 0;
                             if (k == kp) {
-                                st_a = st_b;
-                                x_a = x_b;
+                                at_a = at_b;
                                 item_a = item_b;
                             }
                             ++k;
                             taken = true;
                         }
                         if (!taken) alive = patient();
+                    }
+                    if (++st == L::kStages) {
+                        st = 0;
+                        ph ^= 1;
                     }
                 }
                 if (last < 0) {
