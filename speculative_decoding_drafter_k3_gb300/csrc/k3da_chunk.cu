@@ -384,8 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ ChunkParams p) {
     using L = Smem<QUANT>;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem =
-        reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // 1 KB aligned, and still known to be shared memory
     Plan *pl = reinterpret_cast<Plan *>(smem + L::kPlan);
     Records *recs = reinterpret_cast<Records *>(smem + L::kRec);
     float2 *xch = reinterpret_cast<float2 *>(smem + L::kXch);
@@ -474,7 +473,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int t_end = min(it.t1, (slot_keys + kTile - 1) / kTile);
             float m = -INFINITY, l = 0.f;
             int mine = 0;
-            for (int t = it.from(s); t < t_end; t += it.step()) {
+            const int t_step = it.step();
+            for (int t = it.from(s); t < t_end; t += t_step) {
                 if (!mbar_wait(bar_sfull + 8 * s, k & 1, abort_flag, p.status)) {
                     alive = false;
                     break;
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_sfree + 8 * s);
-                unsigned long long sum[2] = {0ull, 0ull};
+                unsigned long long sum[4] = {0ull, 0ull, 0ull, 0ull};
                 const int lim = sees - t * kTile;
                 if ((t + 1) * static_cast<long long>(kTile) > least) {
 #pragma unroll
@@ -531,14 +531,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const unsigned long long sl2 = pack_f32x2(p.scale_log2, p.scale_log2);
                 const unsigned long long nm2 = pack_f32x2(-m_eff, -m_eff);
                 // P of 32 keys from column j on, 16 columns of bf16 pairs.
+                // In stages over the 32, in place: every stage's operations
+                // are independent, and none needs registers of its own.
                 auto weights = [&](int j, uint32_t *pk) {
+                    unsigned long long e[16];
+#pragma unroll
+                    for (int q = 0; q < 16; ++q)
+                        e[q] = fma_f32x2(pack_f32x2(__uint_as_float(x[j + 2 * q]), __uint_as_float(x[j + 2 * q + 1])), sl2, nm2);
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) e[q] = exp2_f32x2(e[q]);
 #pragma unroll
                     for (int q = 0; q < 16; ++q) {
-                        const float2 e = unpack_f32x2(fma_f32x2(
-                            pack_f32x2(__uint_as_float(x[j + 2 * q]), __uint_as_float(x[j + 2 * q + 1])), sl2, nm2));
-                        const float p0 = exp2_approx(e.x), p1 = exp2_approx(e.y);
-                        sum[q & 1] = add_f32x2(sum[q & 1], pack_f32x2(p0, p1));
-                        pk[q] = pack2(p0, p1);
+                        const float2 w = unpack_f32x2(e[q]);
+                        pk[q] = pack2(w.x, w.y);
+                        sum[q & 3] = add_f32x2(sum[q & 3], e[q]);
                     }
                 };
                 uint32_t pk0[16], pk1[16];
@@ -570,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_st16(tmem + lanes + col_p(s) + 32, pk0);
                 weights(96, pk1);
                 tmem_st16(tmem + lanes + col_p(s) + 48, pk1);
-                const float2 tot = unpack_f32x2(add_f32x2(sum[0], sum[1]));
+                const float2 tot = unpack_f32x2(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])));
                 l = l * f + (tot.x + tot.y);
                 tmem_wait_st();
                 fence_before();
@@ -711,42 +717,51 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 if (QUANT) {
-                    // Four threads a row, 16 codes each.
-#pragma unroll 2
-                    for (int e = 0; e < 8; ++e) {
-                        const bool is_v = e >= 4;
-                        const int c = (e & 3) * 128 + tid, row = c >> 2, quarter = c & 3;
-                        const uint4 w = *reinterpret_cast<const uint4 *>(raw + (is_v ? kTile * kD : 0) + c * 16);
-                        const uint32_t b = raw[2 * kTile * kD + (is_v ? kTile : 0) + row];
-                        const int key = t * kTile + row;
-                        // 2^120 times the scale, in two factors where it
-                        // passes bf16's range (rows above 448 * 2^7).
-                        const uint32_t e1 = b <= 134u ? b + 120u : 254u;
-                        const uint32_t mul = e1 << 7 | e1 << 23;
-                        uint4 o[2];
-                        uint32_t *ov = reinterpret_cast<uint32_t *>(o);
-                        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+                    // Four threads a row, 16 codes each: K's four rows of
+                    // the thread, then V's, loads first.
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            ov[2 * q] = mul_bf16x2(widen2(__byte_perm(in[q], 0, 0x1404)), mul);
-                            ov[2 * q + 1] = mul_bf16x2(widen2(__byte_perm(in[q], 0, 0x3424)), mul);
+                    for (int is_v = 0; is_v < 2; ++is_v) {
+                        uint4 w[4];
+                        uint32_t b[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int c = e * 128 + tid;
+                            w[e] = *reinterpret_cast<const uint4 *>(raw + is_v * kTile * kD + c * 16);
+                            b[e] = raw[2 * kTile * kD + is_v * kTile + (c >> 2)];
                         }
-                        if (b > 134u) {
-                            const uint32_t mul2 = (b - 7u) << 7 | (b - 7u) << 23;
 #pragma unroll
-                            for (int q = 0; q < 8; ++q) ov[q] = b == 255u ? 0x7fff7fffu : mul_bf16x2(ov[q], mul2);
-                        }
-                        if (is_v && (key >= it.limit || (b == 255u && key >= least))) {
-                            if (key < it.limit) {
+                        for (int e = 0; e < 4; ++e) {
+                            const int row = (e * 128 + tid) >> 2, quarter = tid & 3;
+                            // 2^120 times the scale, in two factors where it
+                            // passes bf16's range (rows above 448 * 2^7).
+                            const uint32_t e1 = b[e] <= 134u ? b[e] + 120u : 254u;
+                            const uint32_t mul = e1 << 7 | e1 << 23;
+                            const uint32_t in[4] = {w[e].x, w[e].y, w[e].z, w[e].w};
+                            uint32_t o[8];
 #pragma unroll
-                                for (int d = 0; d < 16; ++d) atomicMin(&rec->first[2][quarter * 16 + d], tag | (key - least));
-                                rec->piece = piece;
+                            for (int q = 0; q < 4; ++q) {
+                                o[2 * q] = mul_bf16x2(widen2(__byte_perm(in[q], 0, 0x1404)), mul);
+                                o[2 * q + 1] = mul_bf16x2(widen2(__byte_perm(in[q], 0, 0x3424)), mul);
                             }
-                            o[0] = o[1] = make_uint4(0, 0, 0, 0);
+                            if (b[e] > 134u) {
+                                const uint32_t mul2 = (b[e] - 7u) << 7 | (b[e] - 7u) << 23;
+#pragma unroll
+                                for (int q = 0; q < 8; ++q) o[q] = b[e] == 255u ? 0x7fff7fffu : mul_bf16x2(o[q], mul2);
+                            }
+                            const int key = t * kTile + row;
+                            if (is_v && (key >= it.limit || (b[e] == 255u && key >= least))) {
+                                if (key < it.limit) {
+                                    for (int d = 0; d < 16; ++d)
+                                        atomicMin(&rec->first[2][quarter * 16 + d], tag | (key - least));
+                                    rec->piece = piece;
+                                }
+#pragma unroll
+                                for (int q = 0; q < 8; ++q) o[q] = 0u;
+                            }
+                            uint8_t *dst = is_v ? vt : kt;
+                            *reinterpret_cast<uint4 *>(dst + swz(row, 2 * quarter)) = make_uint4(o[0], o[1], o[2], o[3]);
+                            *reinterpret_cast<uint4 *>(dst + swz(row, 2 * quarter + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
                         }
-                        uint8_t *dst = is_v ? vt : kt;
-                        *reinterpret_cast<uint4 *>(dst + swz(row, 2 * quarter)) = o[0];
-                        *reinterpret_cast<uint4 *>(dst + swz(row, 2 * quarter + 1)) = o[1];
                     }
                     fence_proxy_async();
                 } else if ((t + 1) * static_cast<long long>(kTile) > least) {

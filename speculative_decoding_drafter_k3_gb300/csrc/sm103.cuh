@@ -22,14 +22,16 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
 
+// Waits for up to about 1 ms, suspended: a warp that spins instead takes the
+// issue slots of the warps it waits for.
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(bar), "r"(parity)
+        : "r"(bar), "r"(parity), "r"(1000000u)
         : "memory");
     return ok != 0;
 }
@@ -64,7 +66,8 @@ __device__ __forceinline__ unsigned long long global_ns() {
 // Gives up when another warp of the CTA has (abort flag) or after
 // kWaitLimitNs, raising the flag and the TIMEOUT status bit.  The caller then
 // leaves its loop, so that every warp reaches the CTA's last barrier.
-__device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag, int32_t *status) {
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, int32_t *status) {
+    if (mbar_try_wait(bar, parity)) return true;
     const unsigned long long t0 = global_ns();
     while (true) {
         if (mbar_try_wait(bar, parity)) return true;
@@ -75,11 +78,6 @@ __device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, vo
             return false;
         }
     }
-}
-
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, int32_t *status) {
-    if (mbar_try_wait(bar, parity)) return true;
-    return mbar_wait_slow(bar, parity, abort_flag, status);
 }
 
 // --------------------------------------------------------------------- TMA --
@@ -229,6 +227,16 @@ __device__ __forceinline__ unsigned long long add_f32x2(unsigned long long a, un
     unsigned long long d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
+}
+
+// 2^x of both halves.  Volatile, so that a row of them stays together and
+// their latencies overlap.
+__device__ __forceinline__ unsigned long long exp2_f32x2(unsigned long long v) {
+    const float2 x = unpack_f32x2(v);
+    float a, b;
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(x.x));
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(x.y));
+    return pack_f32x2(a, b);
 }
 
 // max(a, b, c) in one instruction; NaN operands are dropped as by fmaxf.
