@@ -20,23 +20,29 @@
 //
 // Both slots of an item read the same K/V tiles (shared).  An item whose
 // tokens fit one slot (a decode step, a draft block, a chunk's tail) gives
-// its tiles to the two slots in turn (alternate), both with the same rows,
-// and the two halves are merged at the end: the softmax of one tile overlaps
-// the products and loads of the next either way.
+// its tiles to the two slots in turn (alternate), both with the same rows.
+// Either way a slot's tile is worked on by two streams, one for each page:
+// four streams, each with 64 columns of S, a softmax warpgroup (one thread a
+// row, its own running maximum and sum), an O accumulator and a thread that
+// issues its products.  A stream alone is a chain: Q K^T, softmax, P V, each
+// waiting for the last; four of them side by side keep the tensor cores, the
+// exponential units and the loads busy, and none needs to know of the others
+// until an item ends and one warpgroup merges what belongs to the same rows.
+// Two streams of 128 columns each, with S and P apart so that Q K^T ran
+// ahead, were slower: two softmax warps a scheduler could not hide their own
+// latencies, and their unrolled code did not fit the instruction cache.
 //
-// Roles of a CTA's 16 warps: two softmax warpgroups (a slot each, one thread
-// a row), one warpgroup that prepares tiles (below), a K/V loader, one MMA
-// issuer for each slot, and a Q loader.  S (128 x 128 fp32) and P (bf16) have
-// tensor memory of their own, so that a slot's next Q K^T runs while its
-// softmax works on the last: S is free as soon as it is in registers.
+// The other warps: a scheduler that cuts the CTA's slice into pieces and
+// loads Q, a K/V loader, the four product issuers, and a few that prepare
+// tiles (below).
 //
-// The preparing warpgroup zeroes the V rows past an item's last key (stale
-// slots may hold anything, and 0 * NaN is NaN), and where only some of an
-// item's rows see a key, it takes infinities and NaN out of that V row and
-// records the first key that had one for each dim: what a row sees is always
-// a prefix of the keys, so the epilogue puts them back for just the rows that
-// see them.  Quantised tiles it widens to bf16 on the way (the scale is a
-// power of two, so the bf16 are exact); both cache types share all the rest.
+// The preparing warps zero the V rows past an item's last key (stale slots
+// may hold anything, and 0 * NaN is NaN), and where only some of an item's
+// rows see a key, they take infinities and NaN out of that V row and record
+// the first key that had one for each dim: what a row sees is always a prefix
+// of the keys, so the epilogue puts them back for just the rows that see
+// them.  Quantised tiles they widen to bf16 on the way (the scale is a power
+// of two, so the bf16 are exact); both cache types share all the rest.
 //
 // Rounding: scores, softmax statistics and O are fp32 throughout (partials
 // too); P is rounded to bf16 once for the P V product, the output once.
@@ -59,24 +65,30 @@ namespace {
 using namespace k3da_cache;
 using namespace sm103;
 
-constexpr int kThreads = 512;
 constexpr int kCtas = 152;         // slices of the line at most: one CTA an SM
 constexpr int kTile = 128;         // keys of a tile: two pages
 constexpr int kSlotRows = 128;     // query rows of a slot
 constexpr int kOverhead = 128;     // an item's fixed cost, in keys
 constexpr int kMinSlice = 256;     // shortest slice, in keys
+constexpr int kStreams = 4;        // stream u: slot u / 2, page u % 2 of its tiles
+constexpr int kRing = 4;           // pieces published ahead
 constexpr int kRecords = 8;        // pieces whose non-finite records are alive at once
 constexpr float kRescale = 8.0f;   // log2 units the running maximum may lag behind
-// Warps.
-constexpr int kPrepWarp = 8, kLoadWarp = 12, kMmaWarp = 13, kQWarp = 15;
-// Registers a thread: 2 x 128 x 192 + 2 x 128 x 64 = 512 x 128.
-constexpr int kSoftmaxRegs = 192, kOtherRegs = 64;
-// Tensor memory columns of slot s.
-__device__ __forceinline__ uint32_t col_s(int s) { return 128u * s; }
-__device__ __forceinline__ uint32_t col_p(int s) { return 256u + 64u * s; }
-__device__ __forceinline__ uint32_t col_o(int s) { return 384u + 64u * s; }
+// Warps: four softmax warpgroups, then single warps, then the preparing ones
+// (widening codes takes more of them than looking tiles over).
+constexpr int kLoadWarp = 16, kSchedWarp = 17, kMmaWarp = 18, kPrepWarp = 22;
+__host__ __device__ constexpr int prep_warps(bool quant) { return quant ? 6 : 2; }
+__host__ __device__ constexpr int threads_of(bool quant) { return 32 * (kPrepWarp + prep_warps(quant)); }
+// Registers a thread.  bf16: 768 threads launched with 80, 512 x 88 + 256 x
+// 64; e4m3: 896 launched with 72, 512 x 88 + 384 x 48.
+__host__ __device__ constexpr int softmax_regs(bool) { return 88; }
+__host__ __device__ constexpr int other_regs(bool quant) { return quant ? 48 : 64; }
+// Tensor memory columns of stream u.  P (32 columns of bf16 pairs) lies over
+// the first half of its S.
+__device__ __forceinline__ uint32_t col_s(int u) { return 64u * u; }
+__device__ __forceinline__ uint32_t col_o(int u) { return 256u + 64u * u; }
 constexpr uint32_t kTmemCols = 512u;
-constexpr uint32_t kIdescQK = idesc_f16(128, kTile, false);
+constexpr uint32_t kIdescQK = idesc_f16(128, kP, false);
 constexpr uint32_t kIdescPV = idesc_f16(128, kD, true);
 
 struct ChunkParams {
@@ -122,7 +134,7 @@ struct Plan {
     int32_t row[kMaxRequests];           // its first row
     int32_t n[kMaxRequests];             // its new tokens
     int32_t ctx[kMaxRequests];           // its cached tokens
-    long long warp_sum[kThreads / 32];
+    long long warp_sum[kMaxRequests / 64];
 };
 
 // Length of the first `pairs` items of one head: each sees `base` keys (and,
@@ -132,16 +144,17 @@ __device__ __forceinline__ long long line_of(const ChunkParams &p, long long bas
     return pairs * (base + kOverhead) + own;
 }
 
-// All threads; syncs.  Lengths the kernel cannot use are clamped and flagged.
+// All threads; syncs.  The first 512 take two requests each.  Lengths the
+// kernel cannot use are clamped and flagged.
 __device__ void build_plan(const ChunkParams &p, Plan *pl, bool report) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const bool mine = t < kMaxRequests / 2;
     const int cap = p.page_stride * kP;
-    static_assert(kMaxRequests == 2 * kThreads, "two requests a thread");
     long long cost[2] = {0, 0};
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const int r = 2 * t + k;
-        if (r >= p.R) continue;
+        if (!mine || r >= p.R) continue;
         const int a = __ldg(p.cu_seqlens + r), b = __ldg(p.cu_seqlens + r + 1), c = __ldg(p.ctx_lens + r);
         const int begin = min(max(a, 0), p.T), end = min(max(b, begin), p.T), n = end - begin;
         const int ctx = min(max(c, 0), cap);
@@ -160,33 +173,39 @@ __device__ void build_plan(const ChunkParams &p, Plan *pl, bool report) {
         const long long up = __shfl_up_sync(kFull, sum, off);
         if (lane >= off) sum += up;
     }
-    if (lane == 31) pl->warp_sum[warp] = sum;
+    if (mine && lane == 31) pl->warp_sum[warp] = sum;
     __syncthreads();
-    long long before = 0;
-    for (int w = 0; w < warp; ++w) before += pl->warp_sum[w];
-    const long long begin = before + sum - cost[0] - cost[1];
-    if (2 * t <= p.R) pl->prefix[2 * t] = begin;
-    if (2 * t + 1 <= p.R) pl->prefix[2 * t + 1] = begin + cost[0];
-    if (t == kThreads - 1 && p.R == kMaxRequests) pl->prefix[kMaxRequests] = begin + cost[0] + cost[1];
+    if (mine) {
+        long long before = 0;
+        for (int w = 0; w < warp; ++w) before += pl->warp_sum[w];
+        const long long begin = before + sum - cost[0] - cost[1];
+        if (2 * t <= p.R) pl->prefix[2 * t] = begin;
+        if (2 * t + 1 <= p.R) pl->prefix[2 * t + 1] = begin + cost[0];
+        if (2 * t + 2 == kMaxRequests && p.R == kMaxRequests) pl->prefix[kMaxRequests] = begin + cost[0] + cost[1];
+    }
     __syncthreads();
 }
 
 // A piece: the tiles [t0, t1) of one item that fall into this CTA's slice.
 struct Piece {
-    long long start, length;  // the item on the line
-    int r, h;
-    int tok0;    // its first token in the chunk
+    int h;
+    int tok0;    // the item's first token in the chunk
     int tokens;
-    int ctx, n;  // its request's
-    int row;     // its first row
+    int ctx, n, r;
+    int row;     // its first row; -1: no more pieces
     int limit;   // keys its last row sees
+    int keys0;   // ... the last row of slot 0
     int nt;      // tiles of the item
     int t0, t1;
-    bool alt;    // one slot's worth of rows: the slots take the tiles in turn
-    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == nt; }
-    // Tiles that slot s works on: [from, to) in steps of `step`.
-    __device__ __forceinline__ int from(int s) const { return alt ? t0 + s : t0; }
+    int alt;     // one slot's worth of rows: the slots take the tiles in turn
+    int seq;     // number of the piece among those with tiles
+    // The tiles of stream u: from, from + step, ... below end.
+    __device__ __forceinline__ int from(int u) const { return alt ? t0 + (u >> 1) : t0; }
     __device__ __forceinline__ int step() const { return alt ? 2 : 1; }
+    __device__ __forceinline__ int end(int u) const {
+        const int keys = (alt || u >= 2 ? limit : keys0) - kP * (u & 1);
+        return keys <= 0 ? 0 : min(t1, (keys - 1) / kTile + 1);
+    }
 };
 
 // Keys that the chunk's token i sees.
@@ -198,12 +217,12 @@ __device__ __forceinline__ int keys_seen(const ChunkParams &p, int ctx, int n, i
     return c < cap ? static_cast<int>(c) : cap;
 }
 
-// The CTA's pieces, in order.  Every warp walks them for itself, with the
-// state in shared memory: the softmax's registers are for scores.
+// The CTA's pieces, in order (the scheduler's).
 struct Walk {
     long long lo, hi;         // the slice
     long long total, slices;
     long long at;             // where the next item begins
+    long long start, length;  // the last item
     int r, h, pair;
 
     // Start of slice c: ceil(c * total / slices), without a wide product.
@@ -267,13 +286,14 @@ struct Walk {
             it.alt = it.tokens <= p.tpt;
             it.limit = keys_seen(p, it.ctx, it.n, it.tok0 + it.tokens - 1);
             it.nt = static_cast<int>((static_cast<long long>(it.limit) + kTile - 1) / kTile);
-            it.start = at;
+            it.keys0 = keys_seen(p, it.ctx, it.n, it.tok0 + min(p.tpt, it.tokens) - 1);
+            start = at;
             const int count = pairs(p, pl, r);
             const long long keys = base(p, pl, r);
-            it.length = line_of(p, keys, pair + 1) - line_of(p, keys, pair);
+            length = line_of(p, keys, pair + 1) - line_of(p, keys, pair);
             it.t0 = lo <= at ? 0 : tile_at(lo - at, it.nt);
-            it.t1 = hi >= at + it.length ? it.nt : tile_at(hi - at, it.nt);
-            at += it.length;
+            it.t1 = hi >= at + length ? it.nt : tile_at(hi - at, it.nt);
+            at += length;
             if (++pair == count) {
                 pair = 0;
                 if (++h == p.Hkv) {
@@ -282,7 +302,7 @@ struct Walk {
                     while (r < p.R && pl->n[r] == 0);
                 }
             }
-            if (it.t0 < it.t1 || (it.nt == 0 && it.start >= lo)) return true;
+            if (it.t0 < it.t1 || (it.nt == 0 && start >= lo)) return true;
         }
         return false;
     }
@@ -299,21 +319,6 @@ struct Walk {
     }
 };
 
-struct WarpState {
-    Walk walk;
-    Piece it;
-    int more;
-    int pad;
-};
-
-// The warp's next piece (in ws->it), false after the last.
-__device__ __forceinline__ bool next_piece(const ChunkParams &p, const Plan *pl, WarpState *ws) {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) ws->more = ws->walk.next(p, pl, ws->it);
-    __syncwarp();
-    return *const_cast<volatile int *>(&ws->more) != 0;
-}
-
 // ----------------------------------------------------------- shared memory --
 
 // What was taken out of a piece's V: for +inf, -inf and NaN and each dim,
@@ -328,24 +333,27 @@ struct Records {
 
 template <bool QUANT>
 struct Smem {
-    static constexpr int kStages = QUANT ? 3 : 5;  // bf16 K/V tiles
+    static constexpr int kStages = QUANT ? 2 : 4;  // bf16 K/V tiles
     static constexpr int kRaw = QUANT ? 4 : 0;     // quantised tiles: K codes, V codes, K scales, V scales
     static constexpr int kRawBytes = 2 * kTile * kD + 2 * kTile;
     static constexpr int kStageBytes = 2 * kTile * kD * 2;
     static constexpr int kVOff = kTile * kD * 2;
+    static constexpr int kQBytes = 2 * kSlotRows * kD * 2;  // of a piece; two pieces' Q
     static constexpr int kQ = 0;
-    static constexpr int kKv = kQ + 2 * kSlotRows * kD * 2;
+    static constexpr int kKv = kQ + 2 * kQBytes;
     static constexpr int kRawOff = kKv + kStages * kStageBytes;
     static constexpr int kPlan = kRawOff + kRaw * kRawBytes;
     static constexpr int kRec = kPlan + static_cast<int>(sizeof(Plan));
     static constexpr int kXch = kRec + kRecords * static_cast<int>(sizeof(Records));
-    static constexpr int kWarps = kXch + kSlotRows * 8;
-    static constexpr int kBars = kWarps + kThreads / 32 * static_cast<int>(sizeof(WarpState));
-    static constexpr int kNumBars = 3 * kStages + 2 * kRaw + 2 + 5 * 2 + 2;
+    static constexpr int kPieces = kXch + kStreams * kSlotRows * 8;
+    static constexpr int kBars = kPieces + kRing * static_cast<int>(sizeof(Piece));
+    static constexpr int kNumBars = 3 * kStages + 2 * kRaw + 2 * kRing + 4 + 5 * kStreams + 2;
     static constexpr int kTail = kBars + kNumBars * 8;  // TMEM address, abort flag
     static constexpr int kBytes = kTail + 16 + 1024;
     static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
-    static_assert(kKv % 1024 == 0 && kRawOff % 128 == 0 && kPlan % 16 == 0 && kRec % 8 == 0 && kBars % 8 == 0, "alignment");
+    static_assert(kKv % 1024 == 0 && kRawOff % 128 == 0 && kPlan % 16 == 0 && kRec % 8 == 0 && kXch % 8 == 0 &&
+                      kBars % 8 == 0,
+                  "alignment");
 };
 
 // Byte of 16-byte chunk `chunk` of a 128-byte row in a 128B-swizzled tile.
@@ -379,55 +387,68 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 }
 
 template <bool QUANT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads_of(QUANT), 1)
     k3da_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap q_map,
                       const __grid_constant__ ChunkParams p) {
     using L = Smem<QUANT>;
+    constexpr int kThreads = threads_of(QUANT), kPrepWarps = prep_warps(QUANT);
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // 1 KB aligned, and still known to be shared memory
     Plan *pl = reinterpret_cast<Plan *>(smem + L::kPlan);
     Records *recs = reinterpret_cast<Records *>(smem + L::kRec);
-    float2 *xch = reinterpret_cast<float2 *>(smem + L::kXch);
+    float2 *xch = reinterpret_cast<float2 *>(smem + L::kXch);  // [kStreams][128] (m, l)
+    Piece *pieces = reinterpret_cast<Piece *>(smem + L::kPieces);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kTail + 8);
     uint32_t *taddr_slot = reinterpret_cast<uint32_t *>(smem + L::kTail);
     const uint32_t bars = smem_u32(smem + L::kBars);
-    const uint32_t bar_full = bars;                        // [kStages] bf16 tile loaded (QUANT: unused)
-    const uint32_t bar_prep = bar_full + 8 * L::kStages;   // [kStages] tile prepared
-    const uint32_t bar_empty = bar_prep + 8 * L::kStages;  // [kStages] both slots are done with the tile
-    const uint32_t bar_rfull = bar_empty + 8 * L::kStages; // [kRaw] quantised tile loaded
-    const uint32_t bar_rempty = bar_rfull + 8 * L::kRaw;   // [kRaw] ... and widened
-    const uint32_t bar_qfull = bar_rempty + 8 * L::kRaw, bar_qempty = bar_qfull + 8;
-    const uint32_t bar_sfull = bar_qempty + 8;   // [2] S written
-    const uint32_t bar_sfree = bar_sfull + 16;   // [2] S read
-    const uint32_t bar_pfull = bar_sfree + 16;   // [2] P written
-    const uint32_t bar_pvdone = bar_pfull + 16;  // [2] P V complete
-    const uint32_t bar_ofree = bar_pvdone + 16;  // [2] an item's O read
-    const uint32_t bar_xch = bar_ofree + 16;     // slot 1's half of an alternate item is ready
-    const uint32_t bar_done = bar_xch + 8;       // both issuers' products are complete
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t bar_full = bars;                         // [kStages] bf16 tile loaded (QUANT: unused)
+    const uint32_t bar_prep = bar_full + 8 * L::kStages;    // [kStages] tile prepared
+    const uint32_t bar_empty = bar_prep + 8 * L::kStages;   // [kStages] the streams are done with the tile
+    const uint32_t bar_rfull = bar_empty + 8 * L::kStages;  // [kRaw] quantised tile loaded
+    const uint32_t bar_rempty = bar_rfull + 8 * L::kRaw;    // [kRaw] ... and widened
+    const uint32_t bar_piece = bar_rempty + 8 * L::kRaw;    // [kRing] piece published
+    const uint32_t bar_pdone = bar_piece + 8 * kRing;       // [kRing] ... and read by everybody
+    const uint32_t bar_qfull = bar_pdone + 8 * kRing;       // [2] a piece's Q loaded
+    const uint32_t bar_qempty = bar_qfull + 16;             // [2] ... and read
+    const uint32_t bar_sfull = bar_qempty + 16;             // [kStreams] S written
+    const uint32_t bar_pfull = bar_sfull + 8 * kStreams;    // [kStreams] P written
+    const uint32_t bar_pvdone = bar_pfull + 8 * kStreams;   // [kStreams] P V complete
+    const uint32_t bar_ofree = bar_pvdone + 8 * kStreams;   // [kStreams] an item's O read
+    // [kStreams + 1] a stream's part of an item is ready: u where all meet in
+    // stream 0, u + u / 2 in a shared item (stream 3 reports to either 0 or 2,
+    // and each counts the phases of a barrier of its own).
+    const uint32_t bar_xch = bar_ofree + 8 * kStreams;
+    const uint32_t bar_done = bar_xch + 8 * (kStreams + 1); // every issuer's products are complete
+    const int warp = __shfl_sync(kFull, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         *abort_flag = 0;
         for (int s = 0; s < L::kStages; ++s) {
             mbar_init(bar_full + 8 * s, 1);
-            mbar_init(bar_prep + 8 * s, 4);
-            mbar_init(bar_empty + 8 * s, 2);
+            mbar_init(bar_prep + 8 * s, kPrepWarps);
+            mbar_init(bar_empty + 8 * s, kStreams);
         }
         for (int s = 0; s < L::kRaw; ++s) {
             mbar_init(bar_rfull + 8 * s, 1);
-            mbar_init(bar_rempty + 8 * s, 4);
+            mbar_init(bar_rempty + 8 * s, kPrepWarps);
         }
-        mbar_init(bar_qfull, 1);
-        mbar_init(bar_qempty, 2);
+        for (int s = 0; s < kRing; ++s) {
+            mbar_init(bar_piece + 8 * s, 1);
+            mbar_init(bar_pdone + 8 * s, kThreads / 32 - 1);  // every warp but the scheduler
+        }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(bar_sfull + 8 * s, 1);
-            mbar_init(bar_sfree + 8 * s, 4);
-            mbar_init(bar_pfull + 8 * s, 4);
-            mbar_init(bar_pvdone + 8 * s, 1);
-            mbar_init(bar_ofree + 8 * s, 4);
+            mbar_init(bar_qfull + 8 * s, 1);
+            mbar_init(bar_qempty + 8 * s, kStreams);
         }
-        mbar_init(bar_xch, 4);
-        mbar_init(bar_done, 2);
+        for (int u = 0; u < kStreams; ++u) {
+            mbar_init(bar_sfull + 8 * u, 1);
+            mbar_init(bar_pfull + 8 * u, 4);
+            mbar_init(bar_pvdone + 8 * u, 1);
+            mbar_init(bar_ofree + 8 * u, 4);
+            mbar_init(bar_xch + 8 * u, 4);
+        }
+        mbar_init(bar_xch + 8 * kStreams, 4);
+        mbar_init(bar_done, kStreams);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     for (int e = threadIdx.x; e < kRecords; e += kThreads) recs[e].piece = -1;
@@ -445,367 +466,265 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_after();
     const uint32_t tmem = *taddr_slot;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    WarpState *ws = reinterpret_cast<WarpState *>(smem + L::kWarps) + warp;
-    const Piece &it = ws->it;
-    if (lane == 0) ws->walk.begin(p, pl, blockIdx.x);
     bool alive = true;
+    if (warp < 4 * kStreams) regs_raise<softmax_regs(QUANT)>();
+    else regs_lower<other_regs(QUANT)>();
 
-    if (warp < kPrepWarp) regs_raise<kSoftmaxRegs>();
-    else regs_lower<kOtherRegs>();
-    if (warp < kPrepWarp) {
+    if (warp == kSchedWarp) {
+        // ---------------------------------------------- pieces and their Q --
+        if (lane == 0) {
+            Walk walk;
+            walk.begin(p, pl, blockIdx.x);
+            Cut cut = {};
+            const uint32_t box = static_cast<uint32_t>(p.G) * p.tpt * 128;
+            int seq = 0;
+            for (int n = 0; alive; ++n) {
+                const int slot = n % kRing;
+                if (!mbar_wait(bar_pdone + 8 * slot, ((n / kRing) & 1) ^ 1, abort_flag, p.status)) {
+                    alive = false;
+                    break;
+                }
+                Piece &it = pieces[slot];
+                const bool more = walk.next(p, pl, it);
+                if (!more) it.row = -1;
+                it.seq = seq;
+                const bool tiles = more && it.t0 < it.t1;
+                const int alt = it.alt, h = it.h, row = it.row;
+                if (more && it.t0 > 0) cut.has[0] = 1;
+                if (tiles && it.t0 == 0 && it.t1 < it.nt) {
+                    cut.has[1] = 1;
+                    cut.row = row;
+                    cut.tokens = it.tokens;
+                    cut.head = h;
+                    cut.last = walk.slice_of(walk.start + walk.length - 1);
+                }
+                mbar_arrive(bar_piece + 8 * slot);
+                if (!more) break;
+                if (!tiles) continue;
+                const int b = seq & 1;
+                if (!mbar_wait(bar_qempty + 8 * b, ((seq >> 1) & 1) ^ 1, abort_flag, p.status)) {
+                    alive = false;
+                    break;
+                }
+                const uint32_t dst = smem_u32(smem + L::kQ) + b * L::kQBytes;
+                mbar_arrive_expect_tx(bar_qfull + 8 * b, alt ? box : 2 * box);
+                tma_load_3d(dst, &q_map, 0, h * p.G, row, bar_qfull + 8 * b);
+                if (!alt) tma_load_3d(dst + kSlotRows * 128, &q_map, 0, h * p.G, row + p.tpt, bar_qfull + 8 * b);
+                ++seq;
+            }
+            p.cuts[blockIdx.x] = cut;
+            // Loads in flight land before the CTA leaves (a wait gave up).
+            if (!alive) {
+                for (int j = seq > 2 ? seq - 2 : 0; j < seq; ++j) {
+                    const unsigned long long t0 = global_ns();
+                    while (!mbar_try_wait(bar_qfull + 8 * (j & 1), (j >> 1) & 1) && global_ns() - t0 < kWaitLimitNs) {
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp < 4 * kStreams) {
         // ------------------------------------------------------ softmax --
-        const int s = warp >> 2;
+        const int u = warp >> 2, s = u >> 1;
         const int rho = threadIdx.x & (kSlotRows - 1);  // this thread's row of the slot
-        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
         const int ti = rho / p.G, gi = rho - ti * p.G;
-        int k = 0;       // tiles of this slot so far
-        int pieces = 0;  // pieces with tiles so far
-        int merges = 0;  // alternate pieces with tiles for both slots so far
-        while (alive && next_piece(p, pl, ws)) {
-            const int token = (it.alt ? 0 : s * p.tpt) + ti;  // in the item
+        int k = 0;           // tiles of this stream so far
+        uint32_t merges = 0;  // bit x: parity of the phases of bar_xch[x] waited for
+        for (int n = 0; alive; ++n) {
+            const Piece &it = pieces[n % kRing];
+            if (!mbar_wait(bar_piece + 8 * (n % kRing), (n / kRing) & 1, abort_flag, p.status)) break;
+            if (it.row < 0) break;
+            const int alt = it.alt;
+            const int token = (alt ? 0 : s * p.tpt) + ti;  // in the item
             const bool row_valid = ti < p.tpt && token < it.tokens;
             const bool warp_valid = __any_sync(kFull, row_valid);
             const int sees = row_valid ? keys_seen(p, it.ctx, it.n, it.tok0 + token) : 0;
-            const int least = keys_seen(p, it.ctx, it.n, it.tok0 + (it.alt ? 0 : s * p.tpt));  // ... of the slot's rows
-            // The slot's own last tile: in a shared item slot 0 sees fewer keys.
-            const int slot_keys =
-                it.alt || s == 1 ? it.limit : keys_seen(p, it.ctx, it.n, it.tok0 + p.tpt - 1);
-            const int t_end = min(it.t1, (slot_keys + kTile - 1) / kTile);
+            const int least = keys_seen(p, it.ctx, it.n, it.tok0 + (alt ? 0 : s * p.tpt));  // ... of the slot's rows
+            const int from = it.from(u), t_end = it.end(u), step = it.step();
             float m = -INFINITY, l = 0.f;
-            int mine = 0;
-            const int t_step = it.step();
-            for (int t = it.from(s); t < t_end; t += t_step) {
-                if (!mbar_wait(bar_sfull + 8 * s, k & 1, abort_flag, p.status)) {
+            for (int t = from; t < t_end; t += step) {
+                if (!mbar_wait(bar_sfull + 8 * u, k & 1, abort_flag, p.status)) {
                     alive = false;
                     break;
                 }
                 fence_after();
-                if (!warp_valid) {
-                    // No row of this warp's: it only keeps step.
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar_sfree + 8 * s);
-                    if (k > 0 && !mbar_wait(bar_pvdone + 8 * s, (k - 1) & 1, abort_flag, p.status)) {
-                        alive = false;
-                        break;
-                    }
-                    fence_after();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar_pfull + 8 * s);
-                    ++k;
-                    ++mine;
-                    continue;
-                }
-                uint32_t x[kTile];
-#pragma unroll
-                for (int j = 0; j < kTile; j += 32) tmem_ld32(tmem + lanes + col_s(s) + j, x + j);
-                tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < kTile; j += 32) pin32(x + j);
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_sfree + 8 * s);
-                unsigned long long sum[4] = {0ull, 0ull, 0ull, 0ull};
-                const int lim = sees - t * kTile;
-                if ((t + 1) * static_cast<long long>(kTile) > least) {
-#pragma unroll
-                    for (int j = 0; j < kTile; ++j) x[j] = j < lim ? x[j] : 0xff800000u;
-                }
-                float mx[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) mx[j] = fmaxf(__uint_as_float(x[j]), __uint_as_float(x[j + 4]));
-#pragma unroll
-                for (int j = 8; j < kTile; j += 8)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        mx[q] = fmax3(mx[q], __uint_as_float(x[j + q]), __uint_as_float(x[j + 4 + q]));
-                const float rmax = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
-                // The base of the exponents follows the row's maximum only
-                // when that passes it by 2^8: P up to 256 is as exact, and O
-                // is left alone.
-                const bool need = mine > 0 && rmax > m + kRescale;
-                const float m_new = mine == 0 || need ? rmax : m;
-                const float m_eff = m_new == -INFINITY ? 0.f : m_new;  // a row that has seen nothing yet
-                const float f = need ? exp2_approx(m - m_eff) : 1.f;
-                m = m_new;
-                const unsigned long long sl2 = pack_f32x2(p.scale_log2, p.scale_log2);
-                const unsigned long long nm2 = pack_f32x2(-m_eff, -m_eff);
-                // P of 32 keys from column j on, 16 columns of bf16 pairs.
-                // In stages over the 32, in place: every stage's operations
-                // are independent, and none needs registers of its own.
-                auto weights = [&](int j, uint32_t *pk) {
-                    unsigned long long e[16];
-#pragma unroll
-                    for (int q = 0; q < 16; ++q)
-                        e[q] = fma_f32x2(pack_f32x2(__uint_as_float(x[j + 2 * q]), __uint_as_float(x[j + 2 * q + 1])), sl2, nm2);
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) e[q] = exp2_f32x2(e[q]);
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) {
-                        const float2 w = unpack_f32x2(e[q]);
-                        pk[q] = pack2(w.x, w.y);
-                        sum[q & 3] = add_f32x2(sum[q & 3], e[q]);
-                    }
-                };
-                uint32_t pk0[16], pk1[16];
-                weights(0, pk0);
-                weights(32, pk1);
-                // P's room is free, and O at rest, once the last P V is complete.
-                if (k > 0) {
-                    if (!mbar_wait(bar_pvdone + 8 * s, (k - 1) & 1, abort_flag, p.status)) {
-                        alive = false;
-                        break;
-                    }
-                    fence_after();
-                }
-                if (__any_sync(kFull, need)) {
-#pragma unroll
-                    for (int part = 0; part < 4; ++part) {
-                        uint32_t o[16];
-                        tmem_ld16(tmem + lanes + col_o(s) + 16 * part, o);
-                        tmem_wait_ld();
-                        pin16(o);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                        tmem_st16(tmem + lanes + col_o(s) + 16 * part, o);
-                    }
-                }
-                tmem_st16(tmem + lanes + col_p(s), pk0);
-                tmem_st16(tmem + lanes + col_p(s) + 16, pk1);
-                weights(64, pk0);
-                tmem_st16(tmem + lanes + col_p(s) + 32, pk0);
-                weights(96, pk1);
-                tmem_st16(tmem + lanes + col_p(s) + 48, pk1);
-                const float2 tot = unpack_f32x2(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])));
-                l = l * f + (tot.x + tot.y);
-                tmem_wait_st();
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_pfull + 8 * s);
                 ++k;
-                ++mine;
+                if (warp_valid) {
+                    const int key0 = t * kTile + kP * (u & 1);
+                    uint32_t x[kP];
+                    tmem_ld32(lanes + col_s(u), x);
+                    tmem_ld32(lanes + col_s(u) + 32, x + 32);
+                    tmem_wait_ld();
+                    pin32(x);
+                    pin32(x + 32);
+                    if (key0 + kP > least) {
+                        const int lim = sees - key0;
+#pragma unroll
+                        for (int j = 0; j < kP; ++j) x[j] = j < lim ? x[j] : 0xff800000u;
+                    }
+                    float mx[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mx[j] = fmaxf(__uint_as_float(x[j]), __uint_as_float(x[j + 4]));
+#pragma unroll
+                    for (int j = 8; j < kP; j += 8)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            mx[q] = fmax3(mx[q], __uint_as_float(x[j + q]), __uint_as_float(x[j + 4 + q]));
+                    const float rmax = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
+                    // The base of the exponents follows the row's maximum
+                    // only when that passes it by 2^8: P up to 256 is as
+                    // exact, and O is left alone.
+                    const bool first = t == from;
+                    const bool need = !first && rmax > m + kRescale;
+                    const float m_new = first || need ? rmax : m;
+                    const float m_eff = m_new == -INFINITY ? 0.f : m_new;  // a row that has seen nothing yet
+                    const float f = need ? exp2_approx(m - m_eff) : 1.f;
+                    m = m_new;
+                    if (__any_sync(kFull, need)) {
+                        // O is at rest: this S was written after the last P V.
+#pragma unroll 1
+                        for (int d0 = 0; d0 < kD; d0 += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(lanes + col_o(u) + d0, o);
+                            tmem_wait_ld();
+                            pin16(o);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                            tmem_st16(lanes + col_o(u) + d0, o);
+                        }
+                    }
+                    const unsigned long long sl2 = pack_f32x2(p.scale_log2, p.scale_log2);
+                    const unsigned long long nm2 = pack_f32x2(-m_eff, -m_eff);
+                    unsigned long long sum[2] = {0ull, 0ull};
+                    // P of 32 keys at a time, over the S just read; in stages
+                    // of independent operations.
+#pragma unroll
+                    for (int j = 0; j < kP; j += 32) {
+                        unsigned long long e[16];
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int q = 0; q < 16; ++q)
+                            e[q] = fma_f32x2(pack_f32x2(__uint_as_float(x[j + 2 * q]), __uint_as_float(x[j + 2 * q + 1])), sl2, nm2);
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) e[q] = exp2_f32x2(e[q]);
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) {
+                            const float2 w = unpack_f32x2(e[q]);
+                            pk[q] = pack2(w.x, w.y);
+                            sum[q & 1] = add_f32x2(sum[q & 1], e[q]);
+                        }
+                        tmem_st16(lanes + col_s(u) + j / 2, pk);
+                    }
+                    const float2 tot = unpack_f32x2(add_f32x2(sum[0], sum[1]));
+                    l = l * f + (tot.x + tot.y);
+                    tmem_wait_st();
+                }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_pfull + 8 * u);
             }
             if (!alive) break;
             // ------------------------------------------------- epilogue --
-            const int piece = pieces;
-            if (it.t0 < it.t1) ++pieces;
-            const bool both = it.alt && it.t1 - it.t0 > 1;  // slot 1 has tiles of an alternate item
-            if (mine > 0) {
-                if (!mbar_wait(bar_pvdone + 8 * s, (k - 1) & 1, abort_flag, p.status)) {
-                    alive = false;
-                    break;
-                }
-                fence_after();
-            }
-            if (it.alt && s == 1) {
-                // Slot 0 merges: it owns the same tensor memory lanes.
-                if (both) {
-                    xch[rho] = make_float2(m, l);
+            const bool mine = from < t_end;
+            if (mine && !mbar_wait(bar_pvdone + 8 * u, (k - 1) & 1, abort_flag, p.status)) break;
+            // The streams of the same rows meet in the first of them, whose
+            // warps own the same tensor memory lanes.
+            const int leader = alt ? 0 : u & 2;
+            if (u != leader) {
+                if (mine) {
+                    xch[u * kSlotRows + rho] = make_float2(m, l);
                     fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar_xch);
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    if (mine) mbar_arrive(bar_xch + 8 * (alt ? u : u + (u >> 1)));
+                    mbar_arrive(bar_pdone + 8 * (n % kRing));
                 }
                 continue;
             }
-            float wa = 1.f, wb = 0.f;
-            if (both) {
-                if (!mbar_wait(bar_xch, merges & 1, abort_flag, p.status)) {
+            const int others = alt ? kStreams : leader + 2;
+            float mt = m;
+            uint32_t part_of = mine ? 1u << u : 0u;  // the streams that bring something
+            for (int v = u + 1; v < others; ++v) {
+                if (it.from(v) >= it.end(v)) continue;
+                const int x = alt ? v : v + (v >> 1);
+                if (!mbar_wait(bar_xch + 8 * x, (merges >> x) & 1, abort_flag, p.status)) {
                     alive = false;
                     break;
                 }
-                fence_after();
-                ++merges;
-                const float2 o = xch[rho];
-                const float mt = fmaxf(m, o.x);
-                const float me = mt == -INFINITY ? 0.f : mt;
-                wa = exp2_approx(m - me);
-                wb = exp2_approx(o.x - me);
-                l = l * wa + o.y * wb;
-                m = mt;
+                merges ^= 1u << x;
+                part_of |= 1u << v;
+                mt = fmaxf(mt, xch[v * kSlotRows + rho].x);
             }
-            const bool whole = it.whole();
-            const float norm = whole ? 1.f / l : 1.f;
+            if (!alive) break;
+            fence_after();
+            const float me = mt == -INFINITY ? 0.f : mt;
+            float w[kStreams], lt = 0.f;
+#pragma unroll
+            for (int v = 0; v < kStreams; ++v) {
+                const float2 ml = v == u ? make_float2(m, l) : xch[v * kSlotRows + rho];
+                w[v] = part_of >> v & 1 ? exp2_approx(ml.x - me) : 0.f;
+                if (part_of >> v & 1) lt += ml.y * w[v];
+            }
+            const bool whole = it.t0 == 0 && it.t1 == it.nt;
+            const float norm = whole ? 1.f / lt : 1.f;
             const int row = it.row + token;
             const int head = it.h * p.G + gi;
             const int part = (blockIdx.x * 2 + (it.t0 > 0 ? 0 : 1)) * 2 * kSlotRows + s * kSlotRows + rho;
+            const int piece = it.seq;
             const Records &rec = recs[piece % kRecords];
-            const bool dirty = mine > 0 && rec.piece == piece;
+            const bool dirty = part_of != 0 && rec.piece == piece;
             const int common = keys_seen(p, it.ctx, it.n, it.tok0);  // keys every row of the item sees
             if (row_valid && whole && p.lse)
                 p.lse[static_cast<long long>(row) * p.Hq + head] =
-                    l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-            if (row_valid && !whole) p.part_ml[part] = make_float2(m, l);
+                    lt == 0.f ? -INFINITY : (mt + log2f(lt)) * 0.6931471805599453f;
+            if (row_valid && !whole) p.part_ml[part] = make_float2(mt, lt);
             // 16 dims at a time: the registers are the main loop's.
 #pragma unroll 1
             for (int d0 = 0; d0 < kD; d0 += 16) {
-                uint32_t o[16], ob[16];
-                if (mine > 0) {
-                    tmem_ld16(tmem + lanes + col_o(s) + d0, o);
-                    if (both) tmem_ld16(tmem + lanes + col_o(1) + d0, ob);
-                    tmem_wait_ld();
-                    pin16(o);
-                    if (both) {
-                        pin16(ob);
+                float o[16];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            o[j] = __float_as_uint(__uint_as_float(o[j]) * wa + __uint_as_float(ob[j]) * wb);
-                    }
-                }
-                if (d0 == kD - 16) {
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0 && mine > 0) mbar_arrive(bar_ofree + 8 * s);
-                    if (lane == 0 && both) mbar_arrive(bar_ofree + 8);
+                for (int j = 0; j < 16; ++j) o[j] = 0.f;
+#pragma unroll
+                for (int v = 0; v < kStreams; ++v) {
+                    if (!(part_of >> v & 1)) continue;
+                    uint32_t ov[16];
+                    tmem_ld16(lanes + col_o(v) + d0, ov);
+                    tmem_wait_ld();
+                    pin16(ov);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) o[j] += __uint_as_float(ov[j]) * w[v];
                 }
                 if (!row_valid) continue;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[j]) * norm);
+                for (int j = 0; j < 16; ++j) o[j] = lt == 0.f ? 0.f : o[j] * norm;
                 if (dirty) {
                     const uint32_t tag = ~static_cast<uint32_t>(piece) << 8;
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        bool seen[3];
 #pragma unroll
                         for (int q = 0; q < 3; ++q) {
                             const uint32_t e = rec.first[q][d0 + j];
-                            seen[q] = (e & 0xffffff00u) == tag && common + static_cast<int>(e & 0xffu) < sees;
+                            const bool seen = (e & 0xffffff00u) == tag && common + static_cast<int>(e & 0xffu) < sees;
+                            if (seen) o[j] = q == 2 ? __uint_as_float(0x7fffffffu) : o[j] + (q == 0 ? INFINITY : -INFINITY);
                         }
-                        float v = __uint_as_float(o[j]);
-                        if (seen[0]) v += INFINITY;
-                        if (seen[1]) v -= INFINITY;
-                        if (seen[2]) v = __uint_as_float(0x7fffffffu);
-                        o[j] = __float_as_uint(v);
                     }
                 }
                 if (whole) {
                     uint4 *dst = reinterpret_cast<uint4 *>(p.out + (static_cast<long long>(row) * p.Hq + head) * kD + d0);
-                    uint32_t w[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) w[j] = pack2(__uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1]));
-                    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                    dst[0] = make_uint4(pack2(o[0], o[1]), pack2(o[2], o[3]), pack2(o[4], o[5]), pack2(o[6], o[7]));
+                    dst[1] = make_uint4(pack2(o[8], o[9]), pack2(o[10], o[11]), pack2(o[12], o[13]), pack2(o[14], o[15]));
                 } else {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.part_o + static_cast<long long>(part) * kD + d0);
+                    float4 *dst = reinterpret_cast<float4 *>(p.part_o + static_cast<long long>(part) * kD + d0);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                    for (int j = 0; j < 4; ++j) dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
                 }
             }
-        }
-    } else if (warp < kLoadWarp) {
-        // -------------------------------------------------- preparation --
-        const int tid = threadIdx.x - 32 * kPrepWarp;
-        int st = 0, rs = 0, pieces = 0;
-        uint32_t ph = 0, rph = 0;  // rounds of the stages, mod 2
-        while (alive && next_piece(p, pl, ws)) {
-            if (it.t0 >= it.t1) continue;
-            const int piece = pieces++;
-            Records *rec = recs + piece % kRecords;
-            const uint32_t tag = ~static_cast<uint32_t>(piece) << 8;
-            const int least = keys_seen(p, it.ctx, it.n, it.tok0);  // keys that every row of the item sees
-            for (int t = it.t0; t < it.t1; ++t) {
-                uint8_t *kt = smem + L::kKv + st * L::kStageBytes;
-                uint8_t *vt = kt + L::kVOff;
-                const uint8_t *raw = smem + L::kRawOff + rs * L::kRawBytes;
-                if (QUANT) {
-                    if (!mbar_wait(bar_rfull + 8 * rs, rph, abort_flag, p.status) ||
-                        !mbar_wait(bar_empty + 8 * st, ph ^ 1, abort_flag, p.status)) {
-                        alive = false;
-                        break;
-                    }
-                } else if (!mbar_wait(bar_full + 8 * st, ph, abort_flag, p.status)) {
-                    alive = false;
-                    break;
-                }
-                if (QUANT) {
-                    // Four threads a row, 16 codes each: K's four rows of
-                    // the thread, then V's, loads first.
-#pragma unroll
-                    for (int is_v = 0; is_v < 2; ++is_v) {
-                        uint4 w[4];
-                        uint32_t b[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int c = e * 128 + tid;
-                            w[e] = *reinterpret_cast<const uint4 *>(raw + is_v * kTile * kD + c * 16);
-                            b[e] = raw[2 * kTile * kD + is_v * kTile + (c >> 2)];
-                        }
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int row = (e * 128 + tid) >> 2, quarter = tid & 3;
-                            // 2^120 times the scale, in two factors where it
-                            // passes bf16's range (rows above 448 * 2^7).
-                            const uint32_t e1 = b[e] <= 134u ? b[e] + 120u : 254u;
-                            const uint32_t mul = e1 << 7 | e1 << 23;
-                            const uint32_t in[4] = {w[e].x, w[e].y, w[e].z, w[e].w};
-                            uint32_t o[8];
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                o[2 * q] = mul_bf16x2(widen2(__byte_perm(in[q], 0, 0x1404)), mul);
-                                o[2 * q + 1] = mul_bf16x2(widen2(__byte_perm(in[q], 0, 0x3424)), mul);
-                            }
-                            if (b[e] > 134u) {
-                                const uint32_t mul2 = (b[e] - 7u) << 7 | (b[e] - 7u) << 23;
-#pragma unroll
-                                for (int q = 0; q < 8; ++q) o[q] = b[e] == 255u ? 0x7fff7fffu : mul_bf16x2(o[q], mul2);
-                            }
-                            const int key = t * kTile + row;
-                            if (is_v && (key >= it.limit || (b[e] == 255u && key >= least))) {
-                                if (key < it.limit) {
-                                    for (int d = 0; d < 16; ++d)
-                                        atomicMin(&rec->first[2][quarter * 16 + d], tag | (key - least));
-                                    rec->piece = piece;
-                                }
-#pragma unroll
-                                for (int q = 0; q < 8; ++q) o[q] = 0u;
-                            }
-                            uint8_t *dst = is_v ? vt : kt;
-                            *reinterpret_cast<uint4 *>(dst + swz(row, 2 * quarter)) = make_uint4(o[0], o[1], o[2], o[3]);
-                            *reinterpret_cast<uint4 *>(dst + swz(row, 2 * quarter + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
-                        }
-                    }
-                    fence_proxy_async();
-                } else if ((t + 1) * static_cast<long long>(kTile) > least) {
-                    const int key = t * kTile + tid;  // this thread's V row
-                    if (key >= it.limit) {
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(vt + swz(tid, c)) = make_uint4(0, 0, 0, 0);
-                    } else if (key >= least) {
-                        for (int c = 0; c < 8; ++c) {
-                            uint4 *at = reinterpret_cast<uint4 *>(vt + swz(tid, c));
-                            const uint4 w = *at;
-                            uint32_t v[4] = {w.x, w.y, w.z, w.w};
-                            bool bad = false;
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                bad |= (v[q] & 0x7f80u) == 0x7f80u || (v[q] & 0x7f800000u) == 0x7f800000u;
-                            if (!bad) continue;
-                            for (int q = 0; q < 8; ++q) {
-                                const uint32_t e = v[q >> 1] >> (16 * (q & 1)) & 0xffffu;
-                                if ((e & 0x7f80u) != 0x7f80u) continue;
-                                const int kind = e & 0x7fu ? 2 : e >> 15;
-                                atomicMin(&rec->first[kind][8 * c + q], tag | (key - least));
-                                v[q >> 1] &= q & 1 ? 0x0000ffffu : 0xffff0000u;
-                            }
-                            *at = make_uint4(v[0], v[1], v[2], v[3]);
-                            rec->piece = piece;
-                        }
-                    }
-                    fence_proxy_async();
-                }
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(bar_prep + 8 * st);
-                    if (QUANT) mbar_arrive(bar_rempty + 8 * rs);
-                }
-                if (++st == L::kStages) {
-                    st = 0;
-                    ph ^= 1;
-                }
-                if (QUANT && ++rs == L::kRaw) {
-                    rs = 0;
-                    rph ^= 1;
-                }
-            }
+            fence_before();
+            __syncwarp();
+            if (lane < kStreams && (part_of >> lane & 1)) mbar_arrive(bar_ofree + 8 * lane);
+            if (lane == 0) mbar_arrive(bar_pdone + 8 * (n % kRing));
         }
     } else if (warp == kLoadWarp) {
         // ------------------------------------------------------ K/V loads --
@@ -815,16 +734,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t policy;  // pages are read again by the items of other token pairs
         asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
         int x = 0;
-        Cut cut = {};
-        while (alive && next_piece(p, pl, ws)) {
-            if (it.t0 > 0) cut.has[0] = 1;
-            if (it.t0 == 0 && it.t1 < it.nt) {
-                cut.has[1] = 1;
-                cut.row = it.row;
-                cut.tokens = it.tokens;
-                cut.head = it.h;
-                cut.last = ws->walk.slice_of(it.start + it.length - 1);
-            }
+        for (int n = 0; alive; ++n) {
+            const Piece &it = pieces[n % kRing];
+            if (!mbar_wait(bar_piece + 8 * (n % kRing), (n / kRing) & 1, abort_flag, p.status)) break;
+            if (it.row < 0) break;
             const int pages = (it.limit + kP - 1) / kP;
             int mine = -2;
             for (int t = it.t0; t < it.t1; ++t, ++x) {
@@ -882,167 +795,217 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             }
+            if (lane == 0) mbar_arrive(bar_pdone + 8 * (n % kRing));
         }
-        if (lane == 0) p.cuts[blockIdx.x] = cut;
-        // Loads in flight land before the CTA leaves (a wait that gave up).
-        if (!alive) {
+        // Loads in flight land before the CTA leaves (a wait gave up).
+        if (*abort_flag) {
             for (int j = x > S ? x - S : 0; j < x; ++j) {
                 const unsigned long long t0 = global_ns();
                 while (!mbar_try_wait(full + 8 * (j % S), (j / S) & 1) && global_ns() - t0 < kWaitLimitNs) {
                 }
             }
         }
-    } else if (warp == kQWarp) {
-        // -------------------------------------------------------- Q loads --
-        int j = 0;
-        if (lane == 0) {
-            const uint32_t box = static_cast<uint32_t>(p.G) * p.tpt * 128;
-            while (alive && ws->walk.next(p, pl, ws->it)) {
-                if (it.t0 >= it.t1) continue;
-                if (!mbar_wait(bar_qempty, (j & 1) ^ 1, abort_flag, p.status)) {
+    } else if (warp < kPrepWarp) {
+        // ------------------------------------------- a stream's products --
+        const int u = warp - kMmaWarp;
+        const bool issuer = elect_one();
+        int st = 0;       // the tile's stage
+        uint32_t ph = 0;  // ... and how often the stages have come round, mod 2
+        int k = 0;        // tiles of this stream so far
+        int items = 0;    // pieces with tiles for this stream so far
+        const uint32_t kv = smem_u32(smem + L::kKv) + (u & 1) * (kP * kD * 2);
+        for (int n = 0; alive; ++n) {
+            const Piece &it = pieces[n % kRing];
+            if (!mbar_wait(bar_piece + 8 * (n % kRing), (n / kRing) & 1, abort_flag, p.status)) break;
+            if (it.row < 0) break;
+            const int t0 = it.t0, t1 = it.t1, from = it.from(u), t_end = it.end(u), step = it.step();
+            const int qb = it.seq & 1;
+            const uint32_t qph = (it.seq >> 1) & 1;
+            const uint64_t qd = desc_sw128(smem_u32(smem + L::kQ) + qb * L::kQBytes +
+                                           (it.alt ? 0 : (u >> 1) * kSlotRows * 128));
+            items += from < t_end;
+            int next = from;  // the stream's next tile
+            for (int t = t0; t < t1; ++t) {
+                if (!mbar_wait((QUANT ? bar_prep : bar_full) + 8 * st, ph, abort_flag, p.status)) {
                     alive = false;
                     break;
                 }
-                mbar_arrive_expect_tx(bar_qfull, it.alt ? box : 2 * box);
-                tma_load_3d(smem_u32(smem + L::kQ), &q_map, 0, it.h * p.G, it.row, bar_qfull);
-                if (!it.alt)
-                    tma_load_3d(smem_u32(smem + L::kQ + kSlotRows * 128), &q_map, 0, it.h * p.G, it.row + p.tpt, bar_qfull);
-                ++j;
-            }
-            if (!alive && j > 0) {
-                const unsigned long long t0 = global_ns();
-                while (!mbar_try_wait(bar_qfull, (j - 1) & 1) && global_ns() - t0 < kWaitLimitNs) {
-                }
-            }
-        }
-        __syncwarp();
-    } else {
-        // --------------------------------------------------- MMA issuers --
-        // One thread a slot.  Q K^T of the slot's next tile needs K and a
-        // free S, P V of its last needs P: whichever has its operands is
-        // issued first, with at most two P V outstanding.
-        const int s = warp - kMmaWarp;
-        if (lane == 0) {
-            int st = 0;     // the tile's stage
-            uint32_t ph = 0;  // ... and how often the stages have come round, mod 2
-            int k = 0;      // Q K^T issued
-            int kp = 0;     // P V issued
-            int j = 0;      // pieces with tiles
-            int items = 0;  // ... of them, with tiles for this slot
-            // The tiles whose P V is outstanding, the older first: stage,
-            // round (bit 8), and the number of the slot's item (from 1) at
-            // its first tile, else 0.
-            uint32_t at_a = 0, at_b = 0;
-            int item_a = 0, item_b = 0;
-            auto pv_ready = [&]() -> bool {
-                return mbar_test(bar_pfull + 8 * s, kp & 1) && mbar_test(bar_prep + 8 * (at_a & 255u), at_a >> 8) &&
-                       (item_a < 2 || mbar_test(bar_ofree + 8 * s, item_a & 1));
-            };
-            auto issue_pv = [&]() {
-                const uint64_t v = desc_sw128(smem_u32(smem + L::kKv) + (at_a & 255u) * L::kStageBytes + L::kVOff);
-#pragma unroll
-                for (int kk = 0; kk < kTile / 16; ++kk)
-                    mma_ts(tmem + col_o(s), tmem + col_p(s) + 8 * kk, v + ((kk * 2048) >> 4), kIdescPV,
-                           (kk > 0 || item_a == 0) ? 1u : 0u);
-                mma_commit(bar_pvdone + 8 * s);
-                mma_commit(bar_empty + 8 * (at_a & 255u));
-                at_a = at_b;
-                item_a = item_b;
-                ++kp;
-            };
-            unsigned long long t0 = global_ns();
-            unsigned spins = 0;
-            // Whether to go on waiting: not past the limit, nor after
-            // another warp gave up.
-            auto patient = [&]() -> bool {
-                if ((++spins & 255u) != 0) return true;
-                if (*abort_flag) return false;
-                if (global_ns() - t0 < kWaitLimitNs) return true;
-                *abort_flag = 1;
-                if (p.status) atomicOr(p.status, K3DA_STATUS_TIMEOUT);
-                return false;
-            };
-            while (alive && ws->walk.next(p, pl, ws->it)) {
-                if (it.t0 >= it.t1) continue;
-                const int slot_keys = it.alt || s == 1 ? it.limit : keys_seen(p, it.ctx, it.n, it.tok0 + p.tpt - 1);
-                const int t_end = min(it.t1, (slot_keys + kTile - 1) / kTile);
-                const int t_from = it.from(s);
-                const int last = t_from >= t_end ? -1 : it.alt ? t_from + ((t_end - 1 - t_from) & ~1) : t_end - 1;
-                if (last >= 0) ++items;
-                const uint64_t qd = desc_sw128(smem_u32(smem + L::kQ + (it.alt ? 0 : s * kSlotRows * 128)));
-                for (int t = it.t0; t < it.t1 && alive; ++t) {
-                    const uint32_t ready = (QUANT ? bar_prep : bar_full) + 8 * st;
-                    const bool mine = t >= t_from && t <= last && (!it.alt || ((t - t_from) & 1) == 0);
-                    t0 = global_ns();
-                    bool taken = false;
-                    while (!taken && alive) {
-                        if (k > kp && pv_ready()) {
-                            fence_after();
-                            issue_pv();
-                        }
-                        if (!mine) {
-                            taken = mbar_test(ready, ph);
-                            if (taken) mbar_arrive(bar_empty + 8 * st);
-                        } else if (k - kp < 2 && mbar_test(ready, ph) &&
-                                   (k == 0 || mbar_test(bar_sfree + 8 * s, (k - 1) & 1)) &&
-                                   (t != t_from || mbar_test(bar_qfull, j & 1))) {
-                            fence_after();
-                            const uint64_t kd = desc_sw128(smem_u32(smem + L::kKv) + st * L::kStageBytes);
-#pragma unroll
-                            for (int kk = 0; kk < kD / 16; ++kk)
-                                mma_ss(tmem + col_s(s), qd + ((kk * 32) >> 4), kd + ((kk * 32) >> 4), kIdescQK,
-                                       kk > 0 ? 1u : 0u);
-                            mma_commit(bar_sfull + 8 * s);
-                            if (t == last) mma_commit(bar_qempty);
-                            at_b = static_cast<uint32_t>(st) | ph << 8;
-                            item_b = t == t_from ? items : 0;
-                            if (k == kp) {
-                                at_a = at_b;
-                                item_a = item_b;
-                            }
-                            ++k;
-                            taken = true;
-                        }
-                        if (!taken) alive = patient();
-                    }
-                    if (++st == L::kStages) {
-                        st = 0;
-                        ph ^= 1;
-                    }
-                }
-                if (last < 0) {
-                    // Nothing of this piece for the slot: Q is not needed.
-                    // An outstanding P V is issued meanwhile (the other
-                    // slot's way to this Q may lead through it).
-                    t0 = global_ns();
-                    while (alive && !mbar_test(bar_qfull, j & 1)) {
-                        if (k > kp && pv_ready()) {
-                            fence_after();
-                            issue_pv();
-                        }
-                        alive = patient();
-                    }
-                    if (alive) mbar_arrive(bar_qempty);
-                }
-                ++j;
-            }
-            t0 = global_ns();
-            while (k > kp && alive) {
-                if (pv_ready()) {
-                    fence_after();
-                    issue_pv();
+                if (t != next || t >= t_end) {
+                    if (lane == 0) mbar_arrive(bar_empty + 8 * st);
                 } else {
-                    alive = patient();
+                    next += step;
+                    if (t == from && !mbar_wait(bar_qfull + 8 * qb, qph, abort_flag, p.status)) {
+                        alive = false;
+                        break;
+                    }
+                    // S and P share their columns: the last P V has read its P.
+                    if (k > 0 && !mbar_wait(bar_pvdone + 8 * u, (k - 1) & 1, abort_flag, p.status)) {
+                        alive = false;
+                        break;
+                    }
+                    fence_after();
+                    if (issuer) {
+                        const uint64_t kd = desc_sw128(kv + st * L::kStageBytes);
+#pragma unroll
+                        for (int kk = 0; kk < kD / 16; ++kk)
+                            mma_ss(tmem + col_s(u), qd + ((kk * 32) >> 4), kd + ((kk * 32) >> 4), kIdescQK,
+                                   kk > 0 ? 1u : 0u);
+                        mma_commit(bar_sfull + 8 * u);
+                        if (next >= t_end) mma_commit(bar_qempty + 8 * qb);
+                    }
+                    if (!mbar_wait(bar_pfull + 8 * u, k & 1, abort_flag, p.status) ||
+                        (!QUANT && !mbar_wait(bar_prep + 8 * st, ph, abort_flag, p.status)) ||
+                        (t == from && items > 1 && !mbar_wait(bar_ofree + 8 * u, items & 1, abort_flag, p.status))) {
+                        alive = false;
+                        break;
+                    }
+                    fence_after();
+                    if (issuer) {
+                        const uint64_t vd = desc_sw128(kv + st * L::kStageBytes + L::kVOff);
+#pragma unroll
+                        for (int kk = 0; kk < kP / 16; ++kk)
+                            mma_ts(tmem + col_o(u), tmem + col_s(u) + 8 * kk, vd + ((kk * 2048) >> 4), kIdescPV,
+                                   (kk > 0 || t != from) ? 1u : 0u);
+                        mma_commit(bar_pvdone + 8 * u);
+                        mma_commit(bar_empty + 8 * st);
+                    }
+                    ++k;
+                }
+                if (++st == L::kStages) {
+                    st = 0;
+                    ph ^= 1;
                 }
             }
-            // Every product and its signals complete before the CTA leaves.
-            fence_after();
-            mma_commit(bar_done);
-            t0 = global_ns();
-            while (!mbar_try_wait(bar_done, 0) && global_ns() - t0 < kWaitLimitNs) {
+            if (!alive) break;
+            if (from >= t_end && t0 < t1) {
+                // Nothing of this piece for the stream: Q is not needed.
+                if (!mbar_wait(bar_qfull + 8 * qb, qph, abort_flag, p.status)) break;
+                if (lane == 0) mbar_arrive(bar_qempty + 8 * qb);
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_pdone + 8 * (n % kRing));
         }
+        // Every product and its signals complete before the CTA leaves.
+        fence_after();
+        if (issuer) mma_commit(bar_done);
         __syncwarp();
+        const unsigned long long t0 = global_ns();
+        while (!mbar_try_wait(bar_done, 0) && global_ns() - t0 < kWaitLimitNs) {
+        }
+    } else {
+        // -------------------------------------------------- preparation --
+        const int tid = threadIdx.x - 32 * kPrepWarp;
+        int st = 0, rs = 0;
+        uint32_t ph = 0, rph = 0;  // rounds of the stages, mod 2
+        for (int n = 0; alive; ++n) {
+            const Piece &it = pieces[n % kRing];
+            if (!mbar_wait(bar_piece + 8 * (n % kRing), (n / kRing) & 1, abort_flag, p.status)) break;
+            if (it.row < 0) break;
+            const int piece = it.seq, limit = it.limit, t1 = it.t1;
+            Records *rec = recs + piece % kRecords;
+            const uint32_t tag = ~static_cast<uint32_t>(piece) << 8;
+            const int least = keys_seen(p, it.ctx, it.n, it.tok0);  // keys that every row of the item sees
+            for (int t = it.t0; t < t1; ++t) {
+                uint8_t *kt = smem + L::kKv + st * L::kStageBytes;
+                uint8_t *vt = kt + L::kVOff;
+                if (QUANT) {
+                    const uint8_t *raw = smem + L::kRawOff + rs * L::kRawBytes;
+                    if (!mbar_wait(bar_rfull + 8 * rs, rph, abort_flag, p.status) ||
+                        !mbar_wait(bar_empty + 8 * st, ph ^ 1, abort_flag, p.status)) {
+                        alive = false;
+                        break;
+                    }
+                    // 1024 pieces of 16 codes (K's 512, then V's), four a row.
+#pragma unroll 2
+                    for (int c = tid; c < 1024; c += 32 * kPrepWarps) {
+                        const uint4 w = *reinterpret_cast<const uint4 *>(raw + c * 16);
+                        const uint32_t b = raw[2 * kTile * kD + (c >> 2)];
+                        const bool is_v = c >= 512;
+                        const int row = (c & 511) >> 2, quarter = c & 3;
+                        // 2^120 times the scale, in two factors where it
+                        // passes bf16's range (rows above 448 * 2^7).
+                        const uint32_t e1 = b <= 134u ? b + 120u : 254u;
+                        const uint32_t mul = e1 << 7 | e1 << 23;
+                        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+                        uint32_t o[8];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            o[2 * q] = mul_bf16x2(widen2(__byte_perm(in[q], 0, 0x1404)), mul);
+                            o[2 * q + 1] = mul_bf16x2(widen2(__byte_perm(in[q], 0, 0x3424)), mul);
+                        }
+                        const int key = t * kTile + row;
+                        if (b > 134u || (is_v && key >= limit)) {
+                            const uint32_t mul2 = (b - 7u) << 7 | (b - 7u) << 23;
+                            const bool hidden = is_v && (key >= limit || (b == 255u && key >= least));
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                o[q] = hidden ? 0u : b == 255u ? 0x7fff7fffu : mul_bf16x2(o[q], mul2);
+                            if (hidden && key < limit) {
+                                for (int d = 0; d < 16; ++d)
+                                    atomicMin(&rec->first[2][quarter * 16 + d], tag | (key - least));
+                                rec->piece = piece;
+                            }
+                        }
+                        uint8_t *dst = kt + (is_v ? L::kVOff : 0);
+                        *reinterpret_cast<uint4 *>(dst + swz(row, 2 * quarter)) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4 *>(dst + swz(row, 2 * quarter + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+                    }
+                    fence_proxy_async();
+                } else {
+                    if (!mbar_wait(bar_full + 8 * st, ph, abort_flag, p.status)) {
+                        alive = false;
+                        break;
+                    }
+                    if ((t + 1) * static_cast<long long>(kTile) > least) {
+                        for (int row = tid; row < kTile; row += 32 * kPrepWarps) {
+                            const int key = t * kTile + row;
+                            if (key < least) continue;
+#pragma unroll 1
+                            for (int c = 0; c < 8; ++c) {
+                                uint4 *at = reinterpret_cast<uint4 *>(vt + swz(row, c));
+                                if (key >= limit) {
+                                    *at = make_uint4(0, 0, 0, 0);
+                                    continue;
+                                }
+                                const uint4 w = *at;
+                                uint32_t v[4] = {w.x, w.y, w.z, w.w};
+                                bool bad = false;
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    bad |= (v[q] & 0x7f80u) == 0x7f80u || (v[q] & 0x7f800000u) == 0x7f800000u;
+                                if (!bad) continue;
+#pragma unroll
+                                for (int q = 0; q < 8; ++q) {
+                                    const uint32_t e = v[q >> 1] >> (16 * (q & 1)) & 0xffffu;
+                                    if ((e & 0x7f80u) != 0x7f80u) continue;
+                                    const int kind = e & 0x7fu ? 2 : e >> 15;
+                                    atomicMin(&rec->first[kind][8 * c + q], tag | (key - least));
+                                    v[q >> 1] &= q & 1 ? 0x0000ffffu : 0xffff0000u;
+                                }
+                                *at = make_uint4(v[0], v[1], v[2], v[3]);
+                                rec->piece = piece;
+                            }
+                        }
+                        fence_proxy_async();
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar_prep + 8 * st);
+                    if (QUANT) mbar_arrive(bar_rempty + 8 * rs);
+                }
+                if (++st == L::kStages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+                if (QUANT && ++rs == L::kRaw) {
+                    rs = 0;
+                    rph ^= 1;
+                }
+            }
+            if (!alive) break;
+            if (lane == 0) mbar_arrive(bar_pdone + 8 * (n % kRing));
+        }
     }
 
     fence_before();
@@ -1183,7 +1146,7 @@ int launch_chunk(const CUtensorMap &kv_map, const CUtensorMap &q_map, const Chun
     if (cudaFuncSetAttribute(k3da_chunk_kernel<QUANT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              Smem<QUANT>::kBytes) != cudaSuccess)
         return K3DA_ECUDA;
-    k3da_chunk_kernel<QUANT><<<kCtas, kThreads, Smem<QUANT>::kBytes, st>>>(kv_map, q_map, prm);
+    k3da_chunk_kernel<QUANT><<<kCtas, threads_of(QUANT), Smem<QUANT>::kBytes, st>>>(kv_map, q_map, prm);
     return cudaGetLastError() == cudaSuccess ? K3DA_OK : K3DA_ECUDA;
 }
 
