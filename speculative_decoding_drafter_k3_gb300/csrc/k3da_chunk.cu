@@ -21,20 +21,24 @@
 // Both slots of an item read the same K/V tiles (shared).  An item whose
 // tokens fit one slot (a decode step, a draft block, a chunk's tail) gives
 // its tiles to the two slots in turn (alternate), both with the same rows.
-// Either way a slot's tile is worked on by two streams, one for each page:
-// four streams, each with 64 columns of S, a softmax warpgroup (one thread a
-// row, its own running maximum and sum), an O accumulator and a thread that
-// issues its products.  A stream alone is a chain: Q K^T, softmax, P V, each
-// waiting for the last; four of them side by side keep the tensor cores, the
-// exponential units and the loads busy, and none needs to know of the others
-// until an item ends and one warpgroup merges what belongs to the same rows.
-// Two streams of 128 columns each, with S and P apart so that Q K^T ran
-// ahead, were slower: two softmax warps a scheduler could not hide their own
-// latencies, and their unrolled code did not fit the instruction cache.
+// Either way a slot's tile is worked on by two softmax warpgroups, one for
+// each page: a thread has 64 scores of a row in registers.  The two share the
+// row's running maximum (each leaves its page's in shared memory, and reads
+// the other's) and one O.  Four softmax warps a scheduler hide each other's
+// latencies; two (a slot's 128 columns in one thread) did not, and their
+// unrolled code did not fit the instruction cache.
+//
+// Tensor memory holds three S of 128 columns for the two slots, taken in
+// turn by the CTA's steps (a step: one slot's tile), P over its own S, and an
+// O a slot.  The third S is Q K^T of the next step, ready when its slot has
+// formed the last weights; and since the step after that has to wait for a P V
+// of the other slot, the slots fall out of step by themselves: one forms
+// weights, which the exponential units bound, while the other loads, looks for
+// maxima and waits.
 //
 // The other warps: a scheduler that cuts the CTA's slice into pieces and
-// loads Q, a K/V loader, the four product issuers, and a few that prepare
-// tiles (below).
+// loads Q, a K/V loader, an issuer of Q K^T, one of P V for each slot, and a
+// few that prepare tiles (below).
 //
 // The preparing warps zero the V rows past an item's last key (stale slots
 // may hold anything, and 0 * NaN is NaN), and where only some of an item's
@@ -70,25 +74,26 @@ constexpr int kTile = 128;         // keys of a tile: two pages
 constexpr int kSlotRows = 128;     // query rows of a slot
 constexpr int kOverhead = 128;     // an item's fixed cost, in keys
 constexpr int kMinSlice = 256;     // shortest slice, in keys
-constexpr int kStreams = 4;        // stream u: slot u / 2, page u % 2 of its tiles
+constexpr int kGroups = 4;         // softmax warpgroups: u has slot u / 2, page u % 2 of its tiles
 constexpr int kRing = 4;           // pieces published ahead
 constexpr int kRecords = 8;        // pieces whose non-finite records are alive at once
 constexpr float kRescale = 8.0f;   // log2 units the running maximum may lag behind
 // Warps: four softmax warpgroups, then single warps, then the preparing ones
 // (widening codes takes more of them than looking tiles over).
-constexpr int kLoadWarp = 16, kSchedWarp = 17, kMmaWarp = 18, kPrepWarp = 22;
-__host__ __device__ constexpr int prep_warps(bool quant) { return quant ? 6 : 2; }
+constexpr int kLoadWarp = 16, kSchedWarp = 17, kQkWarp = 18, kPvWarp = 19, kPrepWarp = 21;
+constexpr int kBufs = 3;           // S buffers
+__host__ __device__ constexpr int prep_warps(bool quant) { return quant ? 7 : 3; }
 __host__ __device__ constexpr int threads_of(bool quant) { return 32 * (kPrepWarp + prep_warps(quant)); }
 // Registers a thread.  bf16: 768 threads launched with 80, 512 x 88 + 256 x
 // 64; e4m3: 896 launched with 72, 512 x 88 + 384 x 48.
 __host__ __device__ constexpr int softmax_regs(bool) { return 88; }
 __host__ __device__ constexpr int other_regs(bool quant) { return quant ? 48 : 64; }
-// Tensor memory columns of stream u.  P (32 columns of bf16 pairs) lies over
-// the first half of its S.
-__device__ __forceinline__ uint32_t col_s(int u) { return 64u * u; }
-__device__ __forceinline__ uint32_t col_o(int u) { return 256u + 64u * u; }
+// Tensor memory columns of S buffer b (each page's P, 32 columns of bf16
+// pairs, over the first half of its S) and of slot s's O.
+__device__ __forceinline__ uint32_t col_s(int b) { return 128u * b; }
+__device__ __forceinline__ uint32_t col_o(int s) { return 384u + 64u * s; }
 constexpr uint32_t kTmemCols = 512u;
-constexpr uint32_t kIdescQK = idesc_f16(128, kP, false);
+constexpr uint32_t kIdescQK = idesc_f16(128, kTile, false);
 constexpr uint32_t kIdescPV = idesc_f16(128, kD, true);
 
 struct ChunkParams {
@@ -131,7 +136,6 @@ constexpr size_t kWorkspace = kCutBytes + kPartRows * (sizeof(float2) + kD * siz
 
 struct Plan {
     long long prefix[kMaxRequests + 1];  // where request r's items begin on the line
-    int32_t row[kMaxRequests];           // its first row
     int32_t n[kMaxRequests];             // its new tokens
     int32_t ctx[kMaxRequests];           // its cached tokens
     long long warp_sum[kMaxRequests / 64];
@@ -161,7 +165,6 @@ __device__ void build_plan(const ChunkParams &p, Plan *pl, bool report) {
         const bool fits = p.mask == K3DA_MASK_CONTEXT || static_cast<long long>(ctx) + n <= cap;
         if (report && p.status && (a != begin || b != end || (n > 0 && (c != ctx || !fits))))
             atomicOr(p.status, K3DA_STATUS_BAD_LENGTH);
-        pl->row[r] = begin;
         pl->n[r] = n;
         pl->ctx[r] = ctx;
         const long long base = static_cast<long long>(ctx) + (p.mask == K3DA_MASK_FULL ? n : 0);
@@ -199,13 +202,21 @@ struct Piece {
     int t0, t1;
     int alt;     // one slot's worth of rows: the slots take the tiles in turn
     int seq;     // number of the piece among those with tiles
-    // The tiles of stream u: from, from + step, ... below end.
-    __device__ __forceinline__ int from(int u) const { return alt ? t0 + (u >> 1) : t0; }
+    int base;    // steps before it
+    // The tiles of slot s: from, from + step, ... below end.
+    __device__ __forceinline__ int from(int s) const { return alt ? t0 + s : t0; }
     __device__ __forceinline__ int step() const { return alt ? 2 : 1; }
-    __device__ __forceinline__ int end(int u) const {
-        const int keys = (alt || u >= 2 ? limit : keys0) - kP * (u & 1);
+    __device__ __forceinline__ int end(int s) const {
+        const int keys = alt || s == 1 ? limit : keys0;
         return keys <= 0 ? 0 : min(t1, (keys - 1) / kTile + 1);
     }
+    // The step of slot s's tile t: tile by tile, slot 0 first.
+    __device__ __forceinline__ int step_of(int s, int t) const {
+        const int d = t - t0;
+        if (alt) return base + d;
+        return base + d + (s == 0 ? d : min(d + 1, max(end(0) - t0, 0)));
+    }
+    __device__ __forceinline__ int steps() const { return t1 - t0 + (alt ? 0 : max(end(0) - t0, 0)); }
 };
 
 // Keys that the chunk's token i sees.
@@ -282,7 +293,7 @@ struct Walk {
             it.n = pl->n[r];
             it.tok0 = pair * 2 * p.tpt;
             it.tokens = min(2 * p.tpt, it.n - it.tok0);
-            it.row = pl->row[r] + it.tok0;
+            it.row = min(max(__ldg(p.cu_seqlens + r), 0), p.T) + it.tok0;
             it.alt = it.tokens <= p.tpt;
             it.limit = keys_seen(p, it.ctx, it.n, it.tok0 + it.tokens - 1);
             it.nt = static_cast<int>((static_cast<long long>(it.limit) + kTile - 1) / kTile);
@@ -345,9 +356,9 @@ struct Smem {
     static constexpr int kPlan = kRawOff + kRaw * kRawBytes;
     static constexpr int kRec = kPlan + static_cast<int>(sizeof(Plan));
     static constexpr int kXch = kRec + kRecords * static_cast<int>(sizeof(Records));
-    static constexpr int kPieces = kXch + kStreams * kSlotRows * 8;
+    static constexpr int kPieces = kXch + (3 * kGroups + 1) * kSlotRows * 4;
     static constexpr int kBars = kPieces + kRing * static_cast<int>(sizeof(Piece));
-    static constexpr int kNumBars = 3 * kStages + 2 * kRaw + 2 * kRing + 4 + 5 * kStreams + 2;
+    static constexpr int kNumBars = 3 * kStages + 2 * kRaw + 2 * kRing + 4 + 7 * kBufs + 2 * 3 + 2;
     static constexpr int kTail = kBars + kNumBars * 8;  // TMEM address, abort flag
     static constexpr int kBytes = kTail + 16 + 1024;
     static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
@@ -369,11 +380,8 @@ __device__ __forceinline__ void pin32(uint32_t *r) {
                      "+r"(r[j + 6]), "+r"(r[j + 7]));
 }
 
-__device__ __forceinline__ void pin16(uint32_t *r) {
-#pragma unroll
-    for (int j = 0; j < 16; j += 8)
-        asm volatile("" : "+r"(r[j]), "+r"(r[j + 1]), "+r"(r[j + 2]), "+r"(r[j + 3]), "+r"(r[j + 4]), "+r"(r[j + 5]),
-                     "+r"(r[j + 6]), "+r"(r[j + 7]));
+__device__ __forceinline__ void pin8(uint32_t *r) {
+    asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]));
 }
 
 // Two e4m3 codes (the top bytes of the halves of h) as bf16 times 2^-120:
@@ -396,7 +404,9 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
     uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // 1 KB aligned, and still known to be shared memory
     Plan *pl = reinterpret_cast<Plan *>(smem + L::kPlan);
     Records *recs = reinterpret_cast<Records *>(smem + L::kRec);
-    float2 *xch = reinterpret_cast<float2 *>(smem + L::kXch);  // [kStreams][128] (m, l)
+    float *xmax = reinterpret_cast<float *>(smem + L::kXch);  // [2][kGroups][128] a page's row maxima, by tile parity
+    float *xl = xmax + 2 * kGroups * kSlotRows;               // [kGroups][128] a page's share of the row sums
+    float *xm = xl + kGroups * kSlotRows;                     // [128] slot 1's base of the exponents
     Piece *pieces = reinterpret_cast<Piece *>(smem + L::kPieces);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kTail + 8);
     uint32_t *taddr_slot = reinterpret_cast<uint32_t *>(smem + L::kTail);
@@ -410,15 +420,18 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
     const uint32_t bar_pdone = bar_piece + 8 * kRing;       // [kRing] ... and read by everybody
     const uint32_t bar_qfull = bar_pdone + 8 * kRing;       // [2] a piece's Q loaded
     const uint32_t bar_qempty = bar_qfull + 16;             // [2] ... and read
-    const uint32_t bar_sfull = bar_qempty + 16;             // [kStreams] S written
-    const uint32_t bar_pfull = bar_sfull + 8 * kStreams;    // [kStreams] P written
-    const uint32_t bar_pvdone = bar_pfull + 8 * kStreams;   // [kStreams] P V complete
-    const uint32_t bar_ofree = bar_pvdone + 8 * kStreams;   // [kStreams] an item's O read
-    // [kStreams + 1] a stream's part of an item is ready: u where all meet in
-    // stream 0, u + u / 2 in a shared item (stream 3 reports to either 0 or 2,
-    // and each counts the phases of a barrier of its own).
-    const uint32_t bar_xch = bar_ofree + 8 * kStreams;
-    const uint32_t bar_done = bar_xch + 8 * (kStreams + 1); // every issuer's products are complete
+    // A slot's k-th tile has the barriers k % 3 of its own three: each side
+    // then waits for every phase of the barriers it waits on, and none can be
+    // two phases ahead (the slot's tile k + 3 needs the buffer of tile k).
+    const uint32_t bar_sfull = bar_qempty + 16;             // [2][kBufs] S written
+    const uint32_t bar_pfull = bar_sfull + 16 * kBufs;      // [2][kBufs] P written
+    const uint32_t bar_bfree = bar_pfull + 16 * kBufs;      // [kBufs] P of the buffer read
+    const uint32_t bar_pvdone = bar_bfree + 8 * kBufs;      // [2][kBufs] a slot's P V complete
+    const uint32_t bar_max = bar_pvdone + 16 * kBufs;       // [2] both pages' maxima left
+    const uint32_t bar_ofree = bar_max + 16;                // [2] an item's O read
+    const uint32_t bar_sums = bar_ofree + 16;               // [2] both pages' row sums left
+    const uint32_t bar_xch = bar_sums + 16;                 // slot 1's half of an alternate item is ready
+    const uint32_t bar_done = bar_xch + 8;                  // every issuer's products are complete
     const int warp = __shfl_sync(kFull, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -426,7 +439,7 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
         for (int s = 0; s < L::kStages; ++s) {
             mbar_init(bar_full + 8 * s, 1);
             mbar_init(bar_prep + 8 * s, kPrepWarps);
-            mbar_init(bar_empty + 8 * s, kStreams);
+            mbar_init(bar_empty + 8 * s, 2);
         }
         for (int s = 0; s < L::kRaw; ++s) {
             mbar_init(bar_rfull + 8 * s, 1);
@@ -438,17 +451,19 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(bar_qfull + 8 * s, 1);
-            mbar_init(bar_qempty + 8 * s, kStreams);
+            mbar_init(bar_qempty + 8 * s, 1);
+            mbar_init(bar_max + 8 * s, 8);
+            mbar_init(bar_ofree + 8 * s, 8);
+            mbar_init(bar_sums + 8 * s, 8);
         }
-        for (int u = 0; u < kStreams; ++u) {
-            mbar_init(bar_sfull + 8 * u, 1);
-            mbar_init(bar_pfull + 8 * u, 4);
-            mbar_init(bar_pvdone + 8 * u, 1);
-            mbar_init(bar_ofree + 8 * u, 4);
-            mbar_init(bar_xch + 8 * u, 4);
+        for (int b = 0; b < 2 * kBufs; ++b) {
+            mbar_init(bar_sfull + 8 * b, 1);
+            mbar_init(bar_pfull + 8 * b, 8);
+            mbar_init(bar_pvdone + 8 * b, 1);
         }
-        mbar_init(bar_xch + 8 * kStreams, 4);
-        mbar_init(bar_done, kStreams);
+        for (int b = 0; b < kBufs; ++b) mbar_init(bar_bfree + 8 * b, 1);
+        mbar_init(bar_xch, 8);
+        mbar_init(bar_done, 3);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     for (int e = threadIdx.x; e < kRecords; e += kThreads) recs[e].piece = -1;
@@ -467,7 +482,7 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
     const uint32_t tmem = *taddr_slot;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     bool alive = true;
-    if (warp < 4 * kStreams) regs_raise<softmax_regs(QUANT)>();
+    if (warp < 4 * kGroups) regs_raise<softmax_regs(QUANT)>();
     else regs_lower<other_regs(QUANT)>();
 
     if (warp == kSchedWarp) {
@@ -477,7 +492,7 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
             walk.begin(p, pl, blockIdx.x);
             Cut cut = {};
             const uint32_t box = static_cast<uint32_t>(p.G) * p.tpt * 128;
-            int seq = 0;
+            int seq = 0, base = 0;
             for (int n = 0; alive; ++n) {
                 const int slot = n % kRing;
                 if (!mbar_wait(bar_pdone + 8 * slot, ((n / kRing) & 1) ^ 1, abort_flag, p.status)) {
@@ -488,7 +503,9 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
                 const bool more = walk.next(p, pl, it);
                 if (!more) it.row = -1;
                 it.seq = seq;
+                it.base = base;
                 const bool tiles = more && it.t0 < it.t1;
+                if (tiles) base += it.steps();
                 const int alt = it.alt, h = it.h, row = it.row;
                 if (more && it.t0 > 0) cut.has[0] = 1;
                 if (tiles && it.t0 == 0 && it.t1 < it.nt) {
@@ -523,14 +540,15 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
             }
         }
         __syncwarp();
-    } else if (warp < 4 * kStreams) {
+    } else if (warp < 4 * kGroups) {
         // ------------------------------------------------------ softmax --
-        const int u = warp >> 2, s = u >> 1;
+        const int u = warp >> 2, s = u >> 1, page = u & 1;
         const int rho = threadIdx.x & (kSlotRows - 1);  // this thread's row of the slot
         const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
         const int ti = rho / p.G, gi = rho - ti * p.G;
-        int k = 0;           // tiles of this stream so far
-        uint32_t merges = 0;  // bit x: parity of the phases of bar_xch[x] waited for
+        int k = 0;       // tiles of this slot so far
+        int sums = 0;    // pieces with tiles for it so far
+        int merges = 0;  // alternate pieces with tiles for both slots so far
         for (int n = 0; alive; ++n) {
             const Piece &it = pieces[n % kRing];
             if (!mbar_wait(bar_piece + 8 * (n % kRing), (n / kRing) & 1, abort_flag, p.status)) break;
@@ -541,190 +559,232 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
             const bool warp_valid = __any_sync(kFull, row_valid);
             const int sees = row_valid ? keys_seen(p, it.ctx, it.n, it.tok0 + token) : 0;
             const int least = keys_seen(p, it.ctx, it.n, it.tok0 + (alt ? 0 : s * p.tpt));  // ... of the slot's rows
-            const int from = it.from(u), t_end = it.end(u), step = it.step();
+            const int from = it.from(s), t_end = it.end(s), step = it.step();
             float m = -INFINITY, l = 0.f;
             for (int t = from; t < t_end; t += step) {
-                if (!mbar_wait(bar_sfull + 8 * u, k & 1, abort_flag, p.status)) {
+                const uint32_t round = static_cast<uint32_t>(k) / kBufs, turn = s * kBufs + k - round * kBufs;
+                if (!mbar_wait(bar_sfull + 8 * turn, round & 1, abort_flag, p.status)) {
                     alive = false;
                     break;
                 }
-                fence_after();
-                ++k;
-                if (warp_valid) {
-                    const int key0 = t * kTile + kP * (u & 1);
-                    uint32_t x[kP];
-                    tmem_ld32(lanes + col_s(u), x);
-                    tmem_ld32(lanes + col_s(u) + 32, x + 32);
-                    tmem_wait_ld();
-                    pin32(x);
-                    pin32(x + 32);
-                    if (key0 + kP > least) {
-                        const int lim = sees - key0;
-#pragma unroll
-                        for (int j = 0; j < kP; ++j) x[j] = j < lim ? x[j] : 0xff800000u;
+                if (!warp_valid) {
+                    // No row of this warp's: it only keeps step.
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar_max + 8 * s);
+                        mbar_arrive(bar_pfull + 8 * turn);
                     }
-                    float mx[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) mx[j] = fmaxf(__uint_as_float(x[j]), __uint_as_float(x[j + 4]));
-#pragma unroll
-                    for (int j = 8; j < kP; j += 8)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            mx[q] = fmax3(mx[q], __uint_as_float(x[j + q]), __uint_as_float(x[j + 4 + q]));
-                    const float rmax = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
-                    // The base of the exponents follows the row's maximum
-                    // only when that passes it by 2^8: P up to 256 is as
-                    // exact, and O is left alone.
-                    const bool first = t == from;
-                    const bool need = !first && rmax > m + kRescale;
-                    const float m_new = first || need ? rmax : m;
-                    const float m_eff = m_new == -INFINITY ? 0.f : m_new;  // a row that has seen nothing yet
-                    const float f = need ? exp2_approx(m - m_eff) : 1.f;
-                    m = m_new;
-                    if (__any_sync(kFull, need)) {
-                        // O is at rest: this S was written after the last P V.
-#pragma unroll 1
-                        for (int d0 = 0; d0 < kD; d0 += 16) {
-                            uint32_t o[16];
-                            tmem_ld16(lanes + col_o(u) + d0, o);
-                            tmem_wait_ld();
-                            pin16(o);
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                            tmem_st16(lanes + col_o(u) + d0, o);
-                        }
+                    if (!mbar_wait(bar_max + 8 * s, k & 1, abort_flag, p.status)) {
+                        alive = false;
+                        break;
                     }
-                    const unsigned long long sl2 = pack_f32x2(p.scale_log2, p.scale_log2);
-                    const unsigned long long nm2 = pack_f32x2(-m_eff, -m_eff);
-                    unsigned long long sum[2] = {0ull, 0ull};
-                    // P of 32 keys at a time, over the S just read; in stages
-                    // of independent operations.
-#pragma unroll
-                    for (int j = 0; j < kP; j += 32) {
-                        unsigned long long e[16];
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int q = 0; q < 16; ++q)
-                            e[q] = fma_f32x2(pack_f32x2(__uint_as_float(x[j + 2 * q]), __uint_as_float(x[j + 2 * q + 1])), sl2, nm2);
-#pragma unroll
-                        for (int q = 0; q < 16; ++q) e[q] = exp2_f32x2(e[q]);
-#pragma unroll
-                        for (int q = 0; q < 16; ++q) {
-                            const float2 w = unpack_f32x2(e[q]);
-                            pk[q] = pack2(w.x, w.y);
-                            sum[q & 1] = add_f32x2(sum[q & 1], e[q]);
-                        }
-                        tmem_st16(lanes + col_s(u) + j / 2, pk);
-                    }
-                    const float2 tot = unpack_f32x2(add_f32x2(sum[0], sum[1]));
-                    l = l * f + (tot.x + tot.y);
-                    tmem_wait_st();
+                    ++k;
+                    continue;
                 }
+                fence_after();
+                const uint32_t cols = lanes + col_s(static_cast<uint32_t>(it.step_of(s, t)) % kBufs) + kP * page;
+                const int key0 = t * kTile + kP * page;
+                uint32_t x[kP];
+                tmem_ld32(cols, x);
+                tmem_ld32(cols + 32, x + 32);
+                tmem_wait_ld();
+                pin32(x);
+                pin32(x + 32);
+                if (key0 + kP > least) {
+                    const int lim = sees - key0;
+#pragma unroll
+                    for (int j = 0; j < kP; ++j) x[j] = j < lim ? x[j] : 0xff800000u;
+                }
+                float mx[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mx[j] = fmaxf(__uint_as_float(x[j]), __uint_as_float(x[j + 4]));
+#pragma unroll
+                for (int j = 8; j < kP; j += 8)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        mx[q] = fmax3(mx[q], __uint_as_float(x[j + q]), __uint_as_float(x[j + 4 + q]));
+                float rmax = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
+                // The row's other page: its maximum.  (A NaN is dropped here
+                // and not from the scores: it reaches the row's sum.)
+                float *leave = xmax + (k & 1) * kGroups * kSlotRows + rho;
+                leave[u * kSlotRows] = rmax;
                 fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar_pfull + 8 * u);
+                if (lane == 0) mbar_arrive(bar_max + 8 * s);
+                if (!mbar_wait(bar_max + 8 * s, k & 1, abort_flag, p.status)) {
+                    alive = false;
+                    break;
+                }
+                rmax = fmaxf(rmax, leave[(u ^ 1) * kSlotRows]);
+                // The base of the exponents follows the row's maximum only
+                // when that passes it by 2^8: P up to 256 is as exact, and O
+                // is left alone.
+                const bool first = t == from;
+                const bool need = !first && rmax > m + kRescale;
+                const float m_new = first || need ? rmax : m;
+                const float m_eff = m_new == -INFINITY ? 0.f : m_new;  // a row that has seen nothing yet
+                const float f = need ? exp2_approx(m - m_eff) : 1.f;
+                m = m_new;
+                if (__any_sync(kFull, need)) {
+                    // A row's two threads scale one half of its O each, once
+                    // the slot's last P V is complete.
+                    const uint32_t last = k - 1;
+                    if (!mbar_wait(bar_pvdone + 8 * (s * kBufs + last % kBufs), last / kBufs & 1, abort_flag, p.status)) {
+                        alive = false;
+                        break;
+                    }
+                    fence_after();
+#pragma unroll 1
+                    for (int d0 = 32 * page; d0 < 32 * page + 32; d0 += 8) {
+                        uint32_t o[8];
+                        tmem_ld8(lanes + col_o(s) + d0, o);
+                        tmem_wait_ld();
+                        pin8(o);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                        tmem_st8(lanes + col_o(s) + d0, o);
+                    }
+                }
+                fence_after();
+                const unsigned long long sl2 = pack_f32x2(p.scale_log2, p.scale_log2);
+                const unsigned long long nm2 = pack_f32x2(-m_eff, -m_eff);
+                unsigned long long sum[2] = {0ull, 0ull};
+                // Weights of 32 keys at a time, in stages of independent
+                // operations.
+#pragma unroll
+                for (int j = 0; j < kP; j += 32) {
+                    unsigned long long e[16];
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int q = 0; q < 16; ++q)
+                        e[q] = fma_f32x2(pack_f32x2(__uint_as_float(x[j + 2 * q]), __uint_as_float(x[j + 2 * q + 1])), sl2, nm2);
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) e[q] = exp2_f32x2(e[q]);
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) {
+                        const float2 w = unpack_f32x2(e[q]);
+                        pk[q] = pack2(w.x, w.y);
+                        sum[q & 1] = add_f32x2(sum[q & 1], e[q]);
+                    }
+                    tmem_st16(cols + j / 2, pk);
+                }
+                const float2 tot = unpack_f32x2(add_f32x2(sum[0], sum[1]));
+                l = l * f + (tot.x + tot.y);
+                tmem_wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_pfull + 8 * turn);
+                ++k;
             }
             if (!alive) break;
             // ------------------------------------------------- epilogue --
             const bool mine = from < t_end;
-            if (mine && !mbar_wait(bar_pvdone + 8 * u, (k - 1) & 1, abort_flag, p.status)) break;
-            // The streams of the same rows meet in the first of them, whose
-            // warps own the same tensor memory lanes.
-            const int leader = alt ? 0 : u & 2;
-            if (u != leader) {
-                if (mine) {
-                    xch[u * kSlotRows + rho] = make_float2(m, l);
-                    fence_before();
-                }
+            if (mine) {
+                const uint32_t last = k - 1;
+                if (!mbar_wait(bar_pvdone + 8 * (s * kBufs + last % kBufs), last / kBufs & 1, abort_flag, p.status)) break;
+                xl[u * kSlotRows + rho] = l;
+                if (s == 1 && page == 0) xm[rho] = m;
+            }
+            const int next = n % kRing;
+            if (alt && s == 1) {
+                // Slot 0 merges: its warps own the same tensor memory lanes.
+                fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if (mine) mbar_arrive(bar_xch + 8 * (alt ? u : u + (u >> 1)));
-                    mbar_arrive(bar_pdone + 8 * (n % kRing));
+                    if (mine) mbar_arrive(bar_xch);
+                    mbar_arrive(bar_pdone + 8 * next);
                 }
                 continue;
             }
-            const int others = alt ? kStreams : leader + 2;
-            float mt = m;
-            uint32_t part_of = mine ? 1u << u : 0u;  // the streams that bring something
-            for (int v = u + 1; v < others; ++v) {
-                if (it.from(v) >= it.end(v)) continue;
-                const int x = alt ? v : v + (v >> 1);
-                if (!mbar_wait(bar_xch + 8 * x, (merges >> x) & 1, abort_flag, p.status)) {
-                    alive = false;
-                    break;
-                }
-                merges ^= 1u << x;
-                part_of |= 1u << v;
-                mt = fmaxf(mt, xch[v * kSlotRows + rho].x);
+            if (mine) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_sums + 8 * s);
+                if (!mbar_wait(bar_sums + 8 * s, sums & 1, abort_flag, p.status)) break;
+                ++sums;
+                l = xl[2 * s * kSlotRows + rho] + xl[(2 * s + 1) * kSlotRows + rho];
             }
-            if (!alive) break;
+            const bool both = alt && it.from(1) < it.end(1);
+            float wa = 1.f, wb = 0.f;
+            if (both) {
+                if (!mbar_wait(bar_xch, merges & 1, abort_flag, p.status)) break;
+                ++merges;
+                const float mb = xm[rho], lb = xl[2 * kSlotRows + rho] + xl[3 * kSlotRows + rho];
+                const float mt = fmaxf(m, mb);
+                const float me = mt == -INFINITY ? 0.f : mt;
+                wa = exp2_approx(m - me);
+                wb = exp2_approx(mb - me);
+                l = l * wa + lb * wb;
+                m = mt;
+            }
             fence_after();
-            const float me = mt == -INFINITY ? 0.f : mt;
-            float w[kStreams], lt = 0.f;
-#pragma unroll
-            for (int v = 0; v < kStreams; ++v) {
-                const float2 ml = v == u ? make_float2(m, l) : xch[v * kSlotRows + rho];
-                w[v] = part_of >> v & 1 ? exp2_approx(ml.x - me) : 0.f;
-                if (part_of >> v & 1) lt += ml.y * w[v];
-            }
             const bool whole = it.t0 == 0 && it.t1 == it.nt;
-            const float norm = whole ? 1.f / lt : 1.f;
+            const float norm = whole ? 1.f / l : 1.f;
             const int row = it.row + token;
             const int head = it.h * p.G + gi;
             const int part = (blockIdx.x * 2 + (it.t0 > 0 ? 0 : 1)) * 2 * kSlotRows + s * kSlotRows + rho;
             const int piece = it.seq;
             const Records &rec = recs[piece % kRecords];
-            const bool dirty = part_of != 0 && rec.piece == piece;
+            const bool dirty = mine && rec.piece == piece;
             const int common = keys_seen(p, it.ctx, it.n, it.tok0);  // keys every row of the item sees
-            if (row_valid && whole && p.lse)
-                p.lse[static_cast<long long>(row) * p.Hq + head] =
-                    lt == 0.f ? -INFINITY : (mt + log2f(lt)) * 0.6931471805599453f;
-            if (row_valid && !whole) p.part_ml[part] = make_float2(mt, lt);
-            // 16 dims at a time: the registers are the main loop's.
+            if (page == 0 && row_valid) {
+                if (!whole) p.part_ml[part] = make_float2(m, l);
+                else if (p.lse)
+                    p.lse[static_cast<long long>(row) * p.Hq + head] =
+                        l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+            }
+            // Half of the dims each, 8 at a time: the registers are the main
+            // loop's.
 #pragma unroll 1
-            for (int d0 = 0; d0 < kD; d0 += 16) {
-                float o[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] = 0.f;
-#pragma unroll
-                for (int v = 0; v < kStreams; ++v) {
-                    if (!(part_of >> v & 1)) continue;
-                    uint32_t ov[16];
-                    tmem_ld16(lanes + col_o(v) + d0, ov);
+            for (int d0 = 32 * page; d0 < 32 * page + 32; d0 += 8) {
+                uint32_t o[8];
+                if (mine) {
+                    tmem_ld8(lanes + col_o(s) + d0, o);
                     tmem_wait_ld();
-                    pin16(ov);
+                    pin8(o);
+                    if (both) {
+                        uint32_t ob[8];
+                        tmem_ld8(lanes + col_o(1) + d0, ob);
+                        tmem_wait_ld();
+                        pin8(ob);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) o[j] += __uint_as_float(ov[j]) * w[v];
+                        for (int j = 0; j < 8; ++j)
+                            o[j] = __float_as_uint(__uint_as_float(o[j]) * wa + __uint_as_float(ob[j]) * wb);
+                    }
                 }
                 if (!row_valid) continue;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] = lt == 0.f ? 0.f : o[j] * norm;
+                for (int j = 0; j < 8; ++j) o[j] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[j]) * norm);
                 if (dirty) {
                     const uint32_t tag = ~static_cast<uint32_t>(piece) << 8;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+#pragma unroll 1
                         for (int q = 0; q < 3; ++q) {
                             const uint32_t e = rec.first[q][d0 + j];
-                            const bool seen = (e & 0xffffff00u) == tag && common + static_cast<int>(e & 0xffu) < sees;
-                            if (seen) o[j] = q == 2 ? __uint_as_float(0x7fffffffu) : o[j] + (q == 0 ? INFINITY : -INFINITY);
+                            if ((e & 0xffffff00u) != tag || common + static_cast<int>(e & 0xffu) >= sees) continue;
+                            o[j] = q == 2 ? 0x7fffffffu : __float_as_uint(__uint_as_float(o[j]) + (q == 0 ? INFINITY : -INFINITY));
                         }
                     }
                 }
+                float v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(o[j]);
                 if (whole) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + (static_cast<long long>(row) * p.Hq + head) * kD + d0);
-                    dst[0] = make_uint4(pack2(o[0], o[1]), pack2(o[2], o[3]), pack2(o[4], o[5]), pack2(o[6], o[7]));
-                    dst[1] = make_uint4(pack2(o[8], o[9]), pack2(o[10], o[11]), pack2(o[12], o[13]), pack2(o[14], o[15]));
+                    *reinterpret_cast<uint4 *>(p.out + (static_cast<long long>(row) * p.Hq + head) * kD + d0) =
+                        make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
                 } else {
                     float4 *dst = reinterpret_cast<float4 *>(p.part_o + static_cast<long long>(part) * kD + d0);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                    dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+                    dst[1] = make_float4(v[4], v[5], v[6], v[7]);
                 }
             }
             fence_before();
             __syncwarp();
-            if (lane < kStreams && (part_of >> lane & 1)) mbar_arrive(bar_ofree + 8 * lane);
-            if (lane == 0) mbar_arrive(bar_pdone + 8 * (n % kRing));
+            if (lane == 0) {
+                if (mine) mbar_arrive(bar_ofree + 8 * s);
+                if (both) mbar_arrive(bar_ofree + 8);
+                mbar_arrive(bar_pdone + 8 * next);
+            }
         }
     } else if (warp == kLoadWarp) {
         // ------------------------------------------------------ K/V loads --
@@ -806,56 +866,67 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
             }
         }
     } else if (warp < kPrepWarp) {
-        // ------------------------------------------- a stream's products --
-        const int u = warp - kMmaWarp;
+        // ------------------------------------------------------ products --
+        // One warp issues Q K^T of every step, one P V of each slot.
+        const bool is_qk = warp == kQkWarp;
+        const int s = is_qk ? 0 : warp - kPvWarp;
         const bool issuer = elect_one();
         int st = 0;       // the tile's stage
         uint32_t ph = 0;  // ... and how often the stages have come round, mod 2
-        int k = 0;        // tiles of this stream so far
-        int items = 0;    // pieces with tiles for this stream so far
-        const uint32_t kv = smem_u32(smem + L::kKv) + (u & 1) * (kP * kD * 2);
+        int items = 0;    // pieces with tiles for the slot so far
+        uint32_t k[2] = {0, 0};  // tiles of each slot so far
+        const uint32_t kv = smem_u32(smem + L::kKv);
         for (int n = 0; alive; ++n) {
             const Piece &it = pieces[n % kRing];
             if (!mbar_wait(bar_piece + 8 * (n % kRing), (n / kRing) & 1, abort_flag, p.status)) break;
             if (it.row < 0) break;
-            const int t0 = it.t0, t1 = it.t1, from = it.from(u), t_end = it.end(u), step = it.step();
+            const int t0 = it.t0, t1 = it.t1, alt = it.alt;
+            const int from = it.from(s), t_end = it.end(s), step = it.step();
             const int qb = it.seq & 1;
-            const uint32_t qph = (it.seq >> 1) & 1;
-            const uint64_t qd = desc_sw128(smem_u32(smem + L::kQ) + qb * L::kQBytes +
-                                           (it.alt ? 0 : (u >> 1) * kSlotRows * 128));
+            const uint64_t qd = desc_sw128(smem_u32(smem + L::kQ) + qb * L::kQBytes);
+            if (is_qk && t0 < t1 && !mbar_wait(bar_qfull + 8 * qb, (it.seq >> 1) & 1, abort_flag, p.status)) break;
             items += from < t_end;
-            int next = from;  // the stream's next tile
+            int next = from;  // the slot's next tile
+            uint32_t i = it.base;
             for (int t = t0; t < t1; ++t) {
+                // Every tile in turn, another slot's too: a phase is never
+                // waited for before the one before it is known to be over.
                 if (!mbar_wait((QUANT ? bar_prep : bar_full) + 8 * st, ph, abort_flag, p.status)) {
                     alive = false;
                     break;
                 }
-                if (t != next || t >= t_end) {
-                    if (lane == 0) mbar_arrive(bar_empty + 8 * st);
-                } else {
-                    next += step;
-                    if (t == from && !mbar_wait(bar_qfull + 8 * qb, qph, abort_flag, p.status)) {
-                        alive = false;
-                        break;
-                    }
-                    // S and P share their columns: the last P V has read its P.
-                    if (k > 0 && !mbar_wait(bar_pvdone + 8 * u, (k - 1) & 1, abort_flag, p.status)) {
-                        alive = false;
-                        break;
-                    }
-                    fence_after();
-                    if (issuer) {
-                        const uint64_t kd = desc_sw128(kv + st * L::kStageBytes);
+                if (is_qk) {
+                    const uint64_t kd = desc_sw128(kv + st * L::kStageBytes);
+                    // An alternate item's slots have the same Q.
+                    for (int slot = alt || t >= t_end ? 1 : 0; slot < 2; ++slot, ++i) {
+                        const uint32_t round = i / kBufs, buf = i - round * kBufs;
+                        if (round > 0 && !mbar_wait(bar_bfree + 8 * buf, (round & 1) ^ 1, abort_flag, p.status)) {
+                            alive = false;
+                            break;
+                        }
+                        fence_after();
+                        if (issuer) {
+                            const uint64_t q = qd + (alt ? 0 : (slot * kSlotRows * 128) >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < kD / 16; ++kk)
-                            mma_ss(tmem + col_s(u), qd + ((kk * 32) >> 4), kd + ((kk * 32) >> 4), kIdescQK,
-                                   kk > 0 ? 1u : 0u);
-                        mma_commit(bar_sfull + 8 * u);
-                        if (next >= t_end) mma_commit(bar_qempty + 8 * qb);
+                            for (int kk = 0; kk < kD / 16; ++kk)
+                                mma_ss(tmem + col_s(buf), q + ((kk * 32) >> 4), kd + ((kk * 32) >> 4), kIdescQK,
+                                       kk > 0 ? 1u : 0u);
+                            const int of = alt ? (t - t0) & 1 : slot;
+                            const uint32_t turn = of * kBufs + (of ? k[1] : k[0]) % kBufs;
+                            mma_commit(bar_sfull + 8 * turn);
+                        }
+                        if (alt ? (t - t0) & 1 : slot) ++k[1];
+                        else ++k[0];
                     }
-                    if (!mbar_wait(bar_pfull + 8 * u, k & 1, abort_flag, p.status) ||
+                    if (!alive) break;
+                } else if (t == next && t < t_end) {
+                    next += step;
+                    const uint32_t buf = static_cast<uint32_t>(it.step_of(s, t)) % kBufs;
+                    const uint32_t round = k[0] / kBufs, turn = s * kBufs + k[0] - round * kBufs;
+                    ++k[0];
+                    if (!mbar_wait(bar_pfull + 8 * turn, round & 1, abort_flag, p.status) ||
                         (!QUANT && !mbar_wait(bar_prep + 8 * st, ph, abort_flag, p.status)) ||
-                        (t == from && items > 1 && !mbar_wait(bar_ofree + 8 * u, items & 1, abort_flag, p.status))) {
+                        (t == from && items > 1 && !mbar_wait(bar_ofree + 8 * s, items & 1, abort_flag, p.status))) {
                         alive = false;
                         break;
                     }
@@ -863,13 +934,15 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
                     if (issuer) {
                         const uint64_t vd = desc_sw128(kv + st * L::kStageBytes + L::kVOff);
 #pragma unroll
-                        for (int kk = 0; kk < kP / 16; ++kk)
-                            mma_ts(tmem + col_o(u), tmem + col_s(u) + 8 * kk, vd + ((kk * 2048) >> 4), kIdescPV,
-                                   (kk > 0 || t != from) ? 1u : 0u);
-                        mma_commit(bar_pvdone + 8 * u);
+                        for (int kk = 0; kk < kTile / 16; ++kk)
+                            mma_ts(tmem + col_o(s), tmem + col_s(buf) + 8 * kk + (kk >= 4 ? 32 : 0), vd + ((kk * 2048) >> 4),
+                                   kIdescPV, (kk > 0 || t != from) ? 1u : 0u);
+                        mma_commit(bar_bfree + 8 * buf);
+                        mma_commit(bar_pvdone + 8 * turn);
                         mma_commit(bar_empty + 8 * st);
                     }
-                    ++k;
+                } else if (lane == 0) {
+                    mbar_arrive(bar_empty + 8 * st);
                 }
                 if (++st == L::kStages) {
                     st = 0;
@@ -877,10 +950,10 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
                 }
             }
             if (!alive) break;
-            if (from >= t_end && t0 < t1) {
-                // Nothing of this piece for the stream: Q is not needed.
-                if (!mbar_wait(bar_qfull + 8 * qb, qph, abort_flag, p.status)) break;
-                if (lane == 0) mbar_arrive(bar_qempty + 8 * qb);
+            if (is_qk && t0 < t1) {
+                // Q is free once the products that read it are complete.
+                fence_after();
+                if (issuer) mma_commit(bar_qempty + 8 * qb);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_pdone + 8 * (n % kRing));

@@ -12,8 +12,8 @@ SOURCE = os.path.join(lint.CSRC, "k3da_chunk.cu")
 
 @pytest.fixture(autouse=True)
 def names(monkeypatch):
-    tmem = ("tmem_ld32", "tmem_ld16", "tmem_st16", "tmem_wait_ld")
-    monkeypatch.setattr(lint, "TC_CALLS", lint.TC_CALLS + tmem[:3])
+    tmem = ("tmem_ld32", "tmem_ld16", "tmem_ld8", "tmem_st16", "tmem_st8", "tmem_wait_ld")
+    monkeypatch.setattr(lint, "TC_CALLS", lint.TC_CALLS + tmem[:5])
     monkeypatch.setattr(lint, "TMEM_TOUCH", lint.TMEM_TOUCH + tmem)
 
 
@@ -34,12 +34,16 @@ def test_the_lint_reads_the_kernel():
 
 
 MUTANTS = {
-    "no_fence_after_s_full_wait": ("mbar_wait(bar_sfull + 8 * u", "fence_after();", True, "A"),
+    "no_fence_after_s_full_wait": ("// No row of this warp's", "fence_after();", True, "A"),
+    "no_fence_after_rescale_wait": ("// A row's two threads scale", "fence_after();", True, "A"),
+    "no_fence_after_maxima_wait": ("tmem_st8(lanes + col_o(s) + d0, o);", "fence_after();", True, "A"),
     "no_fence_after_merge_wait": ("mbar_wait(bar_xch", "fence_after();", True, "A"),
-    "no_fence_before_p_handover": ("mbar_arrive(bar_pfull + 8 * u)", "fence_before();", False, "B"),
-    "no_fence_before_o_free": ("mbar_arrive(bar_ofree + 8 * lane)", "fence_before();", False, "B"),
-    "no_fence_after_k_tile_wait": ("// S and P share their columns: the last P V", "fence_after();", True, "A"),
-    "no_fence_after_p_full_wait": ("mbar_wait(bar_pfull + 8 * u", "fence_after();", True, "A"),
+    "no_fence_before_maxima": ("rmax = fmaxf(rmax, leave", "fence_before();", False, "B"),
+    "no_fence_before_p_handover": ("mbar_arrive(bar_pfull + 8 * turn);\n                ++k;\n            }",
+                                   "fence_before();", False, "B"),
+    "no_fence_before_o_free": ("mbar_arrive(bar_ofree + 8 * s)", "fence_before();", False, "B"),
+    "no_fence_after_buffer_wait": ("mbar_wait(bar_bfree + 8 * buf", "fence_after();", True, "A"),
+    "no_fence_after_p_full_wait": ("mbar_wait(bar_pfull + 8 * turn", "fence_after();", True, "A"),
     "no_fence_after_final_barrier": ("tcgen05.dealloc", "fence_after();", False, "A"),
 }
 
