@@ -136,8 +136,6 @@ constexpr size_t kWorkspace = kCutBytes + kPartRows * (sizeof(float2) + kD * siz
 
 struct Plan {
     long long prefix[kMaxRequests + 1];  // where request r's items begin on the line
-    int32_t n[kMaxRequests];             // its new tokens
-    int32_t ctx[kMaxRequests];           // its cached tokens
     long long warp_sum[kMaxRequests / 64];
 };
 
@@ -148,27 +146,38 @@ __device__ __forceinline__ long long line_of(const ChunkParams &p, long long bas
     return pairs * (base + kOverhead) + own;
 }
 
-// All threads; syncs.  The first 512 take two requests each.  Lengths the
-// kernel cannot use are clamped and flagged.
+// A request's first row, new and cached tokens, clamped to what the call has
+// room for; true when nothing had to be.
+struct Request {
+    int row, n, ctx;
+    __device__ __forceinline__ bool fetch(const ChunkParams &p, int r) {
+        const int a = __ldg(p.cu_seqlens + r), b = __ldg(p.cu_seqlens + r + 1), c = __ldg(p.ctx_lens + r);
+        const int cap = p.page_stride * kP;
+        row = min(max(a, 0), p.T);
+        n = min(max(b, row), p.T) - row;
+        ctx = min(max(c, 0), cap);
+        const bool fits = p.mask == K3DA_MASK_CONTEXT || static_cast<long long>(ctx) + n <= cap;
+        return a == row && b == row + n && (n == 0 || (c == ctx && fits));
+    }
+    __device__ __forceinline__ int pairs(const ChunkParams &p) const { return (n + 2 * p.tpt - 1) / (2 * p.tpt); }
+    // Keys of the line before a causal chunk's own.
+    __device__ __forceinline__ long long base(const ChunkParams &p) const {
+        return static_cast<long long>(ctx) + (p.mask == K3DA_MASK_FULL ? n : 0);
+    }
+};
+
+// All threads; syncs.  The first 512 take two requests each.
 __device__ void build_plan(const ChunkParams &p, Plan *pl, bool report) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const bool mine = t < kMaxRequests / 2;
-    const int cap = p.page_stride * kP;
     long long cost[2] = {0, 0};
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const int r = 2 * t + k;
         if (!mine || r >= p.R) continue;
-        const int a = __ldg(p.cu_seqlens + r), b = __ldg(p.cu_seqlens + r + 1), c = __ldg(p.ctx_lens + r);
-        const int begin = min(max(a, 0), p.T), end = min(max(b, begin), p.T), n = end - begin;
-        const int ctx = min(max(c, 0), cap);
-        const bool fits = p.mask == K3DA_MASK_CONTEXT || static_cast<long long>(ctx) + n <= cap;
-        if (report && p.status && (a != begin || b != end || (n > 0 && (c != ctx || !fits))))
-            atomicOr(p.status, K3DA_STATUS_BAD_LENGTH);
-        pl->n[r] = n;
-        pl->ctx[r] = ctx;
-        const long long base = static_cast<long long>(ctx) + (p.mask == K3DA_MASK_FULL ? n : 0);
-        cost[k] = p.Hkv * line_of(p, base, (n + 2 * p.tpt - 1) / (2 * p.tpt));
+        Request q;
+        if (!q.fetch(p, r) && report && p.status) atomicOr(p.status, K3DA_STATUS_BAD_LENGTH);
+        cost[k] = p.Hkv * line_of(p, q.base(p), q.pairs(p));
     }
     long long sum = cost[0] + cost[1];
 #pragma unroll
@@ -235,19 +244,13 @@ struct Walk {
     long long at;             // where the next item begins
     long long start, length;  // the last item
     int r, h, pair;
+    Request q;  // r's
 
     // Start of slice c: ceil(c * total / slices), without a wide product.
     __device__ __forceinline__ long long slice(long long c) const {
         const long long q = total / slices, rem = total - q * slices;
         return c * q + (c * rem + slices - 1) / slices;
     }
-    __device__ __forceinline__ static long long base(const ChunkParams &p, const Plan *pl, int rr) {
-        return static_cast<long long>(pl->ctx[rr]) + (p.mask == K3DA_MASK_FULL ? pl->n[rr] : 0);
-    }
-    __device__ __forceinline__ static int pairs(const ChunkParams &p, const Plan *pl, int rr) {
-        return (pl->n[rr] + 2 * p.tpt - 1) / (2 * p.tpt);
-    }
-
     __device__ void begin(const ChunkParams &p, const Plan *pl, int cta) {
         total = pl->prefix[p.R];
         slices = total / kMinSlice;
@@ -264,12 +267,13 @@ struct Walk {
             else b = mid;
         }
         r = a;
-        const long long keys = base(p, pl, r);
-        const long long head = line_of(p, keys, pairs(p, pl, r));
+        q.fetch(p, r);
+        const long long keys = q.base(p);
+        const long long head = line_of(p, keys, q.pairs(p));
         long long rest = lo - pl->prefix[r];
         h = static_cast<int>(rest / head);
         rest -= h * head;
-        int x = 0, y = pairs(p, pl, r);
+        int x = 0, y = q.pairs(p);
         while (y - x > 1) {
             const int mid = (x + y) >> 1;
             if (line_of(p, keys, mid) <= rest) x = mid;
@@ -285,22 +289,22 @@ struct Walk {
         return offset <= kOverhead ? 0 : t < nt ? static_cast<int>(t) : nt;
     }
 
-    __device__ bool next(const ChunkParams &p, const Plan *pl, Piece &it) {
+    __device__ bool next(const ChunkParams &p, Piece &it) {
         while (at < hi) {
             it.r = r;
             it.h = h;
-            it.ctx = pl->ctx[r];
-            it.n = pl->n[r];
+            it.ctx = q.ctx;
+            it.n = q.n;
             it.tok0 = pair * 2 * p.tpt;
             it.tokens = min(2 * p.tpt, it.n - it.tok0);
-            it.row = min(max(__ldg(p.cu_seqlens + r), 0), p.T) + it.tok0;
+            it.row = q.row + it.tok0;
             it.alt = it.tokens <= p.tpt;
             it.limit = keys_seen(p, it.ctx, it.n, it.tok0 + it.tokens - 1);
             it.nt = static_cast<int>((static_cast<long long>(it.limit) + kTile - 1) / kTile);
             it.keys0 = keys_seen(p, it.ctx, it.n, it.tok0 + min(p.tpt, it.tokens) - 1);
             start = at;
-            const int count = pairs(p, pl, r);
-            const long long keys = base(p, pl, r);
+            const int count = q.pairs(p);
+            const long long keys = q.base(p);
             length = line_of(p, keys, pair + 1) - line_of(p, keys, pair);
             it.t0 = lo <= at ? 0 : tile_at(lo - at, it.nt);
             it.t1 = hi >= at + length ? it.nt : tile_at(hi - at, it.nt);
@@ -309,8 +313,10 @@ struct Walk {
                 pair = 0;
                 if (++h == p.Hkv) {
                     h = 0;
-                    do ++r;
-                    while (r < p.R && pl->n[r] == 0);
+                    while (++r < p.R) {
+                        q.fetch(p, r);
+                        if (q.n > 0) break;
+                    }
                 }
             }
             if (it.t0 < it.t1 || (it.nt == 0 && start >= lo)) return true;
@@ -356,9 +362,9 @@ struct Smem {
     static constexpr int kPlan = kRawOff + kRaw * kRawBytes;
     static constexpr int kRec = kPlan + static_cast<int>(sizeof(Plan));
     static constexpr int kXch = kRec + kRecords * static_cast<int>(sizeof(Records));
-    static constexpr int kPieces = kXch + (3 * kGroups + 1) * kSlotRows * 4;
+    static constexpr int kPieces = kXch + (5 * kGroups + 1) * kSlotRows * 4;
     static constexpr int kBars = kPieces + kRing * static_cast<int>(sizeof(Piece));
-    static constexpr int kNumBars = 3 * kStages + 2 * kRaw + 2 * kRing + 4 + 7 * kBufs + 2 * 3 + 2;
+    static constexpr int kNumBars = 3 * kStages + 2 * kRaw + 2 * kRing + 4 + 7 * kBufs + 2 * 2 + 2;
     static constexpr int kTail = kBars + kNumBars * 8;  // TMEM address, abort flag
     static constexpr int kBytes = kTail + 16 + 1024;
     static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
@@ -404,8 +410,10 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
     uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // 1 KB aligned, and still known to be shared memory
     Plan *pl = reinterpret_cast<Plan *>(smem + L::kPlan);
     Records *recs = reinterpret_cast<Records *>(smem + L::kRec);
-    float *xmax = reinterpret_cast<float *>(smem + L::kXch);  // [2][kGroups][128] a page's row maxima, by tile parity
-    float *xl = xmax + 2 * kGroups * kSlotRows;               // [kGroups][128] a page's share of the row sums
+    // [2][kGroups][128] a page's row maximum and, above it, the tile it is of
+    // (by the slot's count of tiles, and its parity).
+    volatile unsigned long long *xmax = reinterpret_cast<unsigned long long *>(smem + L::kXch);
+    float *xl = reinterpret_cast<float *>(smem + L::kXch) + 4 * kGroups * kSlotRows;  // [kGroups][128] shares of the row sums
     float *xm = xl + kGroups * kSlotRows;                     // [128] slot 1's base of the exponents
     Piece *pieces = reinterpret_cast<Piece *>(smem + L::kPieces);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kTail + 8);
@@ -427,8 +435,7 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
     const uint32_t bar_pfull = bar_sfull + 16 * kBufs;      // [2][kBufs] P written
     const uint32_t bar_bfree = bar_pfull + 16 * kBufs;      // [kBufs] P of the buffer read
     const uint32_t bar_pvdone = bar_bfree + 8 * kBufs;      // [2][kBufs] a slot's P V complete
-    const uint32_t bar_max = bar_pvdone + 16 * kBufs;       // [2] both pages' maxima left
-    const uint32_t bar_ofree = bar_max + 16;                // [2] an item's O read
+    const uint32_t bar_ofree = bar_pvdone + 16 * kBufs;     // [2] an item's O read
     const uint32_t bar_sums = bar_ofree + 16;               // [2] both pages' row sums left
     const uint32_t bar_xch = bar_sums + 16;                 // slot 1's half of an alternate item is ready
     const uint32_t bar_done = bar_xch + 8;                  // every issuer's products are complete
@@ -452,7 +459,6 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
         for (int s = 0; s < 2; ++s) {
             mbar_init(bar_qfull + 8 * s, 1);
             mbar_init(bar_qempty + 8 * s, 1);
-            mbar_init(bar_max + 8 * s, 8);
             mbar_init(bar_ofree + 8 * s, 8);
             mbar_init(bar_sums + 8 * s, 8);
         }
@@ -467,6 +473,7 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     for (int e = threadIdx.x; e < kRecords; e += kThreads) recs[e].piece = -1;
+    for (int e = threadIdx.x; e < 2 * kGroups * kSlotRows; e += kThreads) xmax[e] = ~0ull;  // of no tile
     for (int e = threadIdx.x; e < kRecords * 3 * kD; e += kThreads)
         (&recs[e / (3 * kD)].first[0][0])[e % (3 * kD)] = 0xffffffffu;
     if (warp == kLoadWarp) {
@@ -500,7 +507,7 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
                     break;
                 }
                 Piece &it = pieces[slot];
-                const bool more = walk.next(p, pl, it);
+                const bool more = walk.next(p, it);
                 if (!more) it.row = -1;
                 it.seq = seq;
                 it.base = base;
@@ -547,6 +554,7 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
         const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
         const int ti = rho / p.G, gi = rho - ti * p.G;
         int k = 0;       // tiles of this slot so far
+        uint32_t turn = 0, round = 0;  // k % kBufs, k / kBufs mod 2
         int sums = 0;    // pieces with tiles for it so far
         int merges = 0;  // alternate pieces with tiles for both slots so far
         for (int n = 0; alive; ++n) {
@@ -560,29 +568,33 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
             const int sees = row_valid ? keys_seen(p, it.ctx, it.n, it.tok0 + token) : 0;
             const int least = keys_seen(p, it.ctx, it.n, it.tok0 + (alt ? 0 : s * p.tpt));  // ... of the slot's rows
             const int from = it.from(s), t_end = it.end(s), step = it.step();
+            const bool mine = from < t_end;
             float m = -INFINITY, l = 0.f;
+            const int shared_end = alt ? 0 : it.end(0);
+            uint32_t buf = mine ? static_cast<uint32_t>(it.step_of(s, from)) % kBufs : 0;
             for (int t = from; t < t_end; t += step) {
-                const uint32_t round = static_cast<uint32_t>(k) / kBufs, turn = s * kBufs + k - round * kBufs;
-                if (!mbar_wait(bar_sfull + 8 * turn, round & 1, abort_flag, p.status)) {
+                if (!mbar_wait(bar_sfull + 8 * (s * kBufs + turn), round, abort_flag, p.status)) {
                     alive = false;
                     break;
                 }
+                const uint32_t pfull = bar_pfull + 8 * (s * kBufs + turn);
+                const uint32_t cols = lanes + col_s(buf) + kP * page;
+                // The slot's next tile is two steps on, but one where slot 0
+                // has none in between.
+                buf += s == 0 || alt || t + 1 < shared_end ? 2 : 1;
+                if (buf >= kBufs) buf -= kBufs;
+                if (++turn == kBufs) {
+                    turn = 0;
+                    round ^= 1;
+                }
+                ++k;
                 if (!warp_valid) {
                     // No row of this warp's: it only keeps step.
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(bar_max + 8 * s);
-                        mbar_arrive(bar_pfull + 8 * turn);
-                    }
-                    if (!mbar_wait(bar_max + 8 * s, k & 1, abort_flag, p.status)) {
-                        alive = false;
-                        break;
-                    }
-                    ++k;
+                    if (lane == 0) mbar_arrive(pfull);
                     continue;
                 }
                 fence_after();
-                const uint32_t cols = lanes + col_s(static_cast<uint32_t>(it.step_of(s, t)) % kBufs) + kP * page;
                 const int key0 = t * kTile + kP * page;
                 uint32_t x[kP];
                 tmem_ld32(cols, x);
@@ -604,18 +616,26 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
                     for (int q = 0; q < 4; ++q)
                         mx[q] = fmax3(mx[q], __uint_as_float(x[j + q]), __uint_as_float(x[j + 4 + q]));
                 float rmax = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
-                // The row's other page: its maximum.  (A NaN is dropped here
-                // and not from the scores: it reaches the row's sum.)
-                float *leave = xmax + (k & 1) * kGroups * kSlotRows + rho;
-                leave[u * kSlotRows] = rmax;
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_max + 8 * s);
-                if (!mbar_wait(bar_max + 8 * s, k & 1, abort_flag, p.status)) {
-                    alive = false;
-                    break;
+                // The row's other page: its maximum.  A word of maximum and
+                // tile number needs no barrier; the warp that has the other
+                // page comes by at about the same time.  (A NaN is dropped
+                // here and not from the scores: it reaches the row's sum.)
+                {
+                    volatile unsigned long long *leave = xmax + (k & 1) * kGroups * kSlotRows + rho;
+                    leave[u * kSlotRows] = static_cast<unsigned long long>(k) << 32 | __float_as_uint(rmax);
+                    unsigned long long got = leave[(u ^ 1) * kSlotRows];
+                    if (static_cast<int>(got >> 32) != k) {
+                        const unsigned long long t0 = global_ns();
+                        do {
+                            got = leave[(u ^ 1) * kSlotRows];
+                        } while (static_cast<int>(got >> 32) != k && !*abort_flag && global_ns() - t0 < kWaitLimitNs);
+                        if (static_cast<int>(got >> 32) != k) {
+                            *abort_flag = 1;
+                            if (p.status) atomicOr(p.status, K3DA_STATUS_TIMEOUT);
+                        }
+                    }
+                    rmax = fmaxf(rmax, __uint_as_float(static_cast<uint32_t>(got)));
                 }
-                rmax = fmaxf(rmax, leave[(u ^ 1) * kSlotRows]);
                 // The base of the exponents follows the row's maximum only
                 // when that passes it by 2^8: P up to 256 is as exact, and O
                 // is left alone.
@@ -628,7 +648,7 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
                 if (__any_sync(kFull, need)) {
                     // A row's two threads scale one half of its O each, once
                     // the slot's last P V is complete.
-                    const uint32_t last = k - 1;
+                    const uint32_t last = k - 2;
                     if (!mbar_wait(bar_pvdone + 8 * (s * kBufs + last % kBufs), last / kBufs & 1, abort_flag, p.status)) {
                         alive = false;
                         break;
@@ -645,7 +665,6 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
                         tmem_st8(lanes + col_o(s) + d0, o);
                     }
                 }
-                fence_after();
                 const unsigned long long sl2 = pack_f32x2(p.scale_log2, p.scale_log2);
                 const unsigned long long nm2 = pack_f32x2(-m_eff, -m_eff);
                 unsigned long long sum[2] = {0ull, 0ull};
@@ -673,12 +692,10 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
                 tmem_wait_st();
                 fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar_pfull + 8 * turn);
-                ++k;
+                if (lane == 0) mbar_arrive(pfull);
             }
             if (!alive) break;
             // ------------------------------------------------- epilogue --
-            const bool mine = from < t_end;
             if (mine) {
                 const uint32_t last = k - 1;
                 if (!mbar_wait(bar_pvdone + 8 * (s * kBufs + last % kBufs), last / kBufs & 1, abort_flag, p.status)) break;

@@ -36,10 +36,8 @@ def test_the_lint_reads_the_kernel():
 MUTANTS = {
     "no_fence_after_s_full_wait": ("// No row of this warp's", "fence_after();", True, "A"),
     "no_fence_after_rescale_wait": ("// A row's two threads scale", "fence_after();", True, "A"),
-    "no_fence_after_maxima_wait": ("tmem_st8(lanes + col_o(s) + d0, o);", "fence_after();", True, "A"),
     "no_fence_after_merge_wait": ("mbar_wait(bar_xch", "fence_after();", True, "A"),
-    "no_fence_before_maxima": ("rmax = fmaxf(rmax, leave", "fence_before();", False, "B"),
-    "no_fence_before_p_handover": ("mbar_arrive(bar_pfull + 8 * turn);\n                ++k;\n            }",
+    "no_fence_before_p_handover": ("mbar_arrive(pfull);\n            }",
                                    "fence_before();", False, "B"),
     "no_fence_before_o_free": ("mbar_arrive(bar_ofree + 8 * s)", "fence_before();", False, "B"),
     "no_fence_after_buffer_wait": ("mbar_wait(bar_bfree + 8 * buf", "fence_after();", True, "A"),
