@@ -211,6 +211,7 @@ struct Piece {
     int t0, t1;
     int alt;     // one slot's worth of rows: the slots take the tiles in turn
     int seq;     // number of the piece among those with tiles
+    int q;       // where its Q is: slot 0's half of the Q room, and (bits 1, 2) how often the halves were filled before, mod 2
     int base;    // steps before it
     // The tiles of slot s: from, from + step, ... below end.
     __device__ __forceinline__ int from(int s) const { return alt ? t0 + s : t0; }
@@ -350,12 +351,13 @@ struct Records {
 
 template <bool QUANT>
 struct Smem {
-    static constexpr int kStages = QUANT ? 2 : 4;  // bf16 K/V tiles
+    static constexpr int kStages = QUANT ? 3 : 5;  // bf16 K/V tiles
     static constexpr int kRaw = QUANT ? 4 : 0;     // quantised tiles: K codes, V codes, K scales, V scales
     static constexpr int kRawBytes = 2 * kTile * kD + 2 * kTile;
     static constexpr int kStageBytes = 2 * kTile * kD * 2;
     static constexpr int kVOff = kTile * kD * 2;
-    static constexpr int kQBytes = 2 * kSlotRows * kD * 2;  // of a piece; two pieces' Q
+    // Two halves: a shared item's slots, or two alternate items' Q in turn.
+    static constexpr int kQBytes = kSlotRows * kD * 2;
     static constexpr int kQ = 0;
     static constexpr int kKv = kQ + 2 * kQBytes;
     static constexpr int kRawOff = kKv + kStages * kStageBytes;
@@ -426,7 +428,7 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
     const uint32_t bar_rempty = bar_rfull + 8 * L::kRaw;    // [kRaw] ... and widened
     const uint32_t bar_piece = bar_rempty + 8 * L::kRaw;    // [kRing] piece published
     const uint32_t bar_pdone = bar_piece + 8 * kRing;       // [kRing] ... and read by everybody
-    const uint32_t bar_qfull = bar_pdone + 8 * kRing;       // [2] a piece's Q loaded
+    const uint32_t bar_qfull = bar_pdone + 8 * kRing;       // [2] a half of the Q room filled
     const uint32_t bar_qempty = bar_qfull + 16;             // [2] ... and read
     // A slot's k-th tile has the barriers k % 3 of its own three: each side
     // then waits for every phase of the barriers it waits on, and none can be
@@ -499,7 +501,8 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
             walk.begin(p, pl, blockIdx.x);
             Cut cut = {};
             const uint32_t box = static_cast<uint32_t>(p.G) * p.tpt * 128;
-            int seq = 0, base = 0;
+            int seq = 0, base = 0, half = 0;
+            uint32_t fills[2] = {0, 0};  // of each half of the Q room
             for (int n = 0; alive; ++n) {
                 const int slot = n % kRing;
                 if (!mbar_wait(bar_pdone + 8 * slot, ((n / kRing) & 1) ^ 1, abort_flag, p.status)) {
@@ -509,11 +512,16 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
                 Piece &it = pieces[slot];
                 const bool more = walk.next(p, it);
                 if (!more) it.row = -1;
+                const bool tiles = more && it.t0 < it.t1;
+                const int alt = it.alt, h = it.h, row = it.row;
+                half = alt ? half ^ 1 : 0;
                 it.seq = seq;
                 it.base = base;
-                const bool tiles = more && it.t0 < it.t1;
-                if (tiles) base += it.steps();
-                const int alt = it.alt, h = it.h, row = it.row;
+                it.q = half | (fills[0] & 1) << 1 | (fills[1] & 1) << 2;
+                if (tiles) {
+                    base += it.steps();
+                    ++seq;
+                }
                 if (more && it.t0 > 0) cut.has[0] = 1;
                 if (tiles && it.t0 == 0 && it.t1 < it.nt) {
                     cut.has[1] = 1;
@@ -525,23 +533,29 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
                 mbar_arrive(bar_piece + 8 * slot);
                 if (!more) break;
                 if (!tiles) continue;
-                const int b = seq & 1;
-                if (!mbar_wait(bar_qempty + 8 * b, ((seq >> 1) & 1) ^ 1, abort_flag, p.status)) {
-                    alive = false;
-                    break;
+                for (int s = 0; s < 2 && alive; ++s) {
+                    if (alt && s != half) continue;
+                    const uint32_t full = bar_qfull + 8 * s;
+                    const uint32_t n_fills = s ? fills[1] : fills[0];
+                    if (!mbar_wait(bar_qempty + 8 * s, (n_fills & 1) ^ 1, abort_flag, p.status)) {
+                        alive = false;
+                        break;
+                    }
+                    if (s) ++fills[1];
+                    else ++fills[0];
+                    mbar_arrive_expect_tx(full, box);
+                    tma_load_3d(smem_u32(smem + L::kQ) + s * L::kQBytes, &q_map, 0, h * p.G,
+                                row + (alt ? 0 : s * p.tpt), full);
                 }
-                const uint32_t dst = smem_u32(smem + L::kQ) + b * L::kQBytes;
-                mbar_arrive_expect_tx(bar_qfull + 8 * b, alt ? box : 2 * box);
-                tma_load_3d(dst, &q_map, 0, h * p.G, row, bar_qfull + 8 * b);
-                if (!alt) tma_load_3d(dst + kSlotRows * 128, &q_map, 0, h * p.G, row + p.tpt, bar_qfull + 8 * b);
-                ++seq;
             }
             p.cuts[blockIdx.x] = cut;
             // Loads in flight land before the CTA leaves (a wait gave up).
             if (!alive) {
-                for (int j = seq > 2 ? seq - 2 : 0; j < seq; ++j) {
+                for (int s = 0; s < 2; ++s) {
+                    const uint32_t n_fills = s ? fills[1] : fills[0];
                     const unsigned long long t0 = global_ns();
-                    while (!mbar_try_wait(bar_qfull + 8 * (j & 1), (j >> 1) & 1) && global_ns() - t0 < kWaitLimitNs) {
+                    while (n_fills > 0 && !mbar_try_wait(bar_qfull + 8 * s, (n_fills - 1) & 1) &&
+                           global_ns() - t0 < kWaitLimitNs) {
                     }
                 }
             }
@@ -899,9 +913,12 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
             if (it.row < 0) break;
             const int t0 = it.t0, t1 = it.t1, alt = it.alt;
             const int from = it.from(s), t_end = it.end(s), step = it.step();
-            const int qb = it.seq & 1;
-            const uint64_t qd = desc_sw128(smem_u32(smem + L::kQ) + qb * L::kQBytes);
-            if (is_qk && t0 < t1 && !mbar_wait(bar_qfull + 8 * qb, (it.seq >> 1) & 1, abort_flag, p.status)) break;
+            const int half = it.q & 1;
+            const uint64_t qd = desc_sw128(smem_u32(smem + L::kQ) + half * L::kQBytes);
+            if (is_qk && t0 < t1) {
+                if ((!alt || half == 0) && !mbar_wait(bar_qfull, it.q >> 1 & 1, abort_flag, p.status)) break;
+                if ((!alt || half == 1) && !mbar_wait(bar_qfull + 8, it.q >> 2 & 1, abort_flag, p.status)) break;
+            }
             items += from < t_end;
             int next = from;  // the slot's next tile
             uint32_t i = it.base;
@@ -923,7 +940,7 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
                         }
                         fence_after();
                         if (issuer) {
-                            const uint64_t q = qd + (alt ? 0 : (slot * kSlotRows * 128) >> 4);
+                            const uint64_t q = qd + (alt ? 0 : (slot * L::kQBytes) >> 4);
 #pragma unroll
                             for (int kk = 0; kk < kD / 16; ++kk)
                                 mma_ss(tmem + col_s(buf), q + ((kk * 32) >> 4), kd + ((kk * 32) >> 4), kIdescQK,
@@ -970,7 +987,10 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
             if (is_qk && t0 < t1) {
                 // Q is free once the products that read it are complete.
                 fence_after();
-                if (issuer) mma_commit(bar_qempty + 8 * qb);
+                if (issuer) {
+                    mma_commit(bar_qempty + 8 * half);
+                    if (!alt) mma_commit(bar_qempty + 8);
+                }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_pdone + 8 * (n % kRing));
@@ -1005,40 +1025,54 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
                         alive = false;
                         break;
                     }
-                    // 1024 pieces of 16 codes (K's 512, then V's), four a row.
-#pragma unroll 2
-                    for (int c = tid; c < 1024; c += 32 * kPrepWarps) {
-                        const uint4 w = *reinterpret_cast<const uint4 *>(raw + c * 16);
-                        const uint32_t b = raw[2 * kTile * kD + (c >> 2)];
-                        const bool is_v = c >= 512;
-                        const int row = (c & 511) >> 2, quarter = c & 3;
-                        // 2^120 times the scale, in two factors where it
-                        // passes bf16's range (rows above 448 * 2^7).
-                        const uint32_t e1 = b <= 134u ? b + 120u : 254u;
-                        const uint32_t mul = e1 << 7 | e1 << 23;
-                        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-                        uint32_t o[8];
+                    // 1024 pieces of 16 codes (K's 512, then V's), four a
+                    // row; loads of a few of them first.
+                    constexpr int kStep = 32 * kPrepWarps, kBatch = 3;
+                    for (int c0 = tid; c0 < 1024; c0 += kBatch * kStep) {
+                        uint4 w[kBatch];
+                        uint32_t sc[kBatch];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            o[2 * q] = mul_bf16x2(widen2(__byte_perm(in[q], 0, 0x1404)), mul);
-                            o[2 * q + 1] = mul_bf16x2(widen2(__byte_perm(in[q], 0, 0x3424)), mul);
+                        for (int e = 0; e < kBatch; ++e) {
+                            const int c = c0 + e * kStep;
+                            if (c >= 1024) break;
+                            w[e] = *reinterpret_cast<const uint4 *>(raw + c * 16);
+                            sc[e] = raw[2 * kTile * kD + (c >> 2)];
                         }
-                        const int key = t * kTile + row;
-                        if (b > 134u || (is_v && key >= limit)) {
-                            const uint32_t mul2 = (b - 7u) << 7 | (b - 7u) << 23;
-                            const bool hidden = is_v && (key >= limit || (b == 255u && key >= least));
 #pragma unroll
-                            for (int q = 0; q < 8; ++q)
-                                o[q] = hidden ? 0u : b == 255u ? 0x7fff7fffu : mul_bf16x2(o[q], mul2);
-                            if (hidden && key < limit) {
-                                for (int d = 0; d < 16; ++d)
-                                    atomicMin(&rec->first[2][quarter * 16 + d], tag | (key - least));
-                                rec->piece = piece;
+                        for (int e = 0; e < kBatch; ++e) {
+                            const int c = c0 + e * kStep;
+                            if (c >= 1024) break;
+                            const uint32_t b = sc[e];
+                            const bool is_v = c >= 512;
+                            const int row = (c & 511) >> 2, quarter = c & 3;
+                            // 2^120 times the scale, in two factors where it
+                            // passes bf16's range (rows above 448 * 2^7).
+                            const uint32_t e1 = b <= 134u ? b + 120u : 254u;
+                            const uint32_t mul = e1 << 7 | e1 << 23;
+                            const uint32_t in[4] = {w[e].x, w[e].y, w[e].z, w[e].w};
+                            uint32_t o[8];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                o[2 * q] = mul_bf16x2(widen2(__byte_perm(in[q], 0, 0x1404)), mul);
+                                o[2 * q + 1] = mul_bf16x2(widen2(__byte_perm(in[q], 0, 0x3424)), mul);
                             }
+                            const int key = t * kTile + row;
+                            if (b > 134u || (is_v && key >= limit)) {
+                                const uint32_t mul2 = (b - 7u) << 7 | (b - 7u) << 23;
+                                const bool hidden = is_v && (key >= limit || (b == 255u && key >= least));
+#pragma unroll
+                                for (int q = 0; q < 8; ++q)
+                                    o[q] = hidden ? 0u : b == 255u ? 0x7fff7fffu : mul_bf16x2(o[q], mul2);
+                                if (hidden && key < limit) {
+                                    for (int d = 0; d < 16; ++d)
+                                        atomicMin(&rec->first[2][quarter * 16 + d], tag | (key - least));
+                                    rec->piece = piece;
+                                }
+                            }
+                            uint8_t *dst = kt + (is_v ? L::kVOff : 0);
+                            *reinterpret_cast<uint4 *>(dst + swz(row, 2 * quarter)) = make_uint4(o[0], o[1], o[2], o[3]);
+                            *reinterpret_cast<uint4 *>(dst + swz(row, 2 * quarter + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
                         }
-                        uint8_t *dst = kt + (is_v ? L::kVOff : 0);
-                        *reinterpret_cast<uint4 *>(dst + swz(row, 2 * quarter)) = make_uint4(o[0], o[1], o[2], o[3]);
-                        *reinterpret_cast<uint4 *>(dst + swz(row, 2 * quarter + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
                     }
                     fence_proxy_async();
                 } else {
