@@ -356,55 +356,86 @@ def alloc_cache(num_pages: int, num_kv_heads: int, *, quantised: bool = False, d
     return pool, torch.zeros(*shape, dtype=torch.uint8, device=device).view(torch.float8_e8m0fnu)
 
 
-def _on(device, **tensors):
-    """Every tensor is contiguous and on the cache's device."""
+def _on(dev, **tensors):
+    """Every tensor is contiguous and on device ``dev``."""
     for name, t in tensors.items():
-        if t is not None and (t.device != device or not t.is_contiguous()):
-            raise K3daError(f"{name} must be contiguous and on the cache's device ({device})")
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            raise K3daError(f"{name} must be contiguous and on the cache's device (cuda:{dev})")
 
 
 def _cache_args(kv_pool, kv_scales, page_table, lens, cu_seqlens, num_kv_heads, status):
-    """Checks a cache call's common tensors; returns the C arguments from
-    kv_pool to num_requests."""
-    if kv_pool.device.type != "cuda":
-        raise K3daError("kv_pool must be a CUDA tensor")
-    _on(kv_pool.device, kv_pool=kv_pool, kv_scales=kv_scales, page_table=page_table, lengths=lens,
-        cu_seqlens=cu_seqlens, status=status)
-    if kv_pool.dim() != 5 or tuple(kv_pool.shape[1:4]) != (2, num_kv_heads, 64):
+    """Checks a cache call's common tensors.  Returns the cache's device index,
+    head_dim and the C arguments from kv_pool to num_requests.  (Calls on
+    small inputs are bound by this code: it asks each tensor for no more than
+    it needs.)"""
+    dev = kv_pool.get_device()
+    if dev < 0 or not kv_pool.is_contiguous():
+        raise K3daError("kv_pool must be a contiguous CUDA tensor")
+    shape = kv_pool.shape
+    if len(shape) != 5 or shape[1] != 2 or shape[2] != num_kv_heads or shape[3] != 64:
         raise K3daError("kv_pool must be [pages, 2, Hkv, 64, 64]")
-    if kv_pool.dtype == torch.bfloat16:
+    dtype = kv_pool.dtype
+    scales = None
+    if dtype is torch.bfloat16:
         code = CACHE_BF16
         if kv_scales is not None:
             raise K3daError("a bf16 cache has no scales")
-    elif kv_pool.dtype == torch.float8_e4m3fn:
+    elif dtype is torch.float8_e4m3fn:
         code = CACHE_E4M3
-        if kv_scales is None or kv_scales.dtype != torch.float8_e8m0fnu or kv_scales.shape != kv_pool.shape[:-1]:
+        if kv_scales is None or kv_scales.dtype is not torch.float8_e8m0fnu or kv_scales.shape != shape[:-1]:
             raise K3daError("an e4m3 cache needs kv_scales [pages, 2, Hkv, 64] float8_e8m0fnu")
+        if kv_scales.get_device() != dev or not kv_scales.is_contiguous():
+            raise K3daError(f"kv_scales must be contiguous and on the cache's device (cuda:{dev})")
+        scales = kv_scales.data_ptr()
     else:
         raise K3daError("kv_pool must be bfloat16 or float8_e4m3fn")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2:
+    table_shape = page_table.shape
+    if page_table.dtype is not torch.int32 or len(table_shape) != 2:
         raise K3daError("page_table must be [R, S] int32")
-    R, S = page_table.shape
-    if lens.dtype != torch.int32 or lens.numel() != R or cu_seqlens.dtype != torch.int32 or cu_seqlens.numel() != R + 1:
+    R, S = table_shape
+    if lens.dtype is not torch.int32 or lens.numel() != R or cu_seqlens.dtype is not torch.int32 or \
+            cu_seqlens.numel() != R + 1:
         raise K3daError("lengths must be [R] and cu_seqlens [R + 1], both int32")
-    if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
-        raise K3daError("status must be an int32 CUDA tensor")
-    return [_ptr(kv_pool), code, _ptr(kv_scales), kv_pool.shape[0], _ptr(page_table), S, _ptr(lens),
-            _ptr(cu_seqlens), R]
+    for t in (page_table, lens, cu_seqlens):
+        if t.get_device() != dev or not t.is_contiguous():
+            raise K3daError(f"page_table, lengths and cu_seqlens must be contiguous and on the cache's device (cuda:{dev})")
+    if status is not None:
+        _on(dev, status=status)
+        if status.dtype is not torch.int32 or status.numel() < 1:
+            raise K3daError("status must be an int32 CUDA tensor")
+    return dev, shape[4], (kv_pool.data_ptr(), code, scales, shape[0], page_table.data_ptr(), S, lens.data_ptr(),
+                           cu_seqlens.data_ptr(), R)
 
 
-def _device_stream(device, stream):
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _enqueue(what, dev, stream, status, *args):
+    """Calls the library's ``what`` with ``args``, the status word and the
+    stream, on device ``dev``."""
+    fn = getattr(_lib or load_library(), what)
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device.index == dev:
+        handle = stream.cuda_stream
+    else:
         raise K3daError("stream must be one of the cache's device")
-    return ctypes.c_void_p(stream.cuda_stream)
+    if torch.cuda.current_device() == dev:
+        rc = fn(*args, _addr(status), handle)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _addr(status), handle)
+    if rc != OK:
+        _check(rc, what)
 
 
-def _qkv_rows(qkv, num_q_heads, num_kv_heads, D):
-    if qkv.dtype != torch.bfloat16 or qkv.dim() != 2 or qkv.shape[1] != (num_q_heads + 2 * num_kv_heads) * D:
-        raise K3daError("qkv must be [T, (Hq+2Hkv)*64] bf16")
-    return qkv.shape[0]
+def _qkv_rows(qkv, num_q_heads, num_kv_heads, D, dev):
+    shape = qkv.shape
+    if qkv.dtype is not torch.bfloat16 or len(shape) != 2 or shape[1] != (num_q_heads + 2 * num_kv_heads) * D or \
+            qkv.get_device() != dev or not qkv.is_contiguous():
+        raise K3daError("qkv must be [T, (Hq+2Hkv)*64] bf16, contiguous and on the cache's device")
+    return shape[0]
 
 
 def k3da_kv_append(kv_pool, qkv, page_table, ctx_lens, cu_seqlens, *, num_q_heads: int, num_kv_heads: int,
@@ -412,14 +443,9 @@ def k3da_kv_append(kv_pool, qkv, page_table, ctx_lens, cu_seqlens, *, num_q_head
     """Write the k and v heads of the packed rows ``qkv`` (k already
     normalised and roped) into the paged cache at tokens ``ctx_lens[r] + i``
     (C: k3da_kv_append).  Returns ``kv_pool``."""
-    args = _cache_args(kv_pool, kv_scales, page_table, ctx_lens, cu_seqlens, num_kv_heads, status)
-    D = kv_pool.shape[-1]
-    T = _qkv_rows(qkv, num_q_heads, num_kv_heads, D)
-    _on(kv_pool.device, qkv=qkv)
-    with torch.cuda.device(kv_pool.device):
-        rc = load_library().k3da_kv_append(*args, _ptr(qkv), T, num_q_heads, num_kv_heads, D, _ptr(status),
-                                           _device_stream(kv_pool.device, stream))
-    _check(rc, "k3da_kv_append")
+    dev, D, args = _cache_args(kv_pool, kv_scales, page_table, ctx_lens, cu_seqlens, num_kv_heads, status)
+    T = _qkv_rows(qkv, num_q_heads, num_kv_heads, D, dev)
+    _enqueue("k3da_kv_append", dev, stream, status, *args, qkv.data_ptr(), T, num_q_heads, num_kv_heads, D)
     return kv_pool
 
 
@@ -429,24 +455,25 @@ def k3da_kv_append_qknorm(kv_pool, qkv, page_table, ctx_lens, cu_seqlens, positi
     """``k3da_kv_append`` of raw k: RMSNorm + NeoX RoPE (with ``yarn``, YaRN
     RoPE) on the way into the cache, and of q into ``q_out`` [T, Hq*64] when
     given (C: k3da_kv_append_qknorm).  Returns ``kv_pool``."""
-    args = _cache_args(kv_pool, kv_scales, page_table, ctx_lens, cu_seqlens, num_kv_heads, status)
-    D = kv_pool.shape[-1]
-    T = _qkv_rows(qkv, num_q_heads, num_kv_heads, D)
-    _on(kv_pool.device, qkv=qkv, positions=positions, q_norm_w=q_norm_w, k_norm_w=k_norm_w, q_out=q_out)
-    if positions.dtype not in (torch.int32, torch.int64) or positions.numel() != T:
+    dev, D, args = _cache_args(kv_pool, kv_scales, page_table, ctx_lens, cu_seqlens, num_kv_heads, status)
+    T = _qkv_rows(qkv, num_q_heads, num_kv_heads, D, dev)
+    _on(dev, positions=positions, q_norm_w=q_norm_w, k_norm_w=k_norm_w, q_out=q_out)
+    if positions.dtype is torch.int64:
+        code = POS_I64
+    elif positions.dtype is torch.int32:
+        code = POS_I32
+    else:
         raise K3daError("positions must be [T] int32 or int64")
-    if q_norm_w.dtype != torch.bfloat16 or k_norm_w.dtype != torch.bfloat16 or \
+    if positions.numel() != T:
+        raise K3daError("positions must be [T] int32 or int64")
+    if q_norm_w.dtype is not torch.bfloat16 or k_norm_w.dtype is not torch.bfloat16 or \
             q_norm_w.numel() != D or k_norm_w.numel() != D:
         raise K3daError("norm weights must be [64] bf16")
-    if q_out is not None and (q_out.dtype != torch.bfloat16 or tuple(q_out.shape) != (T, num_q_heads * D)):
+    if q_out is not None and (q_out.dtype is not torch.bfloat16 or q_out.shape != (T, num_q_heads * D)):
         raise K3daError("q_out must be [T, Hq*64] bf16")
-    with torch.cuda.device(kv_pool.device):
-        rc = load_library().k3da_kv_append_qknorm(
-            *args, _ptr(qkv), T, num_q_heads, num_kv_heads, D, _ptr(positions),
-            POS_I64 if positions.dtype == torch.int64 else POS_I32, _ptr(q_norm_w), _ptr(k_norm_w), float(eps),
-            float(rope_base), None if yarn is None else ctypes.byref(yarn), _ptr(q_out), _ptr(status),
-            _device_stream(kv_pool.device, stream))
-    _check(rc, "k3da_kv_append_qknorm")
+    _enqueue("k3da_kv_append_qknorm", dev, stream, status, *args, qkv.data_ptr(), T, num_q_heads, num_kv_heads, D,
+             positions.data_ptr(), code, q_norm_w.data_ptr(), k_norm_w.data_ptr(), eps, rope_base,
+             None if yarn is None else ctypes.byref(yarn), _addr(q_out))
     return kv_pool
 
 
@@ -455,17 +482,13 @@ def k3da_kv_gather(k_out, v_out, kv_pool, page_table, starts, cu_seqlens, *, num
     """Read cache tokens ``starts[r] + i`` back into the packed rows of
     ``k_out`` and ``v_out`` [T, Hkv*64] bf16 (C: k3da_kv_gather).  Returns
     both."""
-    args = _cache_args(kv_pool, kv_scales, page_table, starts, cu_seqlens, num_kv_heads, status)
-    D = kv_pool.shape[-1]
-    _on(kv_pool.device, k_out=k_out, v_out=v_out)
-    T = k_out.shape[0]
-    for t in (k_out, v_out):
-        if t.dtype != torch.bfloat16 or tuple(t.shape) != (T, num_kv_heads * D):
-            raise K3daError("k_out and v_out must be [T, Hkv*64] bf16")
-    with torch.cuda.device(kv_pool.device):
-        rc = load_library().k3da_kv_gather(_ptr(k_out), _ptr(v_out), *args, T, num_kv_heads, D, _ptr(status),
-                                           _device_stream(kv_pool.device, stream))
-    _check(rc, "k3da_kv_gather")
+    dev, D, args = _cache_args(kv_pool, kv_scales, page_table, starts, cu_seqlens, num_kv_heads, status)
+    _on(dev, k_out=k_out, v_out=v_out)
+    shape = k_out.shape
+    if k_out.dtype is not torch.bfloat16 or v_out.dtype is not torch.bfloat16 or len(shape) != 2 or \
+            shape[1] != num_kv_heads * D or v_out.shape != shape:
+        raise K3daError("k_out and v_out must be [T, Hkv*64] bf16")
+    _enqueue("k3da_kv_gather", dev, stream, status, k_out.data_ptr(), v_out.data_ptr(), *args, shape[0], num_kv_heads, D)
     return k_out, v_out
 
 
@@ -492,25 +515,21 @@ def k3da_chunk_attn(out, q, kv_pool, page_table, ctx_lens, cu_seqlens, *, num_q_
     k3da_chunk_attn).  ``q`` [T, Hq*64] bf16 may be a view whose rows are
     further apart (``qkv[:, :Hq*64]``); ``mask`` is "causal", "full" or
     "context"; ``lse`` [T, Hq] fp32 is optional.  Returns ``out``."""
-    args = _cache_args(kv_pool, kv_scales, page_table, ctx_lens, cu_seqlens, num_kv_heads, status)
-    D = kv_pool.shape[-1]
-    device = kv_pool.device
-    if q.dtype != torch.bfloat16 or q.dim() != 2 or q.shape[1] != num_q_heads * D or q.device != device or \
-            (q.shape[0] and q.stride(1) != 1):
+    dev, D, args = _cache_args(kv_pool, kv_scales, page_table, ctx_lens, cu_seqlens, num_kv_heads, status)
+    shape = q.shape
+    if q.dtype is not torch.bfloat16 or len(shape) != 2 or shape[1] != num_q_heads * D or q.get_device() != dev or \
+            (shape[0] and q.stride(1) != 1):
         raise K3daError("q must be [T, Hq*64] bf16 on the cache's device, each row contiguous")
-    T = q.shape[0]
-    _on(device, out=out, lse=lse, workspace=workspace)
-    if out.dtype != torch.bfloat16 or tuple(out.shape) != (T, num_q_heads * D):
+    T = shape[0]
+    _on(dev, out=out, lse=lse, workspace=workspace)
+    if out.dtype is not torch.bfloat16 or out.shape != shape:
         raise K3daError("out must be [T, Hq*64] bf16")
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (T, num_q_heads)):
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (T, num_q_heads)):
         raise K3daError("lse must be [T, Hq] fp32")
-    if mask not in MASKS:
+    code = MASKS.get(mask)
+    if code is None:
         raise K3daError(f"mask must be one of {', '.join(MASKS)}")
-    row_stride = q.stride(0) if T > 1 else num_q_heads * D
-    with torch.cuda.device(device):
-        rc = load_library().k3da_chunk_attn(
-            _ptr(out), _ptr(lse), _ptr(q), row_stride, T, *args, num_q_heads, num_kv_heads, D, MASKS[mask],
-            float(softmax_scale), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
-            _device_stream(device, stream))
-    _check(rc, "k3da_chunk_attn")
+    _enqueue("k3da_chunk_attn", dev, stream, status, out.data_ptr(), _addr(lse), q.data_ptr(),
+             q.stride(0) if T > 1 else shape[1], T, *args, num_q_heads, num_kv_heads, D, code, softmax_scale,
+             workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out
