@@ -1,0 +1,304 @@
+// chunk_plan.cuh -- how the chunk attention's work is laid out and cut: its
+// parameters, the line of items, a CTA's pieces of it, and what pieces leave
+// for one another.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "cache_common.cuh"
+#include "k3da.h"
+
+namespace k3da_chunk {
+
+using namespace k3da_cache;
+
+constexpr int kCtas = 152;         // slices of the line at most: one CTA an SM
+constexpr int kTile = 128;         // keys of a tile: two pages
+constexpr int kSlotRows = 128;     // query rows of a slot
+constexpr int kOverhead = 128;     // an item's fixed cost, in keys
+constexpr int kMinSlice = 256;     // shortest slice, in keys
+
+struct ChunkParams {
+    __nv_bfloat16 *out;
+    float *lse;
+    const uint8_t *scales;
+    const int32_t *page_table;
+    const int32_t *ctx_lens;
+    const int32_t *cu_seqlens;
+    int32_t *status;
+    const __nv_bfloat16 *q;
+    long long q_stride;
+    struct Cut *cuts;
+    float2 *part_ml;  // [kCtas][2][part_rows] (m in log2 units, l)
+    float *part_o;    // [kCtas][2][part_rows][64]
+    long long num_pages;
+    int page_stride, R, T, Hq, Hkv;
+    int G;    // query heads per kv head
+    int tpt;  // tokens of a slot
+    int mask;
+    int pass;       // 0: the items of long chunks; 1: those of at most kSmallRows rows
+    int part_rows;  // rows of a partial result
+    float scale_log2;
+};
+
+// A request whose chunk is this small (query rows of a kv head) is the small
+// kernel's.
+constexpr int kSmallRows = 16;
+
+// What a CTA leaves for the combine kernel.  part 0: the piece it began with
+// belongs to an item begun before; part 1: the item it ended with goes on in
+// later CTAs, up to `last`.
+struct Cut {
+    int has[2];
+    int row;     // first row of the item that goes on
+    int tokens;  // its tokens
+    int head;    // its kv head
+    int last;
+    int pad[2];
+};
+static_assert(sizeof(Cut) == 32, "cuts are 32 bytes");
+constexpr size_t kCutBytes = 8192;
+static_assert(kCtas * sizeof(Cut) <= kCutBytes, "room for the cuts");
+// Workspace of a pass whose partial results have `rows` rows.
+constexpr size_t part_bytes(int rows) {
+    return kCutBytes + static_cast<size_t>(kCtas) * 2 * rows * (sizeof(float2) + kD * sizeof(float));
+}
+constexpr size_t kWorkspace = part_bytes(2 * kSlotRows) + part_bytes(kSmallRows);
+
+// -------------------------------------------------------------- the line --
+
+struct Plan {
+    long long prefix[kMaxRequests + 1];  // where request r's items begin on the line
+    long long warp_sum[16];
+};
+
+// Length of the first `pairs` items of one head: each sees `base` keys (and,
+// causal, its own tokens and the ones before) and costs kOverhead.
+__device__ __forceinline__ long long line_of(const ChunkParams &p, long long base, long long pairs) {
+    const long long own = p.mask == K3DA_MASK_CAUSAL ? p.tpt * pairs * (pairs + 1) : 0;  // 2 tpt (1 + 2 + ... + pairs)
+    return pairs * (base + kOverhead) + own;
+}
+
+// A request's first row, new and cached tokens, clamped to what the call has
+// room for; true when nothing had to be.
+struct Request {
+    int row, n, ctx;
+    __device__ __forceinline__ bool fetch(const ChunkParams &p, int r) {
+        const int a = __ldg(p.cu_seqlens + r), b = __ldg(p.cu_seqlens + r + 1), c = __ldg(p.ctx_lens + r);
+        const int cap = p.page_stride * kP;
+        row = min(max(a, 0), p.T);
+        n = min(max(b, row), p.T) - row;
+        ctx = min(max(c, 0), cap);
+        const bool fits = p.mask == K3DA_MASK_CONTEXT || static_cast<long long>(ctx) + n <= cap;
+        return a == row && b == row + n && (n == 0 || (c == ctx && fits));
+    }
+    // Items of one kv head in this pass.
+    __device__ __forceinline__ int pairs(const ChunkParams &p) const {
+        const bool small = n <= kSmallRows && n * p.G <= kSmallRows;
+        if (n == 0 || small != (p.pass == 1)) return 0;
+        return small ? 1 : (n + 2 * p.tpt - 1) / (2 * p.tpt);
+    }
+    // Keys of the line before a causal chunk's own.
+    __device__ __forceinline__ long long base(const ChunkParams &p) const {
+        return static_cast<long long>(ctx) + (p.mask == K3DA_MASK_FULL ? n : 0);
+    }
+};
+
+// All threads; syncs.  The first THREADS take two requests each at a time.
+template <int THREADS>
+__device__ __forceinline__ void build_plan(const ChunkParams &p, Plan *pl, bool report) {
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    if (t == 0) pl->prefix[0] = 0;
+    long long done = 0;
+    for (int r0 = 0; r0 < p.R; r0 += 2 * THREADS) {
+        const bool mine = t < THREADS;
+        long long cost[2] = {0, 0};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int r = r0 + 2 * t + k;
+            if (!mine || r >= p.R) continue;
+            Request q;
+            if (!q.fetch(p, r) && report && p.status) atomicOr(p.status, K3DA_STATUS_BAD_LENGTH);
+            cost[k] = p.Hkv * line_of(p, q.base(p), q.pairs(p));
+        }
+        long long sum = cost[0] + cost[1];
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long up = __shfl_up_sync(kFull, sum, off);
+            if (lane >= off) sum += up;
+        }
+        if (mine && lane == 31) pl->warp_sum[warp] = sum;
+        __syncthreads();
+        if (mine) {
+            long long before = done;
+            for (int w = 0; w < warp; ++w) before += pl->warp_sum[w];
+            const int r = r0 + 2 * t;
+            if (r + 1 <= p.R) pl->prefix[r + 1] = before + sum - cost[1];
+            if (r + 2 <= p.R) pl->prefix[r + 2] = before + sum;
+        }
+        __syncthreads();
+        done = pl->prefix[min(r0 + 2 * THREADS, p.R)];
+    }
+}
+
+// A piece: the tiles [t0, t1) of one item that fall into this CTA's slice.
+struct Piece {
+    int h;
+    int tok0;    // the item's first token in the chunk
+    int tokens;
+    int ctx, n, r;
+    int row;     // its first row; -1: no more pieces
+    int limit;   // keys its last row sees
+    int keys0;   // ... the last row of slot 0
+    int nt;      // tiles of the item
+    int t0, t1;
+    int alt;     // one slot's worth of rows: the slots take the tiles in turn
+    int seq;     // number of the piece among those with tiles
+    int q;       // where its Q is: slot 0's half of the Q room, and (bits 1, 2) how often the halves were filled before, mod 2
+    int base;    // steps (small kernel: pages) before it
+    // The tiles of slot s: from, from + step, ... below end.
+    __device__ __forceinline__ int from(int s) const { return alt ? t0 + s : t0; }
+    __device__ __forceinline__ int step() const { return alt ? 2 : 1; }
+    __device__ __forceinline__ int end(int s) const {
+        const int keys = alt || s == 1 ? limit : keys0;
+        return keys <= 0 ? 0 : min(t1, (keys - 1) / kTile + 1);
+    }
+    // The step of slot s's tile t: tile by tile, slot 0 first.
+    __device__ __forceinline__ int step_of(int s, int t) const {
+        const int d = t - t0;
+        if (alt) return base + d;
+        return base + d + (s == 0 ? d : min(d + 1, max(end(0) - t0, 0)));
+    }
+    __device__ __forceinline__ int steps() const { return t1 - t0 + (alt ? 0 : max(end(0) - t0, 0)); }
+};
+
+// Keys that the chunk's token i sees.
+__device__ __forceinline__ int keys_seen(const ChunkParams &p, int ctx, int n, int i) {
+    const long long c = p.mask == K3DA_MASK_CAUSAL ? static_cast<long long>(ctx) + i + 1
+                        : p.mask == K3DA_MASK_FULL ? static_cast<long long>(ctx) + n
+                                                   : ctx;
+    const int cap = p.page_stride * kP;
+    return c < cap ? static_cast<int>(c) : cap;
+}
+
+// The CTA's pieces, in order (the scheduler's).
+struct Walk {
+    long long lo, hi;         // the slice
+    long long total, slices;
+    long long at;             // where the next item begins
+    long long start, length;  // the last item
+    int r, h, pair;
+    Request q;  // r's
+
+    // Start of slice c: ceil(c * total / slices), without a wide product.
+    __device__ __forceinline__ long long slice(long long c) const {
+        const long long q = total / slices, rem = total - q * slices;
+        return c * q + (c * rem + slices - 1) / slices;
+    }
+    __device__ void begin(const ChunkParams &p, const Plan *pl, int cta) {
+        total = pl->prefix[p.R];
+        slices = total / kMinSlice;
+        slices = slices < 1 ? 1 : slices > kCtas ? kCtas : slices;
+        lo = hi = at = 0;
+        r = h = pair = 0;
+        if (cta >= slices || total == 0) return;
+        lo = slice(cta);
+        hi = slice(cta + 1);
+        int a = 0, b = p.R;
+        while (b - a > 1) {
+            const int mid = (a + b) >> 1;
+            if (pl->prefix[mid] <= lo) a = mid;
+            else b = mid;
+        }
+        r = a;
+        q.fetch(p, r);
+        const long long keys = q.base(p);
+        const long long head = line_of(p, keys, q.pairs(p));
+        long long rest = lo - pl->prefix[r];
+        h = static_cast<int>(rest / head);
+        rest -= h * head;
+        int x = 0, y = q.pairs(p);
+        while (y - x > 1) {
+            const int mid = (x + y) >> 1;
+            if (line_of(p, keys, mid) <= rest) x = mid;
+            else y = mid;
+        }
+        pair = x;
+        at = pl->prefix[r] + h * head + line_of(p, keys, pair);
+    }
+
+    // First tile of an item's part from `offset` (in the item) on.
+    __device__ __forceinline__ static int tile_at(long long offset, int nt) {
+        const long long t = (offset - kOverhead + kTile - 1) / kTile;
+        return offset <= kOverhead ? 0 : t < nt ? static_cast<int>(t) : nt;
+    }
+
+    __device__ bool next(const ChunkParams &p, Piece &it) {
+        while (at < hi) {
+            it.r = r;
+            it.h = h;
+            it.ctx = q.ctx;
+            it.n = q.n;
+            it.tok0 = pair * 2 * p.tpt;
+            it.tokens = min(2 * p.tpt, it.n - it.tok0);
+            it.row = q.row + it.tok0;
+            it.alt = it.tokens <= p.tpt;
+            it.limit = keys_seen(p, it.ctx, it.n, it.tok0 + it.tokens - 1);
+            it.nt = static_cast<int>((static_cast<long long>(it.limit) + kTile - 1) / kTile);
+            it.keys0 = keys_seen(p, it.ctx, it.n, it.tok0 + min(p.tpt, it.tokens) - 1);
+            start = at;
+            const int count = q.pairs(p);
+            const long long keys = q.base(p);
+            length = line_of(p, keys, pair + 1) - line_of(p, keys, pair);
+            it.t0 = lo <= at ? 0 : tile_at(lo - at, it.nt);
+            it.t1 = hi >= at + length ? it.nt : tile_at(hi - at, it.nt);
+            at += length;
+            if (++pair == count) {
+                pair = 0;
+                if (++h == p.Hkv) {
+                    h = 0;
+                    while (++r < p.R) {
+                        q.fetch(p, r);
+                        if (q.pairs(p) > 0) break;
+                    }
+                }
+            }
+            if (it.t0 < it.t1 || (it.nt == 0 && start >= lo)) return true;
+        }
+        return false;
+    }
+
+    // The slice that holds this position of the line.
+    __device__ int slice_of(long long pos) const {
+        int a = 0, b = static_cast<int>(slices);
+        while (b - a > 1) {
+            const int mid = (a + b) >> 1;
+            if (slice(mid) <= pos) a = mid;
+            else b = mid;
+        }
+        return a;
+    }
+};
+
+// What was taken out of a piece's V: for +inf, -inf and NaN and each dim,
+// ~piece (24 bits) over the first key that had one, counted from the keys
+// every row sees (8 bits: an item has at most 256 tokens).  atomicMin then
+// lets a later piece's entries replace an earlier one's: nothing is reset.
+struct Records {
+    uint32_t first[3][kD];
+    int piece;  // the last piece that left something here
+    int pad[3];
+};
+
+// Byte of 16-byte chunk `chunk` of a 128-byte row in a 128B-swizzled tile.
+__device__ __forceinline__ uint32_t swz(int row, int chunk) {
+    return static_cast<uint32_t>(row * 128 + ((chunk ^ (row & 7)) << 4));
+}
+
+// The small kernel (k3da_chunk_small.cu).  after_long: it follows the long
+// chunks' kernel on the stream and may start beside it.
+int launch_small(const ChunkParams &p, const void *kv_pool, bool quant, bool after_long, cudaStream_t stream);
+
+}  // namespace k3da_chunk

@@ -58,22 +58,18 @@
 
 #include <cmath>
 #include <cstring>
-#include <mutex>
 
 #include "cache_common.cuh"
+#include "chunk_plan.cuh"
 #include "k3da.h"
 #include "sm103.cuh"
+#include "tensor_maps.h"
 
 namespace {
 
-using namespace k3da_cache;
+using namespace k3da_chunk;
 using namespace sm103;
 
-constexpr int kCtas = 152;         // slices of the line at most: one CTA an SM
-constexpr int kTile = 128;         // keys of a tile: two pages
-constexpr int kSlotRows = 128;     // query rows of a slot
-constexpr int kOverhead = 128;     // an item's fixed cost, in keys
-constexpr int kMinSlice = 256;     // shortest slice, in keys
 constexpr int kGroups = 4;         // softmax warpgroups: u has slot u / 2, page u % 2 of its tiles
 constexpr int kRing = 4;           // pieces published ahead
 constexpr int kRecords = 8;        // pieces whose non-finite records are alive at once
@@ -96,258 +92,7 @@ constexpr uint32_t kTmemCols = 512u;
 constexpr uint32_t kIdescQK = idesc_f16(128, kTile, false);
 constexpr uint32_t kIdescPV = idesc_f16(128, kD, true);
 
-struct ChunkParams {
-    __nv_bfloat16 *out;
-    float *lse;
-    const uint8_t *scales;
-    const int32_t *page_table;
-    const int32_t *ctx_lens;
-    const int32_t *cu_seqlens;
-    int32_t *status;
-    struct Cut *cuts;
-    float2 *part_ml;  // [kCtas][2][256] (m in log2 units, l)
-    float *part_o;    // [kCtas][2][256][64]
-    long long num_pages;
-    int page_stride, R, T, Hq, Hkv;
-    int G;    // query heads per kv head
-    int tpt;  // tokens of a slot
-    int mask;
-    float scale_log2;
-};
-
-// What a CTA leaves for the combine kernel.  part 0: the piece it began with
-// belongs to an item begun before; part 1: the item it ended with goes on in
-// later CTAs, up to `last`.
-struct Cut {
-    int has[2];
-    int row;     // first row of the item that goes on
-    int tokens;  // its tokens
-    int head;    // its kv head
-    int last;
-    int pad[2];
-};
-static_assert(sizeof(Cut) == 32, "cuts are 32 bytes");
-constexpr size_t kCutBytes = 8192;
-static_assert(kCtas * sizeof(Cut) <= kCutBytes, "room for the cuts");
-constexpr size_t kPartRows = static_cast<size_t>(kCtas) * 2 * 2 * kSlotRows;
-constexpr size_t kWorkspace = kCutBytes + kPartRows * (sizeof(float2) + kD * sizeof(float));
-
-// -------------------------------------------------------------- the line --
-
-struct Plan {
-    long long prefix[kMaxRequests + 1];  // where request r's items begin on the line
-    long long warp_sum[kMaxRequests / 64];
-};
-
-// Length of the first `pairs` items of one head: each sees `base` keys (and,
-// causal, its own tokens and the ones before) and costs kOverhead.
-__device__ __forceinline__ long long line_of(const ChunkParams &p, long long base, long long pairs) {
-    const long long own = p.mask == K3DA_MASK_CAUSAL ? p.tpt * pairs * (pairs + 1) : 0;  // 2 tpt (1 + 2 + ... + pairs)
-    return pairs * (base + kOverhead) + own;
-}
-
-// A request's first row, new and cached tokens, clamped to what the call has
-// room for; true when nothing had to be.
-struct Request {
-    int row, n, ctx;
-    __device__ __forceinline__ bool fetch(const ChunkParams &p, int r) {
-        const int a = __ldg(p.cu_seqlens + r), b = __ldg(p.cu_seqlens + r + 1), c = __ldg(p.ctx_lens + r);
-        const int cap = p.page_stride * kP;
-        row = min(max(a, 0), p.T);
-        n = min(max(b, row), p.T) - row;
-        ctx = min(max(c, 0), cap);
-        const bool fits = p.mask == K3DA_MASK_CONTEXT || static_cast<long long>(ctx) + n <= cap;
-        return a == row && b == row + n && (n == 0 || (c == ctx && fits));
-    }
-    __device__ __forceinline__ int pairs(const ChunkParams &p) const { return (n + 2 * p.tpt - 1) / (2 * p.tpt); }
-    // Keys of the line before a causal chunk's own.
-    __device__ __forceinline__ long long base(const ChunkParams &p) const {
-        return static_cast<long long>(ctx) + (p.mask == K3DA_MASK_FULL ? n : 0);
-    }
-};
-
-// All threads; syncs.  The first 512 take two requests each.
-__device__ void build_plan(const ChunkParams &p, Plan *pl, bool report) {
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const bool mine = t < kMaxRequests / 2;
-    long long cost[2] = {0, 0};
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int r = 2 * t + k;
-        if (!mine || r >= p.R) continue;
-        Request q;
-        if (!q.fetch(p, r) && report && p.status) atomicOr(p.status, K3DA_STATUS_BAD_LENGTH);
-        cost[k] = p.Hkv * line_of(p, q.base(p), q.pairs(p));
-    }
-    long long sum = cost[0] + cost[1];
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const long long up = __shfl_up_sync(kFull, sum, off);
-        if (lane >= off) sum += up;
-    }
-    if (mine && lane == 31) pl->warp_sum[warp] = sum;
-    __syncthreads();
-    if (mine) {
-        long long before = 0;
-        for (int w = 0; w < warp; ++w) before += pl->warp_sum[w];
-        const long long begin = before + sum - cost[0] - cost[1];
-        if (2 * t <= p.R) pl->prefix[2 * t] = begin;
-        if (2 * t + 1 <= p.R) pl->prefix[2 * t + 1] = begin + cost[0];
-        if (2 * t + 2 == kMaxRequests && p.R == kMaxRequests) pl->prefix[kMaxRequests] = begin + cost[0] + cost[1];
-    }
-    __syncthreads();
-}
-
-// A piece: the tiles [t0, t1) of one item that fall into this CTA's slice.
-struct Piece {
-    int h;
-    int tok0;    // the item's first token in the chunk
-    int tokens;
-    int ctx, n, r;
-    int row;     // its first row; -1: no more pieces
-    int limit;   // keys its last row sees
-    int keys0;   // ... the last row of slot 0
-    int nt;      // tiles of the item
-    int t0, t1;
-    int alt;     // one slot's worth of rows: the slots take the tiles in turn
-    int seq;     // number of the piece among those with tiles
-    int q;       // where its Q is: slot 0's half of the Q room, and (bits 1, 2) how often the halves were filled before, mod 2
-    int base;    // steps before it
-    // The tiles of slot s: from, from + step, ... below end.
-    __device__ __forceinline__ int from(int s) const { return alt ? t0 + s : t0; }
-    __device__ __forceinline__ int step() const { return alt ? 2 : 1; }
-    __device__ __forceinline__ int end(int s) const {
-        const int keys = alt || s == 1 ? limit : keys0;
-        return keys <= 0 ? 0 : min(t1, (keys - 1) / kTile + 1);
-    }
-    // The step of slot s's tile t: tile by tile, slot 0 first.
-    __device__ __forceinline__ int step_of(int s, int t) const {
-        const int d = t - t0;
-        if (alt) return base + d;
-        return base + d + (s == 0 ? d : min(d + 1, max(end(0) - t0, 0)));
-    }
-    __device__ __forceinline__ int steps() const { return t1 - t0 + (alt ? 0 : max(end(0) - t0, 0)); }
-};
-
-// Keys that the chunk's token i sees.
-__device__ __forceinline__ int keys_seen(const ChunkParams &p, int ctx, int n, int i) {
-    const long long c = p.mask == K3DA_MASK_CAUSAL ? static_cast<long long>(ctx) + i + 1
-                        : p.mask == K3DA_MASK_FULL ? static_cast<long long>(ctx) + n
-                                                   : ctx;
-    const int cap = p.page_stride * kP;
-    return c < cap ? static_cast<int>(c) : cap;
-}
-
-// The CTA's pieces, in order (the scheduler's).
-struct Walk {
-    long long lo, hi;         // the slice
-    long long total, slices;
-    long long at;             // where the next item begins
-    long long start, length;  // the last item
-    int r, h, pair;
-    Request q;  // r's
-
-    // Start of slice c: ceil(c * total / slices), without a wide product.
-    __device__ __forceinline__ long long slice(long long c) const {
-        const long long q = total / slices, rem = total - q * slices;
-        return c * q + (c * rem + slices - 1) / slices;
-    }
-    __device__ void begin(const ChunkParams &p, const Plan *pl, int cta) {
-        total = pl->prefix[p.R];
-        slices = total / kMinSlice;
-        slices = slices < 1 ? 1 : slices > kCtas ? kCtas : slices;
-        lo = hi = at = 0;
-        r = h = pair = 0;
-        if (cta >= slices || total == 0) return;
-        lo = slice(cta);
-        hi = slice(cta + 1);
-        int a = 0, b = p.R;
-        while (b - a > 1) {
-            const int mid = (a + b) >> 1;
-            if (pl->prefix[mid] <= lo) a = mid;
-            else b = mid;
-        }
-        r = a;
-        q.fetch(p, r);
-        const long long keys = q.base(p);
-        const long long head = line_of(p, keys, q.pairs(p));
-        long long rest = lo - pl->prefix[r];
-        h = static_cast<int>(rest / head);
-        rest -= h * head;
-        int x = 0, y = q.pairs(p);
-        while (y - x > 1) {
-            const int mid = (x + y) >> 1;
-            if (line_of(p, keys, mid) <= rest) x = mid;
-            else y = mid;
-        }
-        pair = x;
-        at = pl->prefix[r] + h * head + line_of(p, keys, pair);
-    }
-
-    // First tile of an item's part from `offset` (in the item) on.
-    __device__ __forceinline__ static int tile_at(long long offset, int nt) {
-        const long long t = (offset - kOverhead + kTile - 1) / kTile;
-        return offset <= kOverhead ? 0 : t < nt ? static_cast<int>(t) : nt;
-    }
-
-    __device__ bool next(const ChunkParams &p, Piece &it) {
-        while (at < hi) {
-            it.r = r;
-            it.h = h;
-            it.ctx = q.ctx;
-            it.n = q.n;
-            it.tok0 = pair * 2 * p.tpt;
-            it.tokens = min(2 * p.tpt, it.n - it.tok0);
-            it.row = q.row + it.tok0;
-            it.alt = it.tokens <= p.tpt;
-            it.limit = keys_seen(p, it.ctx, it.n, it.tok0 + it.tokens - 1);
-            it.nt = static_cast<int>((static_cast<long long>(it.limit) + kTile - 1) / kTile);
-            it.keys0 = keys_seen(p, it.ctx, it.n, it.tok0 + min(p.tpt, it.tokens) - 1);
-            start = at;
-            const int count = q.pairs(p);
-            const long long keys = q.base(p);
-            length = line_of(p, keys, pair + 1) - line_of(p, keys, pair);
-            it.t0 = lo <= at ? 0 : tile_at(lo - at, it.nt);
-            it.t1 = hi >= at + length ? it.nt : tile_at(hi - at, it.nt);
-            at += length;
-            if (++pair == count) {
-                pair = 0;
-                if (++h == p.Hkv) {
-                    h = 0;
-                    while (++r < p.R) {
-                        q.fetch(p, r);
-                        if (q.n > 0) break;
-                    }
-                }
-            }
-            if (it.t0 < it.t1 || (it.nt == 0 && start >= lo)) return true;
-        }
-        return false;
-    }
-
-    // The slice that holds this position of the line.
-    __device__ int slice_of(long long pos) const {
-        int a = 0, b = static_cast<int>(slices);
-        while (b - a > 1) {
-            const int mid = (a + b) >> 1;
-            if (slice(mid) <= pos) a = mid;
-            else b = mid;
-        }
-        return a;
-    }
-};
-
 // ----------------------------------------------------------- shared memory --
-
-// What was taken out of a piece's V: for +inf, -inf and NaN and each dim,
-// ~piece (24 bits) over the first key that had one, counted from the keys
-// every row sees (8 bits: an item has at most 256 tokens).  atomicMin then
-// lets a later piece's entries replace an earlier one's: nothing is reset.
-struct Records {
-    uint32_t first[3][kD];
-    int piece;  // the last piece that left something here
-    int pad[3];
-};
 
 template <bool QUANT>
 struct Smem {
@@ -374,11 +119,6 @@ struct Smem {
                       kBars % 8 == 0,
                   "alignment");
 };
-
-// Byte of 16-byte chunk `chunk` of a 128-byte row in a 128B-swizzled tile.
-__device__ __forceinline__ uint32_t swz(int row, int chunk) {
-    return static_cast<uint32_t>(row * 128 + ((chunk ^ (row & 7)) << 4));
-}
 
 // Keeps uses of loaded tensor memory behind the wait for it.
 __device__ __forceinline__ void pin32(uint32_t *r) {
@@ -443,6 +183,11 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
     const uint32_t bar_done = bar_xch + 8;                  // every issuer's products are complete
     const int warp = __shfl_sync(kFull, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
 
+    build_plan<512>(p, pl, blockIdx.x == 0);
+    if (pl->prefix[p.R] == 0) {  // every chunk is small
+        if (threadIdx.x == 0) p.cuts[blockIdx.x] = Cut{};
+        return;
+    }
     if (threadIdx.x == 0) {
         *abort_flag = 0;
         for (int s = 0; s < L::kStages; ++s) {
@@ -484,7 +229,6 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    build_plan(p, pl, blockIdx.x == 0);
     fence_before();
     __syncthreads();
     fence_after();
@@ -1143,7 +887,7 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
 //
 // Folds the partial results of the items that a cut of the line fell into,
 // in the order of their pieces.  CTA (x, y) takes rows [y * rows, (y + 1) *
-// rows) of the x-th such item: 16 threads a row (4 dims each) times `lanes`
+// rows) of the x-th such item of a pass (z): 16 threads a row (4 dims each) times `lanes`
 // piece lanes, lane i folding the pieces i, i + lanes, ...; one lane where
 // there are few pieces (a long chunk: many rows, two or three pieces), eight
 // where one item spreads over many CTAs.  A programmatic dependent of the
@@ -1151,12 +895,13 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
 constexpr int kCombineThreads = 256;
 
 __global__ void __launch_bounds__(kCombineThreads)
-    k3da_chunk_combine_kernel(const __grid_constant__ ChunkParams p, int rows) {
+    k3da_chunk_combine_kernel(const __grid_constant__ ChunkParams first, const __grid_constant__ ChunkParams second, int rows) {
     __shared__ int votes[kCombineThreads / 32];
     __shared__ int owner;
     __shared__ float4 part[8][32];
     __shared__ float2 part_ml[8][2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const ChunkParams &p = blockIdx.z == 0 ? first : second;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // The x-th CTA that left an item unfinished.
     static_assert(kCtas <= kCombineThreads, "one CTA a thread");
@@ -1183,7 +928,7 @@ __global__ void __launch_bounds__(kCombineThreads)
         const int rho = blockIdx.y * rows + base + local;  // the item's row, slot by slot
         const int s = rho / kSlotRows, in_slot = rho % kSlotRows;
         const int token = s * p.tpt + in_slot / p.G;
-        const bool valid = base + local < rows && rho < 2 * kSlotRows && in_slot < slot_rows && token < cut.tokens;
+        const bool valid = base + local < rows && rho < p.part_rows && in_slot < slot_rows && token < cut.tokens;
         float m = -INFINITY, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         if (valid) {
@@ -1197,7 +942,7 @@ __global__ void __launch_bounds__(kCombineThreads)
                     ml[q] = make_float2(-INFINITY, 0.f);
                     v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (i >= pieces || (i > 0 && !p.cuts[a + i].has[0])) continue;
-                    const long long at = (static_cast<long long>(a + i) * 2 + (i == 0 ? 1 : 0)) * 2 * kSlotRows + rho;
+                    const long long at = (static_cast<long long>(a + i) * 2 + (i == 0 ? 1 : 0)) * p.part_rows + rho;
                     ml[q] = p.part_ml[at];
                     v[q] = reinterpret_cast<const float4 *>(p.part_o + at * kD)[dim];
                 }
@@ -1249,29 +994,29 @@ __global__ void __launch_bounds__(kCombineThreads)
 
 // -------------------------------------------------------------------- host --
 
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-    static std::mutex mutex;
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    std::lock_guard<std::mutex> lock(mutex);
-    if (fn == nullptr) {
-        cudaDriverEntryPointQueryResult q;
-        void *f = nullptr;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    }
-    return fn;
-}
-
 template <bool QUANT>
-int launch_chunk(const CUtensorMap &kv_map, const CUtensorMap &q_map, const ChunkParams &prm, cudaStream_t st) {
+int launch_kernel(const CUtensorMap &kv_map, const CUtensorMap &q_map, const ChunkParams &prm, cudaStream_t st) {
     // Set at every call: a context has its own copy of the attribute.
     if (cudaFuncSetAttribute(k3da_chunk_kernel<QUANT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              Smem<QUANT>::kBytes) != cudaSuccess)
         return K3DA_ECUDA;
     k3da_chunk_kernel<QUANT><<<kCtas, threads_of(QUANT), Smem<QUANT>::kBytes, st>>>(kv_map, q_map, prm);
     return cudaGetLastError() == cudaSuccess ? K3DA_OK : K3DA_ECUDA;
+}
+
+int launch_long(const ChunkParams &prm, const void *q, const void *kv_pool, bool quant, cudaStream_t st) {
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    CUtensorMap kv_map, q_map;
+    if (encode == nullptr || !pool_map(encode, &kv_map, kv_pool, prm.num_pages, prm.Hkv, quant)) return K3DA_ECUDA;
+    const cuuint64_t dims[3] = {kD, static_cast<cuuint64_t>(prm.Hq), static_cast<cuuint64_t>(prm.T)};
+    const cuuint64_t strides[2] = {kD * 2, static_cast<cuuint64_t>(prm.q_stride) * 2};
+    const cuuint32_t box[3] = {kD, static_cast<cuuint32_t>(prm.G), static_cast<cuuint32_t>(prm.tpt)};
+    const cuuint32_t estrides[3] = {1, 1, 1};
+    if (encode(&q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box, estrides,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return K3DA_ECUDA;
+    return quant ? launch_kernel<true>(kv_map, q_map, prm, st) : launch_kernel<false>(kv_map, q_map, prm, st);
 }
 
 }  // namespace
@@ -1318,9 +1063,15 @@ extern "C" int k3da_chunk_attn(void *out, float *lse, const void *q, int64_t q_r
     prm.cu_seqlens = cu_seqlens;
     prm.status = status;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    prm.cuts = reinterpret_cast<Cut *>(ws);
-    prm.part_ml = reinterpret_cast<float2 *>(ws + kCutBytes);
-    prm.part_o = reinterpret_cast<float *>(ws + kCutBytes + kPartRows * sizeof(float2));
+    auto parts_at = [](ChunkParams &q, uint8_t *at, int rows) {
+        q.part_rows = rows;
+        q.cuts = reinterpret_cast<Cut *>(at);
+        q.part_ml = reinterpret_cast<float2 *>(at + kCutBytes);
+        q.part_o = reinterpret_cast<float *>(at + kCutBytes + static_cast<size_t>(kCtas) * 2 * rows * sizeof(float2));
+    };
+    parts_at(prm, ws, 2 * kSlotRows);
+    prm.q = static_cast<const __nv_bfloat16 *>(q);
+    prm.q_stride = q_row_stride;
     prm.num_pages = num_pages;
     prm.page_stride = page_stride;
     prm.R = num_requests;
@@ -1332,32 +1083,19 @@ extern "C" int k3da_chunk_attn(void *out, float *lse, const void *q, int64_t q_r
     prm.mask = mask;
     prm.scale_log2 = softmax_scale * 1.4426950408889634f;
 
-    const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
-    if (encode == nullptr) return K3DA_ECUDA;
-    const bool quant = cache_dtype == K3DA_CACHE_E4M3;
-    CUtensorMap kv_map, q_map;
-    {
-        const cuuint64_t dims[2] = {kD, static_cast<cuuint64_t>(num_pages) * 2 * num_kv_heads * kP};
-        const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kD) * (quant ? 1 : 2)};
-        const cuuint32_t box[2] = {kD, kP}, estrides[2] = {1, 1};
-        if (encode(&kv_map, quant ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                   const_cast<void *>(kv_pool), dims, strides, box, estrides, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   quant ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-            return K3DA_ECUDA;
-    }
-    {
-        const cuuint64_t dims[3] = {kD, static_cast<cuuint64_t>(num_q_heads), static_cast<cuuint64_t>(num_tokens)};
-        const cuuint64_t strides[2] = {kD * 2, static_cast<cuuint64_t>(q_row_stride) * 2};
-        const cuuint32_t box[3] = {kD, static_cast<cuuint32_t>(prm.G), static_cast<cuuint32_t>(prm.tpt)};
-        const cuuint32_t estrides[3] = {1, 1, 1};
-        if (encode(&q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box, estrides,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-            return K3DA_ECUDA;
-    }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int launched = quant ? launch_chunk<true>(kv_map, q_map, prm, st) : launch_chunk<false>(kv_map, q_map, prm, st);
+    const bool quant = cache_dtype == K3DA_CACHE_E4M3;
+    // Which requests are small is known to the kernels alone; that none can
+    // be long is known from the number of tokens.
+    const bool any_long = num_tokens > kSmallRows || num_tokens * prm.G > kSmallRows;
+    ChunkParams small = prm;
+    small.pass = 1;
+    parts_at(small, ws + part_bytes(2 * kSlotRows), kSmallRows);
+    if (any_long) {
+        const int launched = launch_long(prm, q, kv_pool, quant, st);
+        if (launched != K3DA_OK) return launched;
+    }
+    const int launched = launch_small(small, kv_pool, quant, any_long, st);
     if (launched != K3DA_OK) return launched;
 
     // Items a cut can fall into, rows one can have: a grid of about 1200
@@ -1365,14 +1103,14 @@ extern "C" int k3da_chunk_attn(void *out, float *lse, const void *q, int64_t q_r
     const long long items =
         ((static_cast<long long>(num_tokens) + 2 * prm.tpt - 1) / (2 * prm.tpt) + num_requests) * num_kv_heads;
     const unsigned gx = static_cast<unsigned>(items < kCtas ? items : kCtas);
-    const long long bound = static_cast<long long>(num_tokens) * prm.G < 2 * kSlotRows
-                                ? (num_tokens <= prm.tpt ? num_tokens * prm.G : 2 * kSlotRows)
-                                : 2 * kSlotRows;
+    const long long bound = !any_long ? num_tokens * prm.G
+                            : num_tokens <= prm.tpt ? num_tokens * prm.G
+                                                    : 2 * kSlotRows;
     int rows = static_cast<int>((bound * gx + 1215) / 1216);
     rows = rows < 2 ? 2 : rows;
     cudaLaunchConfig_t lc;
     std::memset(&lc, 0, sizeof lc);
-    lc.gridDim = dim3(gx, static_cast<unsigned>((bound + rows - 1) / rows));
+    lc.gridDim = dim3(gx, static_cast<unsigned>((bound + rows - 1) / rows), any_long ? 2 : 1);
     lc.blockDim = dim3(kCombineThreads);
     lc.stream = st;
     cudaLaunchAttribute attr[1];
@@ -1380,5 +1118,5 @@ extern "C" int k3da_chunk_attn(void *out, float *lse, const void *q, int64_t q_r
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = attr;
     lc.numAttrs = 1;
-    return cudaLaunchKernelEx(&lc, k3da_chunk_combine_kernel, prm, rows) == cudaSuccess ? K3DA_OK : K3DA_ECUDA;
+    return cudaLaunchKernelEx(&lc, k3da_chunk_combine_kernel, small, prm, rows) == cudaSuccess ? K3DA_OK : K3DA_ECUDA;
 }

@@ -247,6 +247,11 @@ __device__ __forceinline__ unsigned long long add_f32x2(unsigned long long a, un
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
+__device__ __forceinline__ unsigned long long mul_f32x2(unsigned long long a, unsigned long long b) {
+    unsigned long long d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 
 // 2^x of both halves.  Volatile, so that a row of them stays together and
 // their latencies overlap.
