@@ -1007,7 +1007,7 @@ int launch_kernel(const CUtensorMap &kv_map, const CUtensorMap &q_map, const Chu
 int launch_long(const ChunkParams &prm, const void *q, const void *kv_pool, bool quant, cudaStream_t st) {
     const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     CUtensorMap kv_map, q_map;
-    if (encode == nullptr || !pool_map(encode, &kv_map, kv_pool, prm.num_pages, prm.Hkv, quant)) return K3DA_ECUDA;
+    if (encode == nullptr || !pool_map(encode, &kv_map, kv_pool, prm.num_pages, prm.Hkv, quant, !quant)) return K3DA_ECUDA;
     const cuuint64_t dims[3] = {kD, static_cast<cuuint64_t>(prm.Hq), static_cast<cuuint64_t>(prm.T)};
     const cuuint64_t strides[2] = {kD * 2, static_cast<cuuint64_t>(prm.q_stride) * 2};
     const cuuint32_t box[3] = {kD, static_cast<cuuint32_t>(prm.G), static_cast<cuuint32_t>(prm.tpt)};

@@ -4,19 +4,28 @@
 // Same items, line and cuts as the long chunks' kernel (chunk_plan.cuh), but
 // an item is bound by reading its cache, and what 128-row products and the
 // widening of codes to bf16 tiles in shared memory cost would be the bound
-// instead (64 requests of 8000 e4m3 tokens, 24/4 heads: 144 us there).  Here a
-// warp takes a page by itself: 16-row products (mma.sync) with the page's
-// fragments straight from where TMA put them, a running maximum, sum and O of
-// its own in registers, and no barrier but the page's.  Eight such warps share
-// an item's pages; they merge when its piece ends.
+// instead.  Here a warp takes a page by itself: products of 16 keys by 8 rows
+// (mma.sync), the cache's fragments straight from where TMA put them, a
+// running maximum, sum and O of its own in registers, and no barrier but its
+// tiles'.  8 such warps (11 for codes: a page of them is more arithmetic a
+// byte) share an item's pages; another hands out the pieces and folds the
+// warps' results.
 //
-// Quantised pages stay codes in shared memory: a code is a half-precision
-// number as it is (one conversion for two), K's scale multiplies a finished
-// score, and V's goes into the weight: w = 2^(s + e - m'), with a running
-// maximum m' of s + e beside the maximum m of s that the sum keeps.  Both are
-// exponents, so scales of any size meet no range.  q is scaled by a power of
-// two into half precision's range (exact but for dims 2^-39 below the row's
-// largest).
+// Quantised pages stay codes: a code is a half-precision number as it is (one
+// conversion for two), K's scale multiplies a finished score, and V's goes
+// into the weight: w = 2^(s + e - m'), with a reference m' beside the maximum
+// m of s that the sum keeps.  As a rule V's exponents e of a piece lie close
+// together, and m' = m + max e, so that one exp serves sum and weight; else
+// m' is the running maximum of s + e.  Both are exponents, so scales of any
+// size meet no range.  q is scaled by a power of two into half precision's
+// range (exact but for dims 2^-39 below the row's largest).
+//
+// Measured (64 decoded tokens over 8000 each, 24/4 heads): e4m3 61 us, 4.4
+// TB/s of cache, where the long chunks' kernel takes 144; bf16 92 us, 5.7
+// TB/s, against 100.  bf16 is bound by the memory; codes by issue slots (740
+// instructions a page and warp, a third of them conversions and byte
+// permutations) and by instruction fetch.  12 and 15 warps had only 128
+// registers and spilled: 73 and 86 us.
 //
 // Rounding: scores, statistics, O and partial results are fp32; weights are
 // rounded once (bf16, or half precision for codes), the output once.
@@ -38,8 +47,8 @@ namespace {
 
 using namespace sm103;
 
-// Page warps; one more schedules.
-constexpr int page_warps(bool quant) { return quant ? 12 : 8; }
+// Page warps; one more schedules and merges.
+constexpr int page_warps(bool quant) { return quant ? 11 : 8; }
 constexpr int kRing = 4;     // pieces published ahead
 constexpr int kRecords = 8;  // pieces whose non-finite records are alive at once
 // Spread of V's exponents up to which one reference exponent serves a piece's
@@ -50,25 +59,24 @@ constexpr int kORow = kD + 4;  // floats of a row in the merge room (the pad spr
 
 template <bool QUANT>
 struct Smem {
-    // A stage is a page.  A warp loads its
-    // pages itself, into stages of its own: K as soon as the scores of the
-    // page before are done, V after its product.
-    static constexpr int kOwn = 1;  // stages of a warp
     static constexpr int kWarps = page_warps(QUANT);
     static constexpr int kThreads = 32 * (kWarps + 1);
-    static constexpr int kStages = kWarps * kOwn;
-    static constexpr int kTileBytes = kP * kD * (QUANT ? 1 : 2);  // K or V
-    static constexpr int kStageBytes = QUANT ? 2 * kTileBytes + 256 : 2 * kTileBytes;
-    static constexpr int kMerge = kStages * kStageBytes;
+    // A warp loads its own tiles (K, V, K, V, ... of its pages) into its own
+    // places in turn, each as soon as the tile there is done with.
+    static constexpr int kOwn = QUANT ? 3 : 2;
+    static constexpr int kTiles = kWarps * kOwn;
+    static constexpr int kTileBytes = kP * kD * (QUANT ? 1 : 2);
+    static constexpr int kScales = kTiles * kTileBytes;  // [kTiles][64]
+    static constexpr int kMerge = kScales + (QUANT ? kTiles * kP : 0);
     static constexpr int kStats = kMerge + kWarps * kSmallRows * kORow * 4;
     static constexpr int kRec = kStats + kWarps * kSmallRows * 16;
     static constexpr int kPlan = kRec + kRecords * static_cast<int>(sizeof(Records));
     static constexpr int kPieces = kPlan + static_cast<int>(sizeof(Plan));
     static constexpr int kBars = kPieces + kRing * static_cast<int>(sizeof(Piece));
-    static constexpr int kNumBars = 2 * kStages + 2 * kRing + 2;
+    static constexpr int kNumBars = kTiles + kRing + 2;
     static constexpr int kTail = kBars + kNumBars * 8;
     static constexpr int kBytes = kTail + 16 + 1024;
-    static_assert(kBytes <= 227 * 1024 && kStats % 16 == 0 && kRec % 8 == 0 && kPlan % 8 == 0 && kBars % 8 == 0, "layout");
+    static_assert(kBytes <= 227 * 1024 && kMerge % 16 == 0 && kStats % 16 == 0 && kRec % 8 == 0 && kPlan % 8 == 0 && kBars % 8 == 0, "layout");
 };
 
 template <bool HALF>
@@ -113,20 +121,25 @@ __device__ __forceinline__ float exponent_of(uint32_t b) {
 
 // A scale that is not a normal power of two: 2^-127, NaN.
 __device__ __forceinline__ bool odd_scale(uint32_t b) { return b - 1u >= 254u; }
-// The scales of the thread's two keys of a tile, from their two bytes.
 using u64 = unsigned long long;
-__device__ __forceinline__ u64 powers(uint32_t b, int t4) {
-    const uint32_t lo = (b << 23) & 0x7f800000u, hi = (b << 15) & 0x7f800000u;
-    return pack_f32x2(__uint_as_float(t4 & 1 ? hi : lo), __uint_as_float(t4 & 1 ? lo : hi));
+
+// Over the lanes of the same t4: the keys of a product's tile.
+__device__ __forceinline__ float keys_max(float v) {
+    v = fmaxf(v, __shfl_xor_sync(kFull, v, 4));
+    v = fmaxf(v, __shfl_xor_sync(kFull, v, 8));
+    return fmaxf(v, __shfl_xor_sync(kFull, v, 16));
+}
+__device__ __forceinline__ float keys_sum(float v) {
+    v += __shfl_xor_sync(kFull, v, 4);
+    v += __shfl_xor_sync(kFull, v, 8);
+    return v + __shfl_xor_sync(kFull, v, 16);
 }
 
-__device__ __forceinline__ float quad_max(float v) {
-    v = fmaxf(v, __shfl_xor_sync(kFull, v, 1));
-    return fmaxf(v, __shfl_xor_sync(kFull, v, 2));
-}
-__device__ __forceinline__ float quad_sum(float v) {
-    v += __shfl_xor_sync(kFull, v, 1);
-    return v + __shfl_xor_sync(kFull, v, 2);
+// An 8 x 8 tile of 16-bit numbers, transposed across the warp.
+__device__ __forceinline__ uint32_t transposed(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
 }
 
 __device__ __forceinline__ int pages_of(const Piece &it) { return min(2 * it.t1, (it.limit + kP - 1) / kP) - 2 * it.t0; }
@@ -150,24 +163,25 @@ template <bool QUANT>
 struct Loader {
     using L = Smem<QUANT>;
     int warp, lane;
-    uint8_t *stages;
-    uint32_t bar_k, bar_v;
+    uint8_t *tiles, *scales;  // the warp's
+    uint32_t bars;
     uint64_t policy;
     int piece, page, pages, idx;  // the piece it is in, the warp's next page there, how many pages, how many taken
     int r, h, page0;
     int mine;   // row of K of the warp's page idx & ~31 + lane, -1 where the id is no page
-    int yk, yv; // pages of the warp whose K, V are on their way or there
-    int row;    // of page yk - 1
+    int issued;  // tiles on their way or there
+    int place;  // of the next one
+    int row;    // its page's
 
-    __device__ __forceinline__ void begin(int w, int l, uint8_t *smem, uint32_t bk, uint32_t bv) {
+    __device__ __forceinline__ void begin(int w, int l, uint8_t *smem, uint32_t b) {
         warp = w;
         lane = l;
-        stages = smem + w * L::kOwn * L::kStageBytes;
-        bar_k = bk + 8 * w * L::kOwn;
-        bar_v = bv + 8 * w * L::kOwn;
+        tiles = smem + w * L::kOwn * L::kTileBytes;
+        scales = smem + L::kScales + w * L::kOwn * kP;
+        bars = b + 8 * w * L::kOwn;
         asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));  // no page is read twice
         piece = -1;
-        page = pages = idx = yk = yv = 0;
+        page = pages = idx = issued = place = 0;
     }
 
     // Row of the next page's K (-1: no page), or -2 where it is not known
@@ -201,69 +215,424 @@ struct Loader {
         return at;
     }
 
-    // One tile and its scales: dst, their place in the stage.
-    __device__ __forceinline__ void issue(const ChunkParams &p, const CUtensorMap &map, uint32_t bar, uint8_t *stage, int is_v,
-                                          int at) {
-        uint8_t *dst = stage + is_v * L::kTileBytes, *sc = stage + 2 * L::kTileBytes + is_v * kP;
-        if (at < 0) {
-            for (int e = lane; e < L::kTileBytes / 16; e += 32)
-                reinterpret_cast<uint4 *>(dst)[e] = make_uint4(0, 0, 0, 0);
-            if (QUANT && lane < kP / 16) reinterpret_cast<uint4 *>(sc)[lane] = make_uint4(0, 0, 0, 0);
-            fence_proxy_async();  // the stage's next load comes after
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar);
-        } else if (lane == 0) {
-            const int src = at + is_v * p.Hkv * kP;
-            mbar_arrive_expect_tx(bar, L::kTileBytes + (QUANT ? kP : 0));
-            tma_load_2d(smem_u32(dst), &map, 0, src, bar, policy);
-            if (QUANT) bulk_load(smem_u32(sc), p.scales + src, kP, bar);
-        }
-        __syncwarp();
-    }
-    __device__ __forceinline__ bool k(const ChunkParams &p, const CUtensorMap &map, const Piece *pieces, uint32_t bar_piece,
-                                      int n) {
-        const int at = take(p, pieces, bar_piece, n);
-        if (at == -2) return false;
-        if (at < 0 && lane == 0 && p.status) atomicOr(p.status, K3DA_STATUS_BAD_PAGE);
-        row = at;
-        issue(p, map, bar_k + 8 * (yk % L::kOwn), stages + yk % L::kOwn * L::kStageBytes, 0, at);
-        ++yk;
-        return true;
-    }
-    __device__ __forceinline__ void v(const ChunkParams &p, const CUtensorMap &map) {
-        issue(p, map, bar_v + 8 * (yv % L::kOwn), stages + yv % L::kOwn * L::kStageBytes, 1, row);
-        ++yv;
-    }
-
-    // Pages up to y + kOwn: all of the stages but page y's are free.
+    // The tiles that find a place when `done` were done with.
     __device__ __forceinline__ void fill(const ChunkParams &p, const CUtensorMap &map, const Piece *pieces,
-                                         uint32_t bar_piece, int n, int y) {
-        while (yk < y + L::kOwn && k(p, map, pieces, bar_piece, n)) v(p, map);
+                                         uint32_t bar_piece, int n, int done) {
+        while (issued < done + L::kOwn) {
+            const int is_v = issued & 1;
+            if (!is_v) {
+                const int at = take(p, pieces, bar_piece, n);
+                if (at == -2) return;
+                if (at < 0 && lane == 0 && p.status) atomicOr(p.status, K3DA_STATUS_BAD_PAGE);
+                row = at;
+            }
+            uint8_t *dst = tiles + place * L::kTileBytes, *sc = scales + place * kP;
+            const uint32_t bar = bars + 8 * place;
+            if (__builtin_expect(row < 0, 0)) {
+                for (int e = lane; e < L::kTileBytes / 16; e += 32)
+                    reinterpret_cast<uint4 *>(dst)[e] = make_uint4(0, 0, 0, 0);
+                if (QUANT && lane < kP / 16) reinterpret_cast<uint4 *>(sc)[lane] = make_uint4(0, 0, 0, 0);
+                fence_proxy_async();  // the place's next load comes after
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar);
+            } else if (lane == 0) {
+                const int src = row + is_v * p.Hkv * kP;
+                mbar_arrive_expect_tx(bar, L::kTileBytes + (QUANT ? kP : 0));
+                tma_load_2d(smem_u32(dst), &map, 0, src, bar, policy);
+                if (QUANT) bulk_load(smem_u32(sc), p.scales + src, kP, bar);
+            }
+            __syncwarp();
+            ++issued;
+            place = place + 1 == L::kOwn ? 0 : place + 1;
+        }
     }
-    // After page y's scores.
-    __device__ __forceinline__ void next_k(const ChunkParams &p, const CUtensorMap &map, const Piece *pieces,
-                                           uint32_t bar_piece, int n, int y) {
-        if (yk == y + L::kOwn) k(p, map, pieces, bar_piece, n);
-    }
-    // After its product.
-    __device__ __forceinline__ void next_v(const ChunkParams &p, const CUtensorMap &map, const Piece *pieces,
-                                           uint32_t bar_piece, int n, int y) {
-        if (yv < yk) v(p, map);
-        fill(p, map, pieces, bar_piece, n, y + 1);
-    }
-    // Waits (with a limit) for loads that no page was read from: a wait gave
-    // up before.
+    // Waits (with a limit) for loads that no product read: a wait gave up
+    // before.
     __device__ __forceinline__ void drain() {
-        for (int s = 0; s < 2 * L::kOwn; ++s) {
-            const int last = s < L::kOwn ? yk - 1 - s : yv - 1 - (s - L::kOwn);
-            if (last < 0) continue;
-            const uint32_t bar = (s < L::kOwn ? bar_k : bar_v) + 8 * (last % L::kOwn);
+        for (int j = max(issued - L::kOwn, 0); j < issued; ++j) {
             const unsigned long long t0 = global_ns();
-            while (!mbar_try_wait(bar, (last / L::kOwn) & 1) && global_ns() - t0 < kWaitLimitNs) {
+            while (!mbar_try_wait(bars + 8 * (j % L::kOwn), (j / L::kOwn) & 1) && global_ns() - t0 < kWaitLimitNs) {
             }
         }
     }
 };
+
+// The page warps' results of a piece, folded, and out: a row's four dims a
+// lane at a time.
+template <bool QUANT>
+__device__ __forceinline__ void merge_piece(const ChunkParams &p, const Piece &it, const float *merge_o,
+                                            const float4 *merge_s, const Records *recs, int lane) {
+    constexpr int kWarps = Smem<QUANT>::kWarps;
+    const bool whole = it.t0 == 0 && it.t1 == it.nt;
+    const Records &rec = recs[it.seq % kRecords];
+    const bool hidden = !QUANT && it.t0 < it.t1 && rec.piece == it.seq;
+    const int dim = 4 * (lane & 15);
+#pragma unroll 1
+    for (int rho = lane >> 4; rho < it.tokens * p.G; rho += 2) {
+        float mt = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, merge_s[w * kSmallRows + rho].x);
+        const float me = mt == -INFINITY ? 0.f : mt;
+        float lt = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float4 st = merge_s[w * kSmallRows + rho];
+            const float4 part = *reinterpret_cast<const float4 *>(merge_o + (w * kSmallRows + rho) * kORow + dim);
+            const float f = exp2_approx(st.z - me);
+            lt += st.y * exp2_approx(st.x - me);
+            v[0] += part.x * f;
+            v[1] += part.y * f;
+            v[2] += part.z * f;
+            v[3] += part.w * f;
+        }
+        const float norm = whole ? 1.f / lt : 1.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = lt == 0.f ? 0.f : v[q] * norm;
+        const int token = rho / p.G;
+        if (hidden) {
+            const int least = keys_seen(p, it.ctx, it.n, 0), sees = keys_seen(p, it.ctx, it.n, token);
+            const uint32_t tag = ~static_cast<uint32_t>(it.seq) << 8;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                for (int kind = 0; kind < 3; ++kind) {
+                    const uint32_t e = rec.first[kind][dim + q];
+                    if ((e & 0xffffff00u) != tag || least + static_cast<int>(e & 0xffu) >= sees) continue;
+                    v[q] = kind == 2 ? __uint_as_float(0x7fffffffu) : v[q] + (kind == 0 ? INFINITY : -INFINITY);
+                }
+        }
+        if (whole) {
+            const long long at = static_cast<long long>(it.row + token) * p.Hq + it.h * p.G + rho - token * p.G;
+            *reinterpret_cast<uint2 *>(p.out + at * kD + dim) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+            if (dim == 0 && p.lse) p.lse[at] = lt == 0.f ? -INFINITY : (mt + log2f(lt)) * 0.6931471805599453f;
+        } else {
+            const int part = (blockIdx.x * 2 + (it.t0 > 0 ? 0 : 1)) * kSmallRows + rho;
+            *reinterpret_cast<float4 *>(p.part_o + static_cast<long long>(part) * kD + dim) =
+                make_float4(v[0], v[1], v[2], v[3]);
+            if (dim == 0) p.part_ml[part] = make_float2(mt, lt);
+        }
+    }
+}
+
+// The tile a page warp is at.
+template <bool QUANT>
+struct Turn {
+    int done = 0, place = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        ++done;
+        if (++place == Smem<QUANT>::kOwn) {
+            place = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+// What a page warp keeps of a piece.  Products are of 16 keys (or dims) by 8
+// rows, so that the 4 to 8 rows of most items fill them: S^T = K q^T and
+// O^T += V^T w^T.  The thread has rows 8 n + 2 t4 and one more of each row
+// tile n, and of a 16-key tile i the keys 16 i + kg and + 8.
+struct Rows {
+    uint32_t q[2][8];  // of row 8 n + g: dims 16 t4 .. 16 t4 + 15 (and so of every key: a product's order of dims is free)
+    float scale[2][2];
+    int sees[2][2];
+    float m[2][2], l[2][2];
+    float mo[2][2];   // reference of O: m, or with codes the maximum of s + e
+    float o[2][4][4];
+    // Codes: while V's exponents in the piece are within kNear of one another.
+    bool near;
+    int e_hi, e_lo;
+};
+
+// One page, over NT tiles of 8 rows.
+template <bool QUANT, int NT>
+__device__ __forceinline__ bool take_page(Rows &R, Loader<QUANT> &load, const ChunkParams &p, const CUtensorMap &kv_map,
+                                          const Piece *pieces, uint32_t bar_piece, int n, Turn<QUANT> &turn, int key0,
+                                          int least, int limit, Records *rec, int piece, int lane,
+                                          volatile int *abort_flag) {
+    using L = Smem<QUANT>;
+    const int g = lane >> 2, t4 = lane & 3;
+    if (!warp_wait(load.bars + 8 * turn.place, turn.phase, abort_flag, p.status)) return false;
+    const uint8_t *kt = load.tiles + turn.place * L::kTileBytes, *ks = load.scales + turn.place * kP;
+    const bool masked = key0 + kP > least;
+    // Code tiles have rows of 64 bytes, 16-byte chunks swizzled by bits 1 and
+    // 2 of the row.  With keys 2 and 3 of every four exchanged, a thread's
+    // loads of V (below) meet no bank twice.
+    const int kg = QUANT ? g ^ (g >> 1 & 1) : g;
+    float s[NT][4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = 16 * i + kg;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[nt][i][e] = 0.f;
+        if (QUANT) {
+            const uint32_t at = row * kD + 16 * (t4 ^ (g >> 1 & 3));
+            const uint4 u = *reinterpret_cast<const uint4 *>(kt + at), v = *reinterpret_cast<const uint4 *>(kt + at + 8 * kD);
+            const uint32_t a[4] = {u.x, u.y, u.z, u.w}, b[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t a0 = halves_lo(a[e]), a1 = halves_lo(b[e]), a2 = halves_hi(a[e]), a3 = halves_hi(b[e]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma16816<true>(s[nt][i], a0, a1, a2, a3, R.q[nt][2 * e], R.q[nt][2 * e + 1]);
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const uint4 a = *reinterpret_cast<const uint4 *>(kt + swz(row, 2 * t4 + c));
+                const uint4 b = *reinterpret_cast<const uint4 *>(kt + swz(row + 8, 2 * t4 + c));
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma16816<false>(s[nt][i], a.x, b.x, a.y, b.y, R.q[nt][4 * c], R.q[nt][4 * c + 1]);
+                    mma16816<false>(s[nt][i], a.z, b.z, a.w, b.w, R.q[nt][4 * c + 2], R.q[nt][4 * c + 3]);
+                }
+            }
+        }
+    }
+    // Scores in log2 units, masked.
+    float top[NT][2];
+    const uint32_t kb = QUANT ? *reinterpret_cast<const uint16_t *>(ks + 2 * lane) : 0u;
+    const bool plain = !masked && (!QUANT || !__any_sync(kFull, odd_scale(kb & 255u) || odd_scale(kb >> 8)));
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = -INFINITY;
+    if (__builtin_expect(plain, 1)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float f = QUANT ? __uint_as_float(static_cast<uint32_t>(ks[16 * i + 8 * h + kg]) << 23) : 1.f;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    u64 v = mul_f32x2(pack_f32x2(s[nt][i][2 * h], s[nt][i][2 * h + 1]), pack_f32x2(R.scale[nt][0], R.scale[nt][1]));
+                    if (QUANT) v = mul_f32x2(v, pack_f32x2(f, f));
+                    const float2 w = unpack_f32x2(v);
+                    s[nt][i][2 * h] = w.x;
+                    s[nt][i][2 * h + 1] = w.y;
+                    top[nt][0] = fmaxf(top[nt][0], w.x);
+                    top[nt][1] = fmaxf(top[nt][1], w.y);
+                }
+            }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int key = 16 * i + 8 * h + kg;
+                const float f = QUANT ? scale_of(ks[key]) : 1.f;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float &v = s[nt][i][2 * h + c];
+                        v *= R.scale[nt][c];
+                        if (QUANT) v *= f;
+                        if (key0 + key >= R.sees[nt][c] && masked) v = -INFINITY;
+                        top[nt][c] = fmaxf(top[nt][c], v);
+                    }
+            }
+    }
+    __syncwarp();
+    turn.next();
+    load.fill(p, kv_map, pieces, bar_piece, n, turn.done);
+    if (!warp_wait(load.bars + 8 * turn.place, turn.phase, abort_flag, p.status)) return false;
+    uint8_t *vt = load.tiles + turn.place * L::kTileBytes;
+    const uint8_t *vs = load.scales + turn.place * kP;
+    if (QUANT && __builtin_expect(masked, 0)) {
+        // Weights of zero must meet no NaN: none past the last key, nor in a
+        // key that not every row sees (where the largest code stands for it).
+#pragma unroll 1
+        for (int e = lane; e < kP * 4; e += 32) {
+            const int key = key0 + (e >> 2);
+            if (key < least) continue;
+            uint4 *at = reinterpret_cast<uint4 *>(vt + 16 * e);
+            const uint4 w = *at;
+            uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t nan = ((v[q] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                v[q] = key >= limit ? 0u : v[q] - (nan >> 7);
+            }
+            *at = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+        fence_proxy_async();  // the stage's next load comes after
+        __syncwarp();
+    }
+    if (!QUANT && __builtin_expect(masked, 0)) {
+        // As in the long chunks' kernel: V rows past the last key
+        // to zero, infinities and NaN of a key that not every row
+        // sees out of V and into the records.
+        const uint32_t tag = ~static_cast<uint32_t>(piece) << 8;
+#pragma unroll 1
+        for (int e = lane; e < kP * 8; e += 32) {
+            const int key = key0 + (e >> 3), c = e & 7;
+            if (key < least) continue;
+            uint4 *at = reinterpret_cast<uint4 *>(vt + swz(e >> 3, c));
+            if (key >= limit) {
+                *at = make_uint4(0, 0, 0, 0);
+                continue;
+            }
+            const uint4 w = *at;
+            uint32_t v[4] = {w.x, w.y, w.z, w.w};
+            bool bad = false;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) bad |= (v[q] & 0x7f80u) == 0x7f80u || (v[q] & 0x7f800000u) == 0x7f800000u;
+            if (!bad) continue;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const uint32_t b = v[q >> 1] >> (16 * (q & 1)) & 0xffffu;
+                if ((b & 0x7f80u) != 0x7f80u) continue;
+                atomicMin(&rec->first[b & 0x7fu ? 2 : b >> 15][8 * c + q], tag | (key - least));
+                v[q >> 1] &= q & 1 ? 0x0000ffffu : 0xffff0000u;
+            }
+            *at = make_uint4(v[0], v[1], v[2], v[3]);
+            rec->piece = piece;
+        }
+        fence_proxy_async();  // the stage's next load comes after
+        __syncwarp();
+    }
+    // Weights, in place of the scores.
+    float base[NT][2], fo[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const float mn = fmaxf(R.m[nt][c], keys_max(top[nt][c]));
+            base[nt][c] = mn == -INFINITY ? 0.f : mn;
+            fo[nt][c] = exp2_approx(R.m[nt][c] - base[nt][c]);
+            R.l[nt][c] *= fo[nt][c];
+            R.m[nt][c] = mn;
+        }
+    if (QUANT) {
+        const uint32_t vb = *reinterpret_cast<const uint16_t *>(vs + 2 * lane);
+        const int hi = max(R.e_hi, static_cast<int>(__reduce_max_sync(kFull, max(vb & 255u, vb >> 8))));
+        const int lo = min(R.e_lo, static_cast<int>(__reduce_min_sync(kFull, min(vb & 255u, vb >> 8))));
+        R.near = R.near && plain && hi < 255 && hi - lo <= kNear;
+        if (R.near) {
+            R.e_hi = hi;
+            R.e_lo = lo;
+        }
+    }
+    if (__builtin_expect(QUANT ? R.near : plain, 1)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const u64 nb = pack_f32x2(-base[nt][0], -base[nt][1]);
+            u64 sum = 0ull;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    u64 w = exp2_f32x2(add_f32x2(pack_f32x2(s[nt][i][2 * h], s[nt][i][2 * h + 1]), nb));
+                    sum = add_f32x2(sum, w);
+                    if (QUANT) {  // 2^(e - e_hi)
+                        const float f = __uint_as_float((vs[16 * i + 8 * h + kg] + 127u - R.e_hi) << 23);
+                        w = mul_f32x2(w, pack_f32x2(f, f));
+                    }
+                    const float2 v = unpack_f32x2(w);
+                    s[nt][i][2 * h] = v.x;
+                    s[nt][i][2 * h + 1] = v.y;
+                }
+            const float2 v = unpack_f32x2(sum);
+            R.l[nt][0] += v.x;
+            R.l[nt][1] += v.y;
+            if (QUANT) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float mn = R.m[nt][c] + static_cast<float>(R.e_hi - 127);
+                    fo[nt][c] = exp2_approx(R.mo[nt][c] - (mn == -INFINITY ? 0.f : mn));
+                    R.mo[nt][c] = mn;
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float base_o = base[nt][c];
+                if (QUANT) {
+                    // V's exponents join the scores for the weights.
+                    float top_o = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float &v = s[nt][i][2 * h + c];
+                            R.l[nt][c] += exp2_approx(v - base[nt][c]);
+                            if (v != -INFINITY) v += exponent_of(vs[16 * i + 8 * h + kg]);
+                            top_o = fmaxf(top_o, v);
+                        }
+                    const float mn = fmaxf(R.mo[nt][c], keys_max(top_o));
+                    base_o = mn == -INFINITY ? 0.f : mn;
+                    fo[nt][c] = exp2_approx(R.mo[nt][c] - base_o);
+                    R.mo[nt][c] = mn;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float &v = s[nt][i][2 * h + c];
+                        v = exp2_approx(v - base_o);
+                        if (!QUANT) R.l[nt][c] += v;
+                    }
+            }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        if (!__any_sync(kFull, fo[nt][0] != 1.f || fo[nt][1] != 1.f)) continue;
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) R.o[nt][d][e] *= fo[nt][e & 1];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // 16 keys a product
+        uint32_t b[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                b[nt][h] = transposed(QUANT ? pack_half2(s[nt][i][2 * h], s[nt][i][2 * h + 1])
+                                            : pack2(s[nt][i][2 * h], s[nt][i][2 * h + 1]));
+        if (QUANT) {
+            // Four dims of four keys a thread: bytes to pairs of keys, pairs
+            // to halves.  Row g of dim tile 2 hf + u is dim 32 hf + 4 g + 2 u,
+            // row g + 8 the one after.
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int key = 16 * i + 8 * (e >> 1) + 2 * t4 + ((e ^ t4) & 1);
+                    w[e] = *reinterpret_cast<const uint32_t *>(vt + key * kD + 16 * ((2 * hf + (g >> 2)) ^ t4) + 4 * (g & 3));
+                }
+                const uint32_t lo0 = __byte_perm(w[0], w[1], 0x5140), lo1 = __byte_perm(w[0], w[1], 0x7362);
+                const uint32_t hi0 = __byte_perm(w[2], w[3], 0x5140), hi1 = __byte_perm(w[2], w[3], 0x7362);
+                const uint32_t a[8] = {halves_lo(lo0), halves_hi(lo0), halves_lo(hi0), halves_hi(hi0),
+                                       halves_lo(lo1), halves_hi(lo1), halves_lo(hi1), halves_hi(hi1)};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma16816<true>(R.o[nt][2 * hf], a[0], a[1], a[2], a[3], b[nt][0], b[nt][1]);
+                    mma16816<true>(R.o[nt][2 * hf + 1], a[4], a[5], a[6], a[7], b[nt][0], b[nt][1]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                uint32_t a[4];
+                asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(a[0]), "=r"(a[2]), "=r"(a[1]), "=r"(a[3])
+                             : "r"(smem_u32(vt) + swz(16 * i + (lane & 15), 2 * d + (lane >> 4)))
+                             : "memory");
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma16816<false>(R.o[nt][d], a[0], a[1], a[2], a[3], b[nt][0], b[nt][1]);
+            }
+        }
+    }
+    __syncwarp();
+    turn.next();
+    load.fill(p, kv_map, pieces, bar_piece, n, turn.done);
+    return true;
+}
 
 template <bool QUANT>
 __global__ void __launch_bounds__(Smem<QUANT>::kThreads, 1)
@@ -279,12 +648,9 @@ __global__ void __launch_bounds__(Smem<QUANT>::kThreads, 1)
     float4 *merge_s = reinterpret_cast<float4 *>(smem + L::kStats);    // [kWarps][16] (m, l, m' of O)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kTail);
     const uint32_t bars = smem_u32(smem + L::kBars);
-    const uint32_t bar_k = bars;                       // [kStages] K loaded
-    const uint32_t bar_v = bar_k + 8 * L::kStages;     // [kStages] V loaded
-    const uint32_t bar_piece = bar_v + 8 * L::kStages; // [kRing] piece published
-    const uint32_t bar_pdone = bar_piece + 8 * kRing;      // [kRing] ... and read by every page warp
-    const uint32_t bar_left = bar_pdone + 8 * kRing;       // the page warps' results are in the merge room
-    const uint32_t bar_merged = bar_left + 8;              // ... and read
+    const uint32_t bar_piece = bars + 8 * L::kTiles;   // [kRing] piece published; before them, the tiles' own
+    const uint32_t bar_left = bar_piece + 8 * kRing;   // the page warps' results are in the merge room
+    const uint32_t bar_merged = bar_left + 8;          // ... and read, and the piece's place is free
     const int warp = __shfl_sync(kFull, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -296,16 +662,10 @@ __global__ void __launch_bounds__(Smem<QUANT>::kThreads, 1)
     }
     if (threadIdx.x == 0) {
         *abort_flag = 0;
-        for (int s = 0; s < L::kStages; ++s) {
-            mbar_init(bar_k + 8 * s, 1);
-            mbar_init(bar_v + 8 * s, 1);
-        }
-        for (int s = 0; s < kRing; ++s) {
-            mbar_init(bar_piece + 8 * s, 1);
-            mbar_init(bar_pdone + 8 * s, kWarps);
-        }
+        for (int s = 0; s < L::kTiles; ++s) mbar_init(bars + 8 * s, 1);
+        for (int s = 0; s < kRing; ++s) mbar_init(bar_piece + 8 * s, 1);
         mbar_init(bar_left, kWarps);
-        mbar_init(bar_merged, kWarps);
+        mbar_init(bar_merged, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (!QUANT) {
@@ -316,70 +676,73 @@ __global__ void __launch_bounds__(Smem<QUANT>::kThreads, 1)
     __syncthreads();
 
     if (warp == kWarps) {
-        // --------------------------------------------------------- pieces --
-        if (lane == 0) {
-            Walk walk;
-            walk.begin(p, pl, blockIdx.x);
-            Cut cut = {};
-            int x = 0, seq = 0;
-            for (int n = 0;; ++n) {
-                Piece &it = pieces[n % kRing];
-                if (!mbar_wait(bar_pdone + 8 * (n % kRing), ((n / kRing) & 1) ^ 1, abort_flag, p.status)) break;
-                const bool more = walk.next(p, it);
-                if (!more) it.row = -1;
-                it.base = x;
-                it.seq = seq;
-                if (more && it.t0 < it.t1) {
-                    ++seq;
-                    x += pages_of(it);
+        // ------------------------------------ pieces, and what becomes of them --
+        Walk walk;
+        Cut cut = {};
+        int x = 0, seq = 0, published = 0;
+        bool more = true;
+        if (lane == 0) walk.begin(p, pl, blockIdx.x);
+        for (int n = 0;; ++n) {
+            while (more && published < n + kRing) {
+                if (lane == 0) {
+                    Piece &it = pieces[published % kRing];
+                    more = walk.next(p, it);
+                    if (!more) it.row = -1;
+                    it.base = x;
+                    it.seq = seq;
+                    if (more && it.t0 < it.t1) {
+                        ++seq;
+                        x += pages_of(it);
+                    }
+                    if (more && it.t0 > 0) cut.has[0] = 1;
+                    if (more && it.t0 == 0 && it.t0 < it.t1 && it.t1 < it.nt) {
+                        cut.has[1] = 1;
+                        cut.row = it.row;
+                        cut.tokens = it.tokens;
+                        cut.head = it.h;
+                        cut.last = walk.slice_of(walk.start + walk.length - 1);
+                    }
+                    mbar_arrive(bar_piece + 8 * (published % kRing));
+                    if (!more) p.cuts[blockIdx.x] = cut;
                 }
-                if (more && it.t0 > 0) cut.has[0] = 1;
-                if (more && it.t0 == 0 && it.t0 < it.t1 && it.t1 < it.nt) {
-                    cut.has[1] = 1;
-                    cut.row = it.row;
-                    cut.tokens = it.tokens;
-                    cut.head = it.h;
-                    cut.last = walk.slice_of(walk.start + walk.length - 1);
-                }
-                mbar_arrive(bar_piece + 8 * (n % kRing));
-                if (!more) break;
+                more = __shfl_sync(kFull, more, 0);
+                ++published;
             }
-            p.cuts[blockIdx.x] = cut;
+            if (n == published - 1) break;  // the end's mark
+            if (!warp_wait(bar_left, n & 1, abort_flag, p.status)) break;
+            merge_piece<QUANT>(p, pieces[n % kRing], merge_o, merge_s, recs, lane);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_merged);
         }
     } else {
         // ----------------------------------------------------- page warps --
         const int g = lane >> 2, t4 = lane & 3;  // a fragment's row or column group, and the thread in it
         Loader<QUANT> load;
-        load.begin(warp, lane, smem, bar_k, bar_v);
-        int y = 0;  // pages this warp is done with
+        load.begin(warp, lane, smem, bars);
+        Turn<QUANT> turn;
         for (int n = 0;; ++n) {
             const Piece &it = pieces[n % kRing];
             if (!warp_wait(bar_piece + 8 * (n % kRing), (n / kRing) & 1, abort_flag, p.status)) break;
             if (it.row < 0) break;
             const int limit = it.limit, piece = it.seq;
             const int page0 = 2 * it.t0, pages = pages_of(it);
-            load.fill(p, kv_map, pieces, bar_piece, n, y);
+            load.fill(p, kv_map, pieces, bar_piece, n, turn.done);
             const int least = keys_seen(p, it.ctx, it.n, 0);  // keys that every row sees
-            // Rows g and g + 8 of the item (token major, the heads of a token
-            // together); the thread has dims 16 t4 .. 16 t4 + 15 of each, and
-            // so of every key: the order of dims in a product is free.
-            uint32_t qf[2][8];
-            int sees[2];
-            float row_scale[2];
+            // The item's rows: token major, the heads of a token together.
+            const bool wide = it.tokens * p.G > 8;
+            Rows R;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int rho = g + 8 * i, token = rho / p.G;
-                const bool valid = token < it.tokens;
-                sees[i] = valid ? keys_seen(p, it.ctx, it.n, token) : 0;
+            for (int nt = 0; nt < 2; ++nt) {
+                const int rho = g + 8 * nt, token = rho / p.G;
                 uint4 a = make_uint4(0, 0, 0, 0), b = a;
-                if (valid) {
+                if (token < it.tokens) {
                     const uint4 *src = reinterpret_cast<const uint4 *>(
                         p.q + static_cast<long long>(it.row + token) * p.q_stride + (it.h * p.G + rho - token * p.G) * kD + 16 * t4);
                     a = __ldg(src);
                     b = __ldg(src + 1);
                 }
                 const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-                row_scale[i] = p.scale_log2;
+                float scale = p.scale_log2;
                 if (QUANT) {
                     uint32_t top = 0;
 #pragma unroll
@@ -391,338 +754,64 @@ __global__ void __launch_bounds__(Smem<QUANT>::kThreads, 1)
                     const uint32_t ex = top >> 23;
                     const uint32_t f = ex == 0 || ex == 255 ? 127u : min(268u - ex, 253u);
                     const float up = __uint_as_float(f << 23);
-                    row_scale[i] *= __uint_as_float((254u - f) << 23);
+                    scale *= __uint_as_float((254u - f) << 23);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) qf[i][e] = pack_half2(bf16_lo(w[e]) * up, bf16_hi(w[e]) * up);
+                    for (int e = 0; e < 8; ++e) R.q[nt][e] = pack_half2(bf16_lo(w[e]) * up, bf16_hi(w[e]) * up);
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) qf[i][e] = w[e];
+                    for (int e = 0; e < 8; ++e) R.q[nt][e] = w[e];
                 }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int mine = (8 * nt + 2 * t4 + c) / p.G;
+                    R.scale[nt][c] = __shfl_sync(kFull, scale, 4 * (2 * t4 + c));
+                    R.sees[nt][c] = mine < it.tokens ? keys_seen(p, it.ctx, it.n, mine) : 0;
+                    R.m[nt][c] = R.mo[nt][c] = -INFINITY;
+                    R.l[nt][c] = 0.f;
+                }
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) R.o[nt][d][e] = 0.f;
             }
-            float o[8][4];
-#pragma unroll
-            for (int d = 0; d < 8; ++d)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) o[d][q] = 0.f;
-            float m[2] = {-INFINITY, -INFINITY}, mo[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-            // While V's exponents in the piece are within kNear of one another.
-            bool near = QUANT, alive = true;
-            int e_hi = -1, e_lo = 256;
-            for (int j = first_page<QUANT>(warp, it.base); j < pages; j += kWarps, ++y) {
-                const int st = warp * L::kOwn + y % L::kOwn;
-                if (!warp_wait(bar_k + 8 * st, (y / L::kOwn) & 1, abort_flag, p.status)) {
-                    alive = false;
-                    break;
-                }
-                uint8_t *kt = smem + st * L::kStageBytes, *vt = kt + L::kTileBytes;
-                const uint8_t *ks = kt + 2 * L::kTileBytes, *vs = ks + kP;
+            R.near = QUANT;
+            R.e_hi = -1;
+            R.e_lo = 256;
+            bool alive = true;
+            for (int j = first_page<QUANT>(warp, it.base); j < pages; j += kWarps) {
+                Records *rec = recs + piece % kRecords;
                 const int key0 = (page0 + j) * kP;
-                const bool masked = key0 + kP > least;
-                // The thread's scores of tile i are of the keys 8 i + k0 and
-                // 8 i + k1.  Codes lie 64 bytes a row, so keys 2 and 3 of
-                // every four change places, which spreads a product's V rows
-                // over the banks.
-                const int k0 = QUANT ? 2 * t4 + (t4 & 1) : 2 * t4, k1 = QUANT ? 2 * t4 + 1 - (t4 & 1) : 2 * t4 + 1;
-                float s[8][4];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) s[i][q] = 0.f;
-                    if (QUANT) {
-                        const int row = 8 * i + (g ^ (g >> 1 & 1));
-                        const uint4 w = *reinterpret_cast<const uint4 *>(kt + row * kD + 16 * t4);
-                        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            mma16816<true>(s[i], qf[0][2 * q], qf[1][2 * q], qf[0][2 * q + 1], qf[1][2 * q + 1],
-                                           halves_lo(in[q]), halves_hi(in[q]));
-                    } else {
-                        const int row = 8 * i + g;
-                        const uint4 w = *reinterpret_cast<const uint4 *>(kt + swz(row, 2 * t4));
-                        const uint4 y = *reinterpret_cast<const uint4 *>(kt + swz(row, 2 * t4 + 1));
-                        mma16816<false>(s[i], qf[0][0], qf[1][0], qf[0][1], qf[1][1], w.x, w.y);
-                        mma16816<false>(s[i], qf[0][2], qf[1][2], qf[0][3], qf[1][3], w.z, w.w);
-                        mma16816<false>(s[i], qf[0][4], qf[1][4], qf[0][5], qf[1][5], y.x, y.y);
-                        mma16816<false>(s[i], qf[0][6], qf[1][6], qf[0][7], qf[1][7], y.z, y.w);
-                    }
-                }
-                // Scores in log2 units, masked.
-                float top[2] = {-INFINITY, -INFINITY};
-                const uint32_t kb = QUANT ? *reinterpret_cast<const uint16_t *>(ks + 2 * lane) : 0u;
-                const bool plain = QUANT && !masked && !__any_sync(kFull, odd_scale(kb & 255u) || odd_scale(kb >> 8));
-                if (plain) {
-                    const u64 rs[2] = {pack_f32x2(row_scale[0], row_scale[0]), pack_f32x2(row_scale[1], row_scale[1])};
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const u64 f = powers(*reinterpret_cast<const uint16_t *>(ks + 8 * i + 2 * t4), t4);
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            const float2 v = unpack_f32x2(mul_f32x2(mul_f32x2(pack_f32x2(s[i][2 * q], s[i][2 * q + 1]), rs[q]), f));
-                            s[i][2 * q] = v.x;
-                            s[i][2 * q + 1] = v.y;
-                            top[q] = fmax3(top[q], v.x, v.y);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float f0 = 1.f, f1 = 1.f;
-                        if (QUANT) {
-                            const uint32_t b = *reinterpret_cast<const uint16_t *>(ks + 8 * i + 2 * t4);
-                            f0 = scale_of(t4 & 1 ? b >> 8 : b & 255u);
-                            f1 = scale_of(t4 & 1 ? b & 255u : b >> 8);
-                        }
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            s[i][q] *= row_scale[q >> 1];
-                            if (QUANT) s[i][q] *= q & 1 ? f1 : f0;
-                            if (masked && key0 + 8 * i + (q & 1 ? k1 : k0) >= sees[q >> 1]) s[i][q] = -INFINITY;
-                            top[q >> 1] = fmaxf(top[q >> 1], s[i][q]);
-                        }
-                    }
-                }
-                __syncwarp();
-                load.next_k(p, kv_map, pieces, bar_piece, n, y);
-                if (!warp_wait(bar_v + 8 * st, (y / L::kOwn) & 1, abort_flag, p.status)) {
-                    alive = false;
-                    break;
-                }
-                if (!QUANT && masked) {
-                    // As in the long chunks' kernel: V rows past the last key
-                    // to zero, infinities and NaN of a key that not every row
-                    // sees out of V and into the records.
-                    Records *rec = recs + piece % kRecords;
-                    const uint32_t tag = ~static_cast<uint32_t>(piece) << 8;
-#pragma unroll 1
-                    for (int e = lane; e < kP * 8; e += 32) {
-                        const int key = key0 + (e >> 3), c = e & 7;
-                        if (key < least) continue;
-                        uint4 *at = reinterpret_cast<uint4 *>(vt + swz(e >> 3, c));
-                        if (key >= limit) {
-                            *at = make_uint4(0, 0, 0, 0);
-                            continue;
-                        }
-                        const uint4 w = *at;
-                        uint32_t v[4] = {w.x, w.y, w.z, w.w};
-                        bool bad = false;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) bad |= (v[q] & 0x7f80u) == 0x7f80u || (v[q] & 0x7f800000u) == 0x7f800000u;
-                        if (!bad) continue;
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            const uint32_t b = v[q >> 1] >> (16 * (q & 1)) & 0xffffu;
-                            if ((b & 0x7f80u) != 0x7f80u) continue;
-                            atomicMin(&rec->first[b & 0x7fu ? 2 : b >> 15][8 * c + q], tag | (key - least));
-                            v[q >> 1] &= q & 1 ? 0x0000ffffu : 0xffff0000u;
-                        }
-                        *at = make_uint4(v[0], v[1], v[2], v[3]);
-                        rec->piece = piece;
-                    }
-                    fence_proxy_async();  // the stage's next load comes after
-                    __syncwarp();
-                }
-                // Weights, in place of the scores.
-                float base[2], fo[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float mn = fmaxf(m[i], quad_max(top[i]));
-                    base[i] = mn == -INFINITY ? 0.f : mn;
-                    fo[i] = exp2_approx(m[i] - base[i]);
-                    l[i] *= fo[i];
-                    m[i] = mn;
-                }
-                if (QUANT) {
-                    const uint32_t vb = *reinterpret_cast<const uint16_t *>(vs + 2 * lane);
-                    const int hi = max(e_hi, static_cast<int>(__reduce_max_sync(kFull, max(vb & 255u, vb >> 8))));
-                    const int lo = min(e_lo, static_cast<int>(__reduce_min_sync(kFull, min(vb & 255u, vb >> 8))));
-                    near = near && plain && hi < 255 && hi - lo <= kNear;
-                    if (near) {
-                        e_hi = hi;
-                        e_lo = lo;
-                    }
-                }
-                if (near) {
-                    const uint32_t shift = static_cast<uint32_t>(e_hi - 127) * 0x0101u;
-                    const u64 nb[2] = {pack_f32x2(-base[0], -base[0]), pack_f32x2(-base[1], -base[1])};
-                    u64 sum[2] = {0ull, 0ull};
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const u64 g2 = powers(*reinterpret_cast<const uint16_t *>(vs + 8 * i + 2 * t4) - shift, t4);
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            const u64 w = exp2_f32x2(add_f32x2(pack_f32x2(s[i][2 * q], s[i][2 * q + 1]), nb[q]));
-                            sum[q] = add_f32x2(sum[q], w);
-                            const float2 v = unpack_f32x2(mul_f32x2(w, g2));
-                            s[i][2 * q] = v.x;
-                            s[i][2 * q + 1] = v.y;
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float2 v = unpack_f32x2(sum[i]);
-                        l[i] += v.x + v.y;
-                        const float mn = m[i] + static_cast<float>(e_hi - 127);
-                        fo[i] = exp2_approx(mo[i] - (mn == -INFINITY ? 0.f : mn));
-                        mo[i] = mn;
-                    }
-                } else {
-                    float base_o[2] = {base[0], base[1]};
-                    if (QUANT) {
-                        float top_o[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const uint32_t b = *reinterpret_cast<const uint16_t *>(vs + 8 * i + 2 * t4);
-                            const float e0 = exponent_of(t4 & 1 ? b >> 8 : b & 255u), e1 = exponent_of(t4 & 1 ? b & 255u : b >> 8);
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                l[q >> 1] += exp2_approx(s[i][q] - base[q >> 1]);
-                                s[i][q] = s[i][q] == -INFINITY ? -INFINITY : s[i][q] + (q & 1 ? e1 : e0);
-                                top_o[q >> 1] = fmaxf(top_o[q >> 1], s[i][q]);
-                            }
-                        }
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float mn = fmaxf(mo[i], quad_max(top_o[i]));
-                            base_o[i] = mn == -INFINITY ? 0.f : mn;
-                            fo[i] = exp2_approx(mo[i] - base_o[i]);
-                            mo[i] = mn;
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            s[i][q] = exp2_approx(s[i][q] - base_o[q >> 1]);
-                            if (!QUANT) l[q >> 1] += s[i][q];
-                        }
-                }
-                if (__any_sync(kFull, fo[0] != 1.f || fo[1] != 1.f)) {
-#pragma unroll
-                    for (int d = 0; d < 8; ++d)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) o[d][q] *= fo[q >> 1];
-                }
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {  // 16 keys a product
-                    uint32_t a[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float w0 = s[2 * c + (q >> 1)][2 * (q & 1)], w1 = s[2 * c + (q >> 1)][2 * (q & 1) + 1];
-                        a[q] = QUANT ? pack_half2(w0, w1) : pack2(w0, w1);
-                    }
-                    if (QUANT) {
-                        // Four dims of four keys a thread: bytes to pairs of
-                        // keys, pairs to halves.  Column g of product d is
-                        // dim 32 (d / 4) + 4 g + d % 4.
-#pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const int row = 16 * c + 8 * (q >> 1) + (q & 1 ? k1 : k0);
-                                w[q] = *reinterpret_cast<const uint32_t *>(vt + row * kD + 32 * hf + 4 * g);
-                                if (masked) {
-                                    // NaN codes meet weights of zero: none is
-                                    // left past the last key, or at all.
-                                    const uint32_t nan = ((w[q] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                                    w[q] = key0 + row >= limit ? 0u : w[q] - (nan >> 7);
-                                }
-                            }
-                            const uint32_t lo0 = __byte_perm(w[0], w[1], 0x5140), lo1 = __byte_perm(w[0], w[1], 0x7362);
-                            const uint32_t hi0 = __byte_perm(w[2], w[3], 0x5140), hi1 = __byte_perm(w[2], w[3], 0x7362);
-                            mma16816<true>(o[4 * hf + 0], a[0], a[1], a[2], a[3], halves_lo(lo0), halves_lo(hi0));
-                            mma16816<true>(o[4 * hf + 1], a[0], a[1], a[2], a[3], halves_hi(lo0), halves_hi(hi0));
-                            mma16816<true>(o[4 * hf + 2], a[0], a[1], a[2], a[3], halves_lo(lo1), halves_lo(hi1));
-                            mma16816<true>(o[4 * hf + 3], a[0], a[1], a[2], a[3], halves_hi(lo1), halves_hi(hi1));
-                        }
-                    } else {
-#pragma unroll
-                        for (int d = 0; d < 4; ++d) {
-                            const int row = 16 * c + (lane & 15);
-                            uint32_t b[4];
-                            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                                         : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3])
-                                         : "r"(smem_u32(vt) + swz(row, 2 * d + (lane >> 4)))
-                                         : "memory");
-                            mma16816<false>(o[2 * d], a[0], a[1], a[2], a[3], b[0], b[1]);
-                            mma16816<false>(o[2 * d + 1], a[0], a[1], a[2], a[3], b[2], b[3]);
-                        }
-                    }
-                }
-                __syncwarp();
-                load.next_v(p, kv_map, pieces, bar_piece, n, y);
+                alive = __builtin_expect(wide, 0)
+                            ? take_page<QUANT, 2>(R, load, p, kv_map, pieces, bar_piece, n, turn, key0, least, limit, rec,
+                                                  piece, lane, abort_flag)
+                            : take_page<QUANT, 1>(R, load, p, kv_map, pieces, bar_piece, n, turn, key0, least, limit, rec,
+                                                  piece, lane, abort_flag);
+                if (!alive) break;
             }
             if (!alive) break;
             // ---------------------------------------------------- merging --
             if (n > 0 && !warp_wait(bar_merged, (n - 1) & 1, abort_flag, p.status)) break;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float sum = quad_sum(l[i]);
-                if (t4 == 0) merge_s[warp * kSmallRows + g + 8 * i] = make_float4(m[i], sum, QUANT ? mo[i] : m[i], 0.f);
-                float *dst = merge_o + (warp * kSmallRows + g + 8 * i) * kORow;
+            for (int nt = 0; nt < 2; ++nt) {
+                if (nt == 1 && !wide) break;
+                float *dst = merge_o + (warp * kSmallRows + 8 * nt + 2 * t4) * kORow;
 #pragma unroll
-                for (int d = 0; d < 8; ++d) {
-                    const int dim = QUANT ? 32 * (d >> 2) + 8 * t4 + (d & 3) : 8 * d + 2 * t4;
-                    dst[dim] = o[d][2 * i];
-                    dst[dim + (QUANT ? 4 : 1)] = o[d][2 * i + 1];
+                for (int c = 0; c < 2; ++c) {
+                    const float sum = keys_sum(R.l[nt][c]);
+                    if (g == 0)
+                        merge_s[warp * kSmallRows + 8 * nt + 2 * t4 + c] =
+                            make_float4(R.m[nt][c], sum, QUANT ? R.mo[nt][c] : R.m[nt][c], 0.f);
                 }
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int dim = QUANT ? 32 * (d >> 1) + 4 * g + 2 * (d & 1) + (e >> 1) : 16 * d + g + 8 * (e >> 1);
+                        dst[(e & 1) * kORow + dim] = R.o[nt][d][e];
+                    }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_left);
-            if (!warp_wait(bar_left, n & 1, abort_flag, p.status)) break;
-            if (warp < 8) {
-                // A row's four dims a thread.
-                const int rho = threadIdx.x >> 4, dim = 4 * (threadIdx.x & 15), token = rho / p.G;
-                float mt = -INFINITY;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, merge_s[w * kSmallRows + rho].x);
-                const float me = mt == -INFINITY ? 0.f : mt;
-                float lt = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float4 st = merge_s[w * kSmallRows + rho];
-                    const float4 part = *reinterpret_cast<const float4 *>(merge_o + (w * kSmallRows + rho) * kORow + dim);
-                    const float f = exp2_approx(st.z - me);
-                    lt += st.y * exp2_approx(st.x - me);
-                    v[0] += part.x * f;
-                    v[1] += part.y * f;
-                    v[2] += part.z * f;
-                    v[3] += part.w * f;
-                }
-                const bool whole = it.t0 == 0 && it.t1 == it.nt;
-                const float norm = whole ? 1.f / lt : 1.f;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] = lt == 0.f ? 0.f : v[q] * norm;
-                const Records &rec = recs[piece % kRecords];
-                const int row_sees = token < it.tokens ? keys_seen(p, it.ctx, it.n, token) : 0;
-                if (!QUANT && pages > 0 && rec.piece == piece) {
-                    const uint32_t tag = ~static_cast<uint32_t>(piece) << 8;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        for (int kind = 0; kind < 3; ++kind) {
-                            const uint32_t e = rec.first[kind][dim + q];
-                            if ((e & 0xffffff00u) != tag || least + static_cast<int>(e & 0xffu) >= row_sees) continue;
-                            v[q] = kind == 2 ? __uint_as_float(0x7fffffffu) : v[q] + (kind == 0 ? INFINITY : -INFINITY);
-                        }
-                }
-                if (token < it.tokens) {
-                    const long long at = static_cast<long long>(it.row + token) * p.Hq + it.h * p.G + rho - token * p.G;
-                    const int part = (blockIdx.x * 2 + (it.t0 > 0 ? 0 : 1)) * kSmallRows + rho;
-                    if (whole) {
-                        *reinterpret_cast<uint2 *>(p.out + at * kD + dim) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
-                        if (dim == 0 && p.lse) p.lse[at] = lt == 0.f ? -INFINITY : (mt + log2f(lt)) * 0.6931471805599453f;
-                    } else {
-                        *reinterpret_cast<float4 *>(p.part_o + static_cast<long long>(part) * kD + dim) =
-                            make_float4(v[0], v[1], v[2], v[3]);
-                        if (dim == 0) p.part_ml[part] = make_float2(mt, lt);
-                    }
-                }
-            }
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(bar_merged);
-                mbar_arrive(bar_pdone + 8 * (n % kRing));
-            }
         }
         load.drain();
     }
@@ -755,7 +844,7 @@ int launch(const CUtensorMap &kv_map, const ChunkParams &p, bool after_long, cud
 int launch_small(const ChunkParams &p, const void *kv_pool, bool quant, bool after_long, cudaStream_t stream) {
     const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     CUtensorMap kv_map;
-    if (encode == nullptr || !pool_map(encode, &kv_map, kv_pool, p.num_pages, p.Hkv, quant)) return K3DA_ECUDA;
+    if (encode == nullptr || !pool_map(encode, &kv_map, kv_pool, p.num_pages, p.Hkv, quant, true)) return K3DA_ECUDA;
     return quant ? launch<true>(kv_map, p, after_long, stream) : launch<false>(kv_map, p, after_long, stream);
 }
 

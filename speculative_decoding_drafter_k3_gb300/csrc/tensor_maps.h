@@ -27,16 +27,16 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 }
 
 // A pool as rows of 64 dims, in boxes of a page's 64 slots: bf16 with the
-// 128-byte swizzle the products read, codes as they lie.
+// 128-byte swizzle, codes as they lie or with the 64-byte swizzle.
 inline bool pool_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *map, const void *pool, long long num_pages,
-                     int hkv, bool quant) {
+                     int hkv, bool quant, bool swizzled) {
     using namespace k3da_cache;
     const cuuint64_t dims[2] = {kD, static_cast<cuuint64_t>(num_pages) * 2 * hkv * kP};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kD) * (quant ? 1 : 2)};
     const cuuint32_t box[2] = {kD, kP}, estrides[2] = {1, 1};
     return encode(map, quant ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
                   const_cast<void *>(pool), dims, strides, box, estrides, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  quant ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  !swizzled ? CU_TENSOR_MAP_SWIZZLE_NONE : quant ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
