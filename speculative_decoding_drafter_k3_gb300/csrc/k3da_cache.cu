@@ -30,6 +30,19 @@ namespace {
 
 using namespace k3da_cache;
 
+// 32 bytes to 16-byte aligned memory, in one store where `whole` (32-byte
+// aligned): two stores of half a sector each cost the L2 twice.
+__device__ __forceinline__ void store32(uint4 *dst, uint4 a, uint4 b, bool whole) {
+    if (whole) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a.x), "r"(a.y), "r"(a.z),
+                     "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                     : "memory");
+    } else {
+        dst[0] = a;
+        dst[1] = b;
+    }
+}
+
 // -------------------------------------------------------------- quantising --
 
 // e8m0 byte of a row whose largest magnitude has these fp32 bits: 448 is
@@ -91,6 +104,7 @@ __device__ __forceinline__ uint2 values4(uint32_t c, float mul) {
 constexpr int kAppendThreads = 256;
 constexpr int kAppendRows = kAppendThreads / 2;
 constexpr int kAppendTokens = 64;  // most tokens of a CTA
+constexpr int kAppendWave = 2 * 152;  // CTAs that run at once
 
 struct AppendParams {
     const __nv_bfloat16 *qkv;
@@ -181,7 +195,6 @@ __global__ void __launch_bounds__(kAppendThreads) k3da_kv_append_kernel(const __
 
     for (int base = 0; base < ntok * p.rows; base += kAppendRows) {
         const int rl = base + (tid >> 1);
-        if (base > 0) load(rl);
         const bool valid = rl < ntok * p.rows;
         const int tl = valid ? rl / p.rows : 0;
         const int h = valid ? skip + rl - tl * p.rows : heads - 1;
@@ -197,6 +210,7 @@ __global__ void __launch_bounds__(kAppendThreads) k3da_kv_append_kernel(const __
                 hi[2 * e + 1] = bf16_hi(bv[e]);
             }
         }
+        load(rl + kAppendRows);
         if (NORM) {
             float ss = 0.f;
 #pragma unroll
@@ -245,14 +259,17 @@ __global__ void __launch_bounds__(kAppendThreads) k3da_kv_append_kernel(const __
             }
         }
         if (dst != nullptr) {
+            const bool whole = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
+            uint4 w[4];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                dst[2 * hp + c] = make_uint4(pack2(lo[8 * c], lo[8 * c + 1]), pack2(lo[8 * c + 2], lo[8 * c + 3]),
-                                             pack2(lo[8 * c + 4], lo[8 * c + 5]), pack2(lo[8 * c + 6], lo[8 * c + 7]));
-                dst[4 + 2 * hp + c] =
-                    make_uint4(pack2(hi[8 * c], hi[8 * c + 1]), pack2(hi[8 * c + 2], hi[8 * c + 3]),
-                               pack2(hi[8 * c + 4], hi[8 * c + 5]), pack2(hi[8 * c + 6], hi[8 * c + 7]));
+                w[c] = make_uint4(pack2(lo[8 * c], lo[8 * c + 1]), pack2(lo[8 * c + 2], lo[8 * c + 3]),
+                                  pack2(lo[8 * c + 4], lo[8 * c + 5]), pack2(lo[8 * c + 6], lo[8 * c + 7]));
+                w[2 + c] = make_uint4(pack2(hi[8 * c], hi[8 * c + 1]), pack2(hi[8 * c + 2], hi[8 * c + 3]),
+                                      pack2(hi[8 * c + 4], hi[8 * c + 5]), pack2(hi[8 * c + 6], hi[8 * c + 7]));
             }
+            store32(dst + 2 * hp, w[0], w[1], whole);
+            store32(dst + 4 + 2 * hp, w[2], w[3], whole);
         }
     }
 }
@@ -263,7 +280,8 @@ __global__ void __launch_bounds__(kAppendThreads) k3da_kv_append_kernel(const __
 // or 16 codes and the row's scale in, 32 bytes out.  A thread issues the
 // loads of all its rows before it stores any.  Bound by memory.
 constexpr int kGatherThreads = 256;
-constexpr int kGatherTokens = 64;  // most tokens of a CTA
+constexpr int kGatherTokens = 256;  // most tokens of a CTA
+constexpr int kGatherWave = 4 * 152;  // CTAs that run at once
 constexpr int kGatherItems = 4;    // row quarters of a thread in flight
 
 struct GatherParams {
@@ -348,13 +366,22 @@ __global__ void __launch_bounds__(kGatherThreads) k3da_kv_gather_kernel(const __
             uint4 *dst = reinterpret_cast<uint4 *>((kv ? p.v_out : p.k_out) +
                                                    (static_cast<long long>(t0 + tl) * p.Hkv + head) * kD) +
                          2 * quarter;
-            dst[0] = x[k];
-            dst[1] = y[k];
+            store32(dst, x[k], y[k], (reinterpret_cast<uintptr_t>(dst) & 31) == 0);
         }
     }
 }
 
 // -------------------------------------------------------------------- host --
+
+// Tokens of a CTA: as many as its threads take at once, and so many times
+// that where the call would fill the SMs more than once (what a CTA does
+// before its first row is two dependent loads and a search).
+inline int tokens_of(int T, int at_once, int most, int wave) {
+    if (at_once < 1) at_once = 1;
+    const long long ctas = (static_cast<long long>(T) + at_once - 1) / at_once;
+    const long long tokens = (ctas + wave - 1) / wave * at_once;
+    return static_cast<int>(tokens < most ? tokens : most);
+}
 
 int launch_append(void *kv_pool, int cache_dtype, void *kv_scales, int64_t num_pages, const int32_t *page_table,
                   int page_stride, const int32_t *ctx_lens, const int32_t *cu_seqlens, int R, const void *qkv,
@@ -405,9 +432,7 @@ int launch_append(void *kv_pool, int cache_dtype, void *kv_scales, int64_t num_p
     prm.Hq = Hq;
     prm.Hkv = Hkv;
     prm.rows = 2 * Hkv + (norm && q_out ? Hq : 0);
-    prm.tokens_per_cta = kAppendRows / prm.rows;
-    if (prm.tokens_per_cta < 1) prm.tokens_per_cta = 1;
-    if (prm.tokens_per_cta > kAppendTokens) prm.tokens_per_cta = kAppendTokens;
+    prm.tokens_per_cta = tokens_of(T, kAppendRows / prm.rows, kAppendTokens, kAppendWave);
     prm.pos_i64 = pos_dtype == K3DA_POS_I64;
     prm.eps = eps;
     prm.mscale = 1.0f;
@@ -484,9 +509,7 @@ extern "C" int k3da_kv_gather(void *k_out, void *v_out, const void *kv_pool, int
     // SMs without work.
     const long long items = static_cast<long long>(num_tokens) * num_kv_heads * 8;
     const int per_cta = items >= 304LL * kGatherThreads * kGatherItems ? kGatherThreads * kGatherItems : kGatherThreads;
-    prm.tokens_per_cta = per_cta / (num_kv_heads * 8);
-    if (prm.tokens_per_cta < 1) prm.tokens_per_cta = 1;
-    if (prm.tokens_per_cta > kGatherTokens) prm.tokens_per_cta = kGatherTokens;
+    prm.tokens_per_cta = tokens_of(num_tokens, per_cta / (num_kv_heads * 8), kGatherTokens, kGatherWave);
     const unsigned ctas =
         static_cast<unsigned>((static_cast<long long>(num_tokens) + prm.tokens_per_cta - 1) / prm.tokens_per_cta);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
