@@ -301,7 +301,7 @@ struct GatherParams {
 template <bool QUANT>
 __global__ void __launch_bounds__(kGatherThreads) k3da_kv_gather_kernel(const __grid_constant__ GatherParams p) {
     __shared__ int32_t cu[kMaxRequests + 1];
-    __shared__ long long slot[kGatherTokens];  // page * 64 + slot, -1: zeros, -2: the row is left alone
+    __shared__ long long slot[kGatherTokens];  // first row of the token's page and its slot, -1: zeros, -2: the row is left alone
     const int tid = threadIdx.x;
     const int t0 = blockIdx.x * p.tokens_per_cta;
     const int ntok = min(p.T - t0, p.tokens_per_cta);
@@ -318,44 +318,54 @@ __global__ void __launch_bounds__(kGatherThreads) k3da_kv_gather_kernel(const __
                 if (p.status) atomicOr(p.status, K3DA_STATUS_BAD_LENGTH);
             } else {
                 const long long page = page_of(p.page_table, p.page_stride, p.num_pages, r, static_cast<int>(c));
-                if (page >= 0) at = page * kP + c % kP;
+                if (page >= 0) at = page * 2 * p.Hkv * kP + c % kP;
                 else if (p.status) atomicOr(p.status, K3DA_STATUS_BAD_PAGE);
             }
         }
         slot[tid] = at;
     }
     __syncthreads();
-    const int per_token = p.Hkv * 8;  // row quarters of a token
-    const int items = ntok * per_token;
-    for (int base = 0; base < items; base += kGatherThreads * kGatherItems) {
+    // The thread's quarters: token tl's quarter `rest` (K's heads, then V's),
+    // kGatherThreads further on each time.
+    const int per_token = p.Hkv * 8, half = p.Hkv * 4;
+    const int step = kGatherThreads / per_token, over = kGatherThreads - step * per_token;
+    int tl = tid / per_token, rest = tid - tl * per_token;
+    while (tl < ntok) {
         uint4 x[kGatherItems], y[kGatherItems];
         uint32_t sc[kGatherItems];
+        __nv_bfloat16 *dst[kGatherItems];
 #pragma unroll
         for (int k = 0; k < kGatherItems; ++k) {
-            const int e = base + k * kGatherThreads + tid;
             x[k] = y[k] = make_uint4(0, 0, 0, 0);
             sc[k] = 127u;
-            if (e >= items) continue;
-            const int tl = e / per_token, rest = e - tl * per_token;
-            const int kv = rest >= p.Hkv * 4, head = (rest >> 2) - kv * p.Hkv, quarter = rest & 3;
-            if (slot[tl] < 0) continue;
-            const long long row = ((slot[tl] / kP * 2 + kv) * p.Hkv + head) * kP + slot[tl] % kP;
-            if (QUANT) {
-                x[k] = __ldg(reinterpret_cast<const uint4 *>(p.pool + row * kD) + quarter);
-                sc[k] = __ldg(p.scales + row);
-            } else {
-                const uint4 *src = reinterpret_cast<const uint4 *>(p.pool + row * (kD * 2)) + 2 * quarter;
-                x[k] = __ldg(src);
-                y[k] = __ldg(src + 1);
+            dst[k] = nullptr;
+            const long long at = tl < ntok ? slot[tl] : -2;
+            if (at != -2) {
+                const int in_half = rest < half ? rest : rest - half;
+                dst[k] = (rest < half ? p.k_out : p.v_out) + (static_cast<long long>(t0 + tl) * half + in_half) * (kD / 4);
+                if (at >= 0) {
+                    const long long row = at + (rest >> 2) * kP;
+                    const int quarter = rest & 3;
+                    if (QUANT) {
+                        x[k] = __ldg(reinterpret_cast<const uint4 *>(p.pool + row * kD) + quarter);
+                        sc[k] = __ldg(p.scales + row);
+                    } else {
+                        const uint4 *src = reinterpret_cast<const uint4 *>(p.pool + row * (kD * 2)) + 2 * quarter;
+                        x[k] = __ldg(src);
+                        y[k] = __ldg(src + 1);
+                    }
+                }
+            }
+            tl += step;
+            rest += over;
+            if (rest >= per_token) {
+                rest -= per_token;
+                ++tl;
             }
         }
 #pragma unroll
         for (int k = 0; k < kGatherItems; ++k) {
-            const int e = base + k * kGatherThreads + tid;
-            if (e >= items) continue;
-            const int tl = e / per_token, rest = e - tl * per_token;
-            const int kv = rest >= p.Hkv * 4, head = (rest >> 2) - kv * p.Hkv, quarter = rest & 3;
-            if (slot[tl] == -2) continue;
+            if (dst[k] == nullptr) continue;
             if (QUANT) {
                 const float mul = scale_of(sc[k]);
                 const uint2 v0 = values4(x[k].x, mul), v1 = values4(x[k].y, mul), v2 = values4(x[k].z, mul),
@@ -363,10 +373,7 @@ __global__ void __launch_bounds__(kGatherThreads) k3da_kv_gather_kernel(const __
                 x[k] = make_uint4(v0.x, v0.y, v1.x, v1.y);
                 y[k] = make_uint4(v2.x, v2.y, v3.x, v3.y);
             }
-            uint4 *dst = reinterpret_cast<uint4 *>((kv ? p.v_out : p.k_out) +
-                                                   (static_cast<long long>(t0 + tl) * p.Hkv + head) * kD) +
-                         2 * quarter;
-            store32(dst, x[k], y[k], (reinterpret_cast<uintptr_t>(dst) & 31) == 0);
+            store32(reinterpret_cast<uint4 *>(dst[k]), x[k], y[k], (reinterpret_cast<uintptr_t>(dst[k]) & 31) == 0);
         }
     }
 }
