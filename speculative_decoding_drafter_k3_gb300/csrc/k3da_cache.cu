@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kAppendThreads) k3da_kv_append_kernel(const __
     __shared__ float2 trig[NORM ? kAppendTokens * (kD / 2) : 1];
     __shared__ float wsm[NORM ? 2 * kD : 1];
     __shared__ int32_t cu[kMaxRequests + 1];
-    __shared__ long long slot[kAppendTokens];  // page * 64 + slot of the token, or -1: nothing is written
+    __shared__ long long slot[kAppendTokens];  // first row of the token's page and its slot, -1: nothing is written
     __shared__ bool real[kAppendTokens];       // the token is some request's
     const int tid = threadIdx.x;
     const int t0 = blockIdx.x * p.tokens_per_cta;
@@ -143,17 +143,20 @@ __global__ void __launch_bounds__(kAppendThreads) k3da_kv_append_kernel(const __
     const int hp = tid & 1;
 
     uint4 a0, a1, b0, b1;
-    auto load = [&](int rl) {
+    // The thread's rows: head row h of token tl, kAppendRows further on each
+    // time; next_* is the row whose loads are on their way.
+    const int step = kAppendRows / p.rows, over = kAppendRows - step * p.rows;
+    int next_tl = (tid >> 1) / p.rows, next_h = skip + (tid >> 1) - next_tl * p.rows;
+    auto load = [&](int tl, int h) {
         a0 = a1 = b0 = b1 = make_uint4(0, 0, 0, 0);
-        if (rl >= ntok * p.rows) return;
-        const int tl = rl / p.rows, h = skip + rl - tl * p.rows;
+        if (tl >= ntok) return;
         const uint4 *x = reinterpret_cast<const uint4 *>(p.qkv + (static_cast<long long>(t0 + tl) * heads + h) * kD);
         a0 = __ldg(x + 2 * hp);
         a1 = __ldg(x + 2 * hp + 1);
         b0 = __ldg(x + 4 + 2 * hp);
         b1 = __ldg(x + 4 + 2 * hp + 1);
     };
-    load(tid >> 1);
+    load(next_tl, next_h);
     if (NORM) {
         unsigned long long rate = 0;  // read with constant indices: a lane-dependent one would serialise the warp
 #pragma unroll
@@ -184,7 +187,7 @@ __global__ void __launch_bounds__(kAppendThreads) k3da_kv_append_kernel(const __
                 if (p.status) atomicOr(p.status, K3DA_STATUS_BAD_LENGTH);
             } else {
                 const long long page = page_of(p.page_table, p.page_stride, p.num_pages, r, static_cast<int>(c));
-                if (page >= 0) at = page * kP + c % kP;
+                if (page >= 0) at = page * 2 * p.Hkv * kP + c % kP;
                 else if (p.status) atomicOr(p.status, K3DA_STATUS_BAD_PAGE);
             }
         }
@@ -194,10 +197,14 @@ __global__ void __launch_bounds__(kAppendThreads) k3da_kv_append_kernel(const __
     __syncthreads();
 
     for (int base = 0; base < ntok * p.rows; base += kAppendRows) {
-        const int rl = base + (tid >> 1);
-        const bool valid = rl < ntok * p.rows;
-        const int tl = valid ? rl / p.rows : 0;
-        const int h = valid ? skip + rl - tl * p.rows : heads - 1;
+        const bool valid = next_tl < ntok;
+        const int tl = valid ? next_tl : 0, h = valid ? next_h : heads - 1;
+        next_tl += step;
+        next_h += over;
+        if (next_h >= heads) {
+            next_h -= p.rows;
+            ++next_tl;
+        }
         float lo[16], hi[16];
         {
             const uint32_t av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
@@ -210,7 +217,7 @@ __global__ void __launch_bounds__(kAppendThreads) k3da_kv_append_kernel(const __
                 hi[2 * e + 1] = bf16_hi(bv[e]);
             }
         }
-        load(rl + kAppendRows);
+        load(next_tl, next_h);
         if (NORM) {
             float ss = 0.f;
 #pragma unroll
@@ -243,9 +250,7 @@ __global__ void __launch_bounds__(kAppendThreads) k3da_kv_append_kernel(const __
         if (h < p.Hq) {
             if (real[tl]) dst = reinterpret_cast<uint4 *>(p.q_out + (static_cast<long long>(t0 + tl) * p.Hq + h) * kD);
         } else if (slot[tl] >= 0) {
-            const int kv = h >= p.Hq + p.Hkv;
-            const int head = h - p.Hq - kv * p.Hkv;
-            const long long row = ((slot[tl] / kP * 2 + kv) * p.Hkv + head) * kP + slot[tl] % kP;
+            const long long row = slot[tl] + (h - p.Hq) * kP;
             if (QUANT) {
                 const uint32_t b = scale_byte(top);
                 const float mul = b == 255u ? 0.f : __uint_as_float((254u - b) << 23);  // 2^(127 - b)
