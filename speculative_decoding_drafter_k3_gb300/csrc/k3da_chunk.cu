@@ -544,13 +544,13 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
                 float v[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(o[j]);
+                // Each row is another line: a store takes a cycle a thread,
+                // whatever it brings.
                 if (whole) {
                     *reinterpret_cast<uint4 *>(p.out + (static_cast<long long>(row) * p.Hq + head) * kD + d0) =
                         make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
                 } else {
-                    float4 *dst = reinterpret_cast<float4 *>(p.part_o + static_cast<long long>(part) * kD + d0);
-                    dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-                    dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+                    store32(p.part_o + static_cast<long long>(part) * kD + d0, v);
                 }
             }
             fence_before();

@@ -108,6 +108,13 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// 32 bytes to a 32-byte boundary in one store.
+__device__ __forceinline__ void store32(float *dst, const float (&v)[8]) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                 "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
+
 // ----------------------------------------------------------------- tcgen05 --
 
 // Instruction descriptor of kind::f16: D fp32 (bits 4-5 = 1), A and B bf16
