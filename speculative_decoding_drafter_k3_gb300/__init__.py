@@ -457,7 +457,9 @@ def k3da_kv_append_qknorm(kv_pool, qkv, page_table, ctx_lens, cu_seqlens, positi
     given (C: k3da_kv_append_qknorm).  Returns ``kv_pool``."""
     dev, D, args = _cache_args(kv_pool, kv_scales, page_table, ctx_lens, cu_seqlens, num_kv_heads, status)
     T = _qkv_rows(qkv, num_q_heads, num_kv_heads, D, dev)
-    _on(dev, positions=positions, q_norm_w=q_norm_w, k_norm_w=k_norm_w, q_out=q_out)
+    for t in (positions, q_norm_w, k_norm_w):
+        if t.get_device() != dev or not t.is_contiguous():
+            raise K3daError(f"positions and norm weights must be contiguous and on the cache's device (cuda:{dev})")
     if positions.dtype is torch.int64:
         code = POS_I64
     elif positions.dtype is torch.int32:
@@ -469,8 +471,9 @@ def k3da_kv_append_qknorm(kv_pool, qkv, page_table, ctx_lens, cu_seqlens, positi
     if q_norm_w.dtype is not torch.bfloat16 or k_norm_w.dtype is not torch.bfloat16 or \
             q_norm_w.numel() != D or k_norm_w.numel() != D:
         raise K3daError("norm weights must be [64] bf16")
-    if q_out is not None and (q_out.dtype is not torch.bfloat16 or q_out.shape != (T, num_q_heads * D)):
-        raise K3daError("q_out must be [T, Hq*64] bf16")
+    if q_out is not None and (q_out.dtype is not torch.bfloat16 or q_out.shape != (T, num_q_heads * D) or
+                              q_out.get_device() != dev or not q_out.is_contiguous()):
+        raise K3daError("q_out must be [T, Hq*64] bf16, contiguous and on the cache's device")
     _enqueue("k3da_kv_append_qknorm", dev, stream, status, *args, qkv.data_ptr(), T, num_q_heads, num_kv_heads, D,
              positions.data_ptr(), code, q_norm_w.data_ptr(), k_norm_w.data_ptr(), eps, rope_base,
              None if yarn is None else ctypes.byref(yarn), _addr(q_out))
@@ -521,7 +524,9 @@ def k3da_chunk_attn(out, q, kv_pool, page_table, ctx_lens, cu_seqlens, *, num_q_
             (shape[0] and q.stride(1) != 1):
         raise K3daError("q must be [T, Hq*64] bf16 on the cache's device, each row contiguous")
     T = shape[0]
-    _on(dev, out=out, lse=lse, workspace=workspace)
+    for t in (out, workspace) if lse is None else (out, workspace, lse):
+        if t.get_device() != dev or not t.is_contiguous():
+            raise K3daError(f"out, lse and workspace must be contiguous and on the cache's device (cuda:{dev})")
     if out.dtype is not torch.bfloat16 or out.shape != shape:
         raise K3daError("out must be [T, Hq*64] bf16")
     if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (T, num_q_heads)):

@@ -19,6 +19,7 @@ constexpr int kTile = 128;         // keys of a tile: two pages
 constexpr int kSlotRows = 128;     // query rows of a slot
 constexpr int kOverhead = 128;     // an item's fixed cost, in keys
 constexpr int kMinSlice = 256;     // shortest slice, in keys
+constexpr int kMinSmallSlice = 512;  // ... of the small kernel: a page for each of its warps
 
 struct ChunkParams {
     __nv_bfloat16 *out;
@@ -38,14 +39,15 @@ struct ChunkParams {
     int G;    // query heads per kv head
     int tpt;  // tokens of a slot
     int mask;
-    int pass;       // 0: the items of long chunks; 1: those of at most kSmallRows rows
+    int pass;       // which items: kLong, kSmall or kAll
     int part_rows;  // rows of a partial result
     float scale_log2;
 };
 
 // A request whose chunk is this small (query rows of a kv head) is the small
-// kernel's.
+// kernel's, but in calls that are all latency (kAll).
 constexpr int kSmallRows = 16;
+enum { kLong, kSmall, kAll };
 
 // What a CTA leaves for the combine kernel.  part 0: the piece it began with
 // belongs to an item begun before; part 1: the item it ended with goes on in
@@ -96,8 +98,8 @@ struct Request {
     }
     // Items of one kv head in this pass.
     __device__ __forceinline__ int pairs(const ChunkParams &p) const {
-        const bool small = n <= kSmallRows && n * p.G <= kSmallRows;
-        if (n == 0 || small != (p.pass == 1)) return 0;
+        const bool small = p.pass != kAll && n <= kSmallRows && n * p.G <= kSmallRows;
+        if (n == 0 || small != (p.pass == kSmall)) return 0;
         return small ? 1 : (n + 2 * p.tpt - 1) / (2 * p.tpt);
     }
     // Keys of the line before a causal chunk's own.
@@ -199,7 +201,7 @@ struct Walk {
     }
     __device__ void begin(const ChunkParams &p, const Plan *pl, int cta) {
         total = pl->prefix[p.R];
-        slices = total / kMinSlice;
+        slices = total / (p.pass == kSmall ? kMinSmallSlice : kMinSlice);
         slices = slices < 1 ? 1 : slices > kCtas ? kCtas : slices;
         lo = hi = at = 0;
         r = h = pair = 0;

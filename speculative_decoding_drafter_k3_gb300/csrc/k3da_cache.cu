@@ -395,6 +395,28 @@ inline int tokens_of(int T, int at_once, int most, int wave) {
     return static_cast<int>(tokens < most ? tokens : most);
 }
 
+// Turn rates of the rotary pairs.  A thread keeps those of the base and YaRN
+// that it had last: they take 1 us, a quarter of a small call's host time.
+inline void turn_rates(unsigned long long (&rate)[kD / 2], float base, const k3da_yarn *yarn) {
+    struct Last {
+        float base = 0.f;  // no base is 0
+        k3da_yarn yarn;    // factor 0: none
+        unsigned long long rate[kD / 2];
+    };
+    thread_local Last last;
+    k3da_yarn y;
+    std::memset(&y, 0, sizeof y);
+    if (yarn != nullptr) y = *yarn;
+    if (last.base != base || std::memcmp(&last.yarn, &y, sizeof y) != 0) {
+        double inv_freq[kD / 2];
+        k3da_host::rope_frequencies(inv_freq, kD / 2, base, yarn);
+        for (int j = 0; j < kD / 2; ++j) last.rate[j] = k3da_host::turn_rate_fixed64(inv_freq[j]);
+        last.base = base;
+        last.yarn = y;
+    }
+    std::memcpy(rate, last.rate, sizeof last.rate);
+}
+
 int launch_append(void *kv_pool, int cache_dtype, void *kv_scales, int64_t num_pages, const int32_t *page_table,
                   int page_stride, const int32_t *ctx_lens, const int32_t *cu_seqlens, int R, const void *qkv,
                   int T, int Hq, int Hkv, int head_dim, bool norm, const void *positions, int pos_dtype,
@@ -449,9 +471,7 @@ int launch_append(void *kv_pool, int cache_dtype, void *kv_scales, int64_t num_p
     prm.eps = eps;
     prm.mscale = 1.0f;
     if (norm) {
-        double inv_freq[kD / 2];
-        k3da_host::rope_frequencies(inv_freq, kD / 2, rope_base, yarn);
-        for (int j = 0; j < kD / 2; ++j) prm.turn_rate[j] = k3da_host::turn_rate_fixed64(inv_freq[j]);
+        turn_rates(prm.turn_rate, rope_base, yarn);
         if (yarn != nullptr) prm.mscale = k3da_host::yarn_mscale(yarn);
     }
     const unsigned ctas = static_cast<unsigned>((static_cast<long long>(T) + prm.tokens_per_cta - 1) / prm.tokens_per_cta);

@@ -996,9 +996,7 @@ __global__ void __launch_bounds__(kCombineThreads)
 
 template <bool QUANT>
 int launch_kernel(const CUtensorMap &kv_map, const CUtensorMap &q_map, const ChunkParams &prm, cudaStream_t st) {
-    // Set at every call: a context has its own copy of the attribute.
-    if (cudaFuncSetAttribute(k3da_chunk_kernel<QUANT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Smem<QUANT>::kBytes) != cudaSuccess)
+    if (!allow_smem<QUANT>(reinterpret_cast<const void *>(k3da_chunk_kernel<QUANT>), Smem<QUANT>::kBytes))
         return K3DA_ECUDA;
     k3da_chunk_kernel<QUANT><<<kCtas, threads_of(QUANT), Smem<QUANT>::kBytes, st>>>(kv_map, q_map, prm);
     return cudaGetLastError() == cudaSuccess ? K3DA_OK : K3DA_ECUDA;
@@ -1086,31 +1084,40 @@ extern "C" int k3da_chunk_attn(void *out, float *lse, const void *q, int64_t q_r
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool quant = cache_dtype == K3DA_CACHE_E4M3;
     // Which requests are small is known to the kernels alone; that none can
-    // be long is known from the number of tokens.
-    const bool any_long = num_tokens > kSmallRows || num_tokens * prm.G > kSmallRows;
+    // be long is known from the number of tokens.  A call whose caches are
+    // small, whatever their lengths, is bound by latency: one kernel for all
+    // (8 x 6 tokens over up to 2041, 6/1 heads: 16.4 us, with both 18.6; the
+    // small kernel's gain on 64 x 8000 codes comes to those 3 us at 75000 keys).
+    const long long line = static_cast<long long>(num_requests) * num_kv_heads *
+                           (static_cast<long long>(page_stride) * kP + kOverhead + 2 * prm.tpt + kSmallRows);
+    const bool can_be_long = num_tokens > kSmallRows || num_tokens * prm.G > kSmallRows;
+    const bool one_kernel = can_be_long && line <= static_cast<long long>(kCtas) * kMinSmallSlice;
+    prm.pass = one_kernel ? kAll : kLong;
     ChunkParams small = prm;
-    small.pass = 1;
+    small.pass = kSmall;
     parts_at(small, ws + part_bytes(2 * kSlotRows), kSmallRows);
-    if (any_long) {
+    if (can_be_long) {
         const int launched = launch_long(prm, q, kv_pool, quant, st);
         if (launched != K3DA_OK) return launched;
     }
-    const int launched = launch_small(small, kv_pool, quant, any_long, st);
-    if (launched != K3DA_OK) return launched;
-
+    if (!one_kernel) {
+        const int launched = launch_small(small, kv_pool, quant, can_be_long, st);
+        if (launched != K3DA_OK) return launched;
+    }
+    // Where all there can be fits one slice, nothing is cut (a token over 300:
+    // 8.5 instead of 9.6 us).
+    if (!can_be_long && line < 2 * kMinSmallSlice) return K3DA_OK;
     // Items a cut can fall into, rows one can have: a grid of about 1200
     // CTAs over both.
     const long long items =
         ((static_cast<long long>(num_tokens) + 2 * prm.tpt - 1) / (2 * prm.tpt) + num_requests) * num_kv_heads;
     const unsigned gx = static_cast<unsigned>(items < kCtas ? items : kCtas);
-    const long long bound = !any_long ? num_tokens * prm.G
-                            : num_tokens <= prm.tpt ? num_tokens * prm.G
-                                                    : 2 * kSlotRows;
+    const long long bound = num_tokens <= prm.tpt ? num_tokens * prm.G : 2 * kSlotRows;
     int rows = static_cast<int>((bound * gx + 1215) / 1216);
     rows = rows < 2 ? 2 : rows;
     cudaLaunchConfig_t lc;
     std::memset(&lc, 0, sizeof lc);
-    lc.gridDim = dim3(gx, static_cast<unsigned>((bound + rows - 1) / rows), any_long ? 2 : 1);
+    lc.gridDim = dim3(gx, static_cast<unsigned>((bound + rows - 1) / rows), can_be_long && !one_kernel ? 2 : 1);
     lc.blockDim = dim3(kCombineThreads);
     lc.stream = st;
     cudaLaunchAttribute attr[1];
@@ -1118,5 +1125,5 @@ extern "C" int k3da_chunk_attn(void *out, float *lse, const void *q, int64_t q_r
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = attr;
     lc.numAttrs = 1;
-    return cudaLaunchKernelEx(&lc, k3da_chunk_combine_kernel, small, prm, rows) == cudaSuccess ? K3DA_OK : K3DA_ECUDA;
+    return cudaLaunchKernelEx(&lc, k3da_chunk_combine_kernel, one_kernel ? prm : small, prm, rows) == cudaSuccess ? K3DA_OK : K3DA_ECUDA;
 }

@@ -821,9 +821,7 @@ __global__ void __launch_bounds__(Smem<QUANT>::kThreads, 1)
 
 template <bool QUANT>
 int launch(const CUtensorMap &kv_map, const ChunkParams &p, bool after_long, cudaStream_t stream) {
-    // Set at every call: a context has its own copy of the attribute.
-    if (cudaFuncSetAttribute(k3da_chunk_small_kernel<QUANT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Smem<QUANT>::kBytes) != cudaSuccess)
+    if (!allow_smem<2 + QUANT>(reinterpret_cast<const void *>(k3da_chunk_small_kernel<QUANT>), Smem<QUANT>::kBytes))
         return K3DA_ECUDA;
     cudaLaunchConfig_t lc;
     std::memset(&lc, 0, sizeof lc);

@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
+#include <stdint.h>
 
 #include <mutex>
 
@@ -24,6 +25,20 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
             fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
     }
     return fn;
+}
+
+// Lets `kernel` have `bytes` of dynamic shared memory, once per device.
+template <int SLOT>
+inline bool allow_smem(const void *kernel, int bytes) {
+    static std::mutex mutex;
+    static uint64_t done[4] = {0, 0, 0, 0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 256) return false;
+    std::lock_guard<std::mutex> lock(mutex);
+    if (done[dev / 64] >> (dev % 64) & 1) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    done[dev / 64] |= 1ull << (dev % 64);
+    return true;
 }
 
 // A pool as rows of 64 dims, in boxes of a page's 64 slots: bf16 with the

@@ -13,9 +13,12 @@ import torch
 
 import speculative_decoding_drafter_k3_gb300 as k3da
 from cache_cases import Batch, D
-from test_chunk_attn import call, check, dev
+from test_chunk_attn import BATCHES, HEADS, MASKS, call, check, dev
 
 pytestmark = pytest.mark.gpu
+
+
+WIDE = 1300  # pages a request: a table for which a call is not small, whatever the lengths
 
 
 def random_batch(seed, cache, hq=6, hkv=1):
@@ -24,7 +27,19 @@ def random_batch(seed, cache, hq=6, hkv=1):
     sizes = [0, 1, 1, 1, 2, 3, 16 * hkv // hq, 16 * hkv // hq + 1, 21, 22, 40, 43, 85, 130]
     new = [int(g.choice(sizes)) for _ in range(R)]
     ctx = [int(g.integers(0, 40 + 400 * (seed % 4))) for _ in range(R)]
-    return Batch(new, ctx, hq, hkv, cache, pad=3, seed=seed)
+    return Batch(new, ctx, hq, hkv, cache, pad=3, seed=seed, stride=WIDE if seed % 2 else None)
+
+
+@pytest.mark.parametrize("mask", MASKS)
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hq,hkv", HEADS)
+@pytest.mark.parametrize("new,ctx,pad", BATCHES + [([2] * 8 + [3], [70 * r for r in range(9)], 1)])
+def test_small_lengths_in_wide_tables(new, ctx, pad, hq, hkv, cache, mask):
+    b = Batch(new, ctx, hq, hkv, cache, pad, seed=sum(new) + hq, stride=WIDE)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = call(b, mask, status=status)
+    assert int(status) == 0
+    check(b, out, lse, mask)
 
 
 @pytest.mark.parametrize("cache", ["bf16", "e4m3"])
@@ -68,7 +83,7 @@ def test_items_whose_slots_end_apart():
 def test_rows_of_very_different_scales(new, hq, spread):
     """V's exponents close together, at the border, far apart, and with them
     rows of zeros (the smallest scale there is); K's a little apart."""
-    b = Batch(new, [900, 70][:len(new)], hq, 1, "e4m3", seed=20 + spread)
+    b = Batch(new, [900, 70][:len(new)], hq, 1, "e4m3", seed=20 + spread, stride=WIDE)
     g = torch.Generator().manual_seed(spread)
     byte = b.scales.view(torch.uint8)
     low = torch.randint(0, spread + 1, byte.shape, generator=g, dtype=torch.uint8)
@@ -87,7 +102,7 @@ def test_rows_of_very_different_scales(new, hq, spread):
 @pytest.mark.parametrize("what", ["k", "v"])
 @pytest.mark.parametrize("new,hq,ctx", [([2], 6, [125]), ([3], 5, [126]), ([2], 8, [63]), ([16], 1, [120])])
 def test_a_nan_in_a_small_chunk_reaches_only_rows_that_see_it(new, hq, ctx, what, cache):
-    b = Batch(new, ctx, hq, 1, cache, seed=12)
+    b = Batch(new, ctx, hq, 1, cache, seed=12, stride=WIDE)
     at = ctx[0] + new[0] // 2
     page, slot = int(b.table[0, at // 64]), at % 64
     kv = "kv".index(what)
@@ -116,7 +131,7 @@ def test_an_infinite_value_in_a_small_chunk(value, at):
 
 @pytest.mark.parametrize("cache", ["bf16", "e4m3"])
 def test_bad_pages_of_a_small_chunk_are_zeros(cache):
-    b = Batch([1, 2], [300, 62], 6, 1, cache, seed=14)
+    b = Batch([1, 2], [300, 62], 6, 1, cache, seed=14, stride=WIDE)
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     d = list(dev(b))
     d[3] = d[3].clone()
@@ -157,7 +172,7 @@ def test_many_long_contexts_over_the_same_pages(cache):
 
 def test_two_captured_graphs_share_a_workspace():
     """Replayed one after the other on a stream, in either order."""
-    bs = [Batch([1] * 9, [700 * r for r in range(9)], 6, 1, "bf16", seed=23), Batch([60, 1, 130], [1000, 9000, 40], 6, 1, "bf16", seed=24)]
+    bs = [Batch([1] * 9, [700 * r for r in range(9)], 6, 1, "bf16", seed=23, stride=WIDE), Batch([60, 1, 130], [1000, 9000, 40], 6, 1, "bf16", seed=24)]
     ds = [dev(b) for b in bs]
     want = [call(b, d=d) for b, d in zip(bs, ds)]
     ws = k3da.alloc_chunk_workspace(max(b.T for b in bs), 9, 6, 1, max(b.stride for b in bs))
