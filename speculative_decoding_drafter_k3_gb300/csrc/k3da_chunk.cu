@@ -132,9 +132,15 @@ __device__ __forceinline__ void pin8(uint32_t *r) {
     asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]));
 }
 
-// Two e4m3 codes (the top bytes of the halves of h) as bf16 times 2^-120:
-// the sign, and the other seven bits moved to where bf16's exponent ends.
-__device__ __forceinline__ uint32_t widen2(uint32_t h) { return (h & 0x80008000u) | ((h >> 4) & 0x07f007f0u); }
+// Two e4m3 codes as bf16 times 2^-120: the sign, and the other seven bits
+// where bf16's exponent ends.  BYTES (of prmt) extends two of the four bytes
+// to halfwords, with their signs.
+template <int BYTES>
+__device__ __forceinline__ uint32_t widen2(uint32_t codes) {
+    uint32_t h;
+    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(h) : "r"(codes), "n"(BYTES));
+    return (h * 16u) & 0x87f087f0u;
+}
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     uint32_t d;
@@ -797,8 +803,8 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
                             uint32_t o[8];
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {
-                                o[2 * q] = mul_bf16x2(widen2(__byte_perm(in[q], 0, 0x1404)), mul);
-                                o[2 * q + 1] = mul_bf16x2(widen2(__byte_perm(in[q], 0, 0x3424)), mul);
+                                o[2 * q] = mul_bf16x2(widen2<0x9180>(in[q]), mul);
+                                o[2 * q + 1] = mul_bf16x2(widen2<0xb3a2>(in[q]), mul);
                             }
                             const int key = t * kTile + row;
                             if (b > 134u || (is_v && key >= limit)) {
