@@ -575,24 +575,26 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
         uint64_t policy;  // pages are read again by the items of other token pairs
         asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
         int x = 0;
+        const bool issuer = elect_one();
         for (int n = 0; alive; ++n) {
             const Piece &it = pieces[n % kRing];
             if (!mbar_wait(bar_piece + 8 * (n % kRing), (n / kRing) & 1, abort_flag, p.status)) break;
             if (it.row < 0) break;
-            const int pages = (it.limit + kP - 1) / kP;
-            int mine = -2;
-            for (int t = it.t0; t < it.t1; ++t, ++x) {
-                const int ahead = (t - it.t0) & 15;
-                if (ahead == 0) {
-                    // The next 32 pages, one a lane: row of its K, -1 where
-                    // the id is no page, -2 past the item's last key.
-                    const int pg = 2 * t + lane;
-                    mine = -2;
-                    if (pg < pages && pg < 2 * it.t1) {
-                        const long long page = page_of(p.page_table, p.page_stride, p.num_pages, it.r, pg * kP);
-                        mine = page < 0 ? -1 : static_cast<int>((page * 2 * p.Hkv + it.h) * kP);
-                    }
-                }
+            const int t0 = it.t0, t1 = it.t1, pages = min((it.limit + kP - 1) / kP, 2 * t1), r = it.r, h = it.h;
+            // 32 pages at a time, one a lane: row of its K, -1 where the id
+            // is no page, -2 past the item's last key.  The next ones are
+            // asked for half way.
+            auto rows_at = [&](int t) {
+                const int pg = 2 * t + lane;
+                if (pg >= pages) return -2;
+                const long long page = page_of(p.page_table, p.page_stride, p.num_pages, r, pg * kP);
+                return page < 0 ? -1 : static_cast<int>((page * 2 * p.Hkv + h) * kP);
+            };
+            int mine = -2, next = t0 < t1 ? rows_at(t0) : -2;
+            for (int t = t0; t < t1; ++t, ++x) {
+                const int ahead = (t - t0) & 15;
+                if (ahead == 0) mine = next;
+                if (ahead == 8) next = rows_at(t + 8);
                 const int st = x % S;
                 if (!mbar_wait(empty + 8 * st, ((x / S) & 1) ^ 1, abort_flag, p.status)) {
                     alive = false;
@@ -618,7 +620,7 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
                     }
                 }
                 __syncwarp();
-                if (lane == 0) {
+                if (issuer) {
                     const uint32_t bar = full + 8 * st;
                     if (bytes > 0) mbar_arrive_expect_tx(bar, bytes);
                     else mbar_arrive(bar);

@@ -235,7 +235,7 @@ struct Loader {
                 fence_proxy_async();  // the place's next load comes after
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar);
-            } else if (lane == 0) {
+            } else if (elect_one()) {
                 const int src = row + is_v * p.Hkv * kP;
                 mbar_arrive_expect_tx(bar, L::kTileBytes + (QUANT ? kP : 0));
                 tma_load_2d(smem_u32(dst), &map, 0, src, bar, policy);
