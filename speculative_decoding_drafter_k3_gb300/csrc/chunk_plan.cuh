@@ -109,8 +109,9 @@ struct Request {
 };
 
 // All threads; syncs.  The first THREADS take two requests each at a time.
+// False, and no plan, where the pass has no items.
 template <int THREADS>
-__device__ __forceinline__ void build_plan(const ChunkParams &p, Plan *pl, bool report) {
+__device__ __forceinline__ bool build_plan(const ChunkParams &p, Plan *pl, bool report) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     if (t == 0) pl->prefix[0] = 0;
     long long done = 0;
@@ -132,7 +133,7 @@ __device__ __forceinline__ void build_plan(const ChunkParams &p, Plan *pl, bool 
             if (lane >= off) sum += up;
         }
         if (mine && lane == 31) pl->warp_sum[warp] = sum;
-        __syncthreads();
+        if (!__syncthreads_or(mine && sum > 0) && p.R <= 2 * THREADS) return false;
         if (mine) {
             long long before = done;
             for (int w = 0; w < warp; ++w) before += pl->warp_sum[w];
@@ -143,6 +144,7 @@ __device__ __forceinline__ void build_plan(const ChunkParams &p, Plan *pl, bool 
         __syncthreads();
         done = pl->prefix[min(r0 + 2 * THREADS, p.R)];
     }
+    return done > 0;
 }
 
 // A piece: the tiles [t0, t1) of one item that fall into this CTA's slice.

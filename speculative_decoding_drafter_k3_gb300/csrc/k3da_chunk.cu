@@ -96,22 +96,25 @@ constexpr uint32_t kIdescPV = idesc_f16(128, kD, true);
 
 template <bool QUANT>
 struct Smem {
-    static constexpr int kStages = QUANT ? 3 : 5;  // bf16 K/V tiles
+    // bf16 tiles of K and of V.  V's are held until the weights of their keys
+    // are formed, K's not, so that more of V leaves as many of both on their
+    // way.  (Widened tiles are made together: the same of both.)
+    static constexpr int kKs = QUANT ? 3 : 4, kVs = QUANT ? 3 : 6;
     static constexpr int kRaw = QUANT ? 4 : 0;     // quantised tiles: K codes, V codes, K scales, V scales
     static constexpr int kRawBytes = 2 * kTile * kD + 2 * kTile;
-    static constexpr int kStageBytes = 2 * kTile * kD * 2;
-    static constexpr int kVOff = kTile * kD * 2;
+    static constexpr int kTileBytes = kTile * kD * 2;
     // Two halves: a shared item's slots, or two alternate items' Q in turn.
     static constexpr int kQBytes = kSlotRows * kD * 2;
     static constexpr int kQ = 0;
     static constexpr int kKv = kQ + 2 * kQBytes;
-    static constexpr int kRawOff = kKv + kStages * kStageBytes;
+    static constexpr int kV = kKv + kKs * kTileBytes;
+    static constexpr int kRawOff = kV + kVs * kTileBytes;
     static constexpr int kPlan = kRawOff + kRaw * kRawBytes;
     static constexpr int kRec = kPlan + static_cast<int>(sizeof(Plan));
     static constexpr int kXch = kRec + kRecords * static_cast<int>(sizeof(Records));
     static constexpr int kPieces = kXch + (5 * kGroups + 1) * kSlotRows * 4;
     static constexpr int kBars = kPieces + kRing * static_cast<int>(sizeof(Piece));
-    static constexpr int kNumBars = 3 * kStages + 2 * kRaw + 2 * kRing + 4 + 7 * kBufs + 2 * 2 + 2;
+    static constexpr int kNumBars = 2 * kKs + 3 * kVs + 2 * kRaw + 2 * kRing + 4 + 7 * kBufs + 2 * 2 + 2;
     static constexpr int kTail = kBars + kNumBars * 8;  // TMEM address, abort flag
     static constexpr int kBytes = kTail + 16 + 1024;
     static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
@@ -167,10 +170,12 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kTail + 8);
     uint32_t *taddr_slot = reinterpret_cast<uint32_t *>(smem + L::kTail);
     const uint32_t bars = smem_u32(smem + L::kBars);
-    const uint32_t bar_full = bars;                         // [kStages] bf16 tile loaded (QUANT: unused)
-    const uint32_t bar_prep = bar_full + 8 * L::kStages;    // [kStages] tile prepared
-    const uint32_t bar_empty = bar_prep + 8 * L::kStages;   // [kStages] the streams are done with the tile
-    const uint32_t bar_rfull = bar_empty + 8 * L::kStages;  // [kRaw] quantised tile loaded
+    const uint32_t bar_kfull = bars;                       // [kKs] K loaded (QUANT: unused, as the next two)
+    const uint32_t bar_kempty = bar_kfull + 8 * L::kKs;    // [kKs] ... and multiplied
+    const uint32_t bar_vfull = bar_kempty + 8 * L::kKs;    // [kVs] V loaded
+    const uint32_t bar_prep = bar_vfull + 8 * L::kVs;      // [kVs] ... and prepared (QUANT: K too)
+    const uint32_t bar_empty = bar_prep + 8 * L::kVs;      // [kVs] ... and multiplied by both slots that take it
+    const uint32_t bar_rfull = bar_empty + 8 * L::kVs;     // [kRaw] quantised tile loaded
     const uint32_t bar_rempty = bar_rfull + 8 * L::kRaw;    // [kRaw] ... and widened
     const uint32_t bar_piece = bar_rempty + 8 * L::kRaw;    // [kRing] piece published
     const uint32_t bar_pdone = bar_piece + 8 * kRing;       // [kRing] ... and read by everybody
@@ -189,15 +194,18 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
     const uint32_t bar_done = bar_xch + 8;                  // every issuer's products are complete
     const int warp = __shfl_sync(kFull, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
 
-    build_plan<512>(p, pl, blockIdx.x == 0);
-    if (pl->prefix[p.R] == 0) {  // every chunk is small
+    if (!build_plan<512>(p, pl, blockIdx.x == 0)) {  // every chunk is small
         if (threadIdx.x == 0) p.cuts[blockIdx.x] = Cut{};
         return;
     }
     if (threadIdx.x == 0) {
         *abort_flag = 0;
-        for (int s = 0; s < L::kStages; ++s) {
-            mbar_init(bar_full + 8 * s, 1);
+        for (int s = 0; s < L::kKs; ++s) {
+            mbar_init(bar_kfull + 8 * s, 1);
+            mbar_init(bar_kempty + 8 * s, 1);
+        }
+        for (int s = 0; s < L::kVs; ++s) {
+            mbar_init(bar_vfull + 8 * s, 1);
             mbar_init(bar_prep + 8 * s, kPrepWarps);
             mbar_init(bar_empty + 8 * s, 2);
         }
@@ -569,12 +577,10 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
         }
     } else if (warp == kLoadWarp) {
         // ------------------------------------------------------ K/V loads --
-        constexpr int S = QUANT ? L::kRaw : L::kStages;
-        const uint32_t full = QUANT ? bar_rfull : bar_full, empty = QUANT ? bar_rempty : bar_empty;
         constexpr int kPageTile = kP * kD * (QUANT ? 1 : 2);  // bytes of a page's K or V of one head
         uint64_t policy;  // pages are read again by the items of other token pairs
         asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
-        int x = 0;
+        int issued[2] = {0, 0};  // tiles of K (codes: of both), of V
         const bool issuer = elect_one();
         for (int n = 0; alive; ++n) {
             const Piece &it = pieces[n % kRing];
@@ -591,62 +597,75 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
                 return page < 0 ? -1 : static_cast<int>((page * 2 * p.Hkv + h) * kP);
             };
             int mine = -2, next = t0 < t1 ? rows_at(t0) : -2;
-            for (int t = t0; t < t1; ++t, ++x) {
+            for (int t = t0; t < t1; ++t) {
                 const int ahead = (t - t0) & 15;
                 if (ahead == 0) mine = next;
                 if (ahead == 8) next = rows_at(t + 8);
-                const int st = x % S;
-                if (!mbar_wait(empty + 8 * st, ((x / S) & 1) ^ 1, abort_flag, p.status)) {
-                    alive = false;
-                    break;
-                }
-                uint8_t *dst = smem + (QUANT ? L::kRawOff + st * L::kRawBytes : L::kKv + st * L::kStageBytes);
-                uint32_t bytes = 0;
-                int krow[2];
+                // K, then V (codes: both, with their scales, in one place).
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    krow[half] = __shfl_sync(kFull, mine, 2 * ahead + half);
-                    if (krow[half] >= 0) bytes += 2 * kPageTile + (QUANT ? 2 * kP : 0);
-                    if (krow[half] == -1) {
-                        if (lane == 0 && p.status) atomicOr(p.status, K3DA_STATUS_BAD_PAGE);
-                        for (int e = lane; e < kPageTile / 16; e += 32) {
-                            reinterpret_cast<uint4 *>(dst + half * kPageTile)[e] = make_uint4(0, 0, 0, 0);
-                            reinterpret_cast<uint4 *>(dst + (2 + half) * kPageTile)[e] = make_uint4(0, 0, 0, 0);
-                        }
-                        if (QUANT)
-                            for (int e = lane; e < kP; e += 32)
-                                dst[4 * kPageTile + half * kP + e] = dst[4 * kPageTile + (2 + half) * kP + e] = 0;
-                        fence_proxy_async();
+                for (int part = 0; part < (QUANT ? 1 : 2); ++part) {
+                    const int ring = QUANT ? L::kRaw : part ? L::kVs : L::kKs, x = issued[part], st = x % ring;
+                    const uint32_t full = (QUANT ? bar_rfull : part ? bar_vfull : bar_kfull) + 8 * st;
+                    if (!mbar_wait((QUANT ? bar_rempty : part ? bar_empty : bar_kempty) + 8 * st, ((x / ring) & 1) ^ 1,
+                                   abort_flag, p.status)) {
+                        alive = false;
+                        break;
                     }
-                }
-                __syncwarp();
-                if (issuer) {
-                    const uint32_t bar = full + 8 * st;
-                    if (bytes > 0) mbar_arrive_expect_tx(bar, bytes);
-                    else mbar_arrive(bar);
+                    uint8_t *dst = smem + (QUANT ? L::kRawOff + st * L::kRawBytes
+                                                 : (part ? L::kV : L::kKv) + st * L::kTileBytes);
+                    uint32_t bytes = 0;
+                    int krow[2];
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        if (krow[half] < 0) continue;
-                        const int vrow = krow[half] + p.Hkv * kP;
-                        tma_load_2d(smem_u32(dst + half * kPageTile), &kv_map, 0, krow[half], bar, policy);
-                        tma_load_2d(smem_u32(dst + (2 + half) * kPageTile), &kv_map, 0, vrow, bar, policy);
-                        if (QUANT) {
-                            bulk_load(smem_u32(dst + 4 * kPageTile + half * kP), p.scales + krow[half], kP, bar);
-                            bulk_load(smem_u32(dst + 4 * kPageTile + (2 + half) * kP), p.scales + vrow, kP, bar);
+                        krow[half] = __shfl_sync(kFull, mine, 2 * ahead + half);
+                        if (krow[half] >= 0) bytes += QUANT ? 2 * kPageTile + 2 * kP : kPageTile;
+                        if (krow[half] == -1) {
+                            if (lane == 0 && p.status) atomicOr(p.status, K3DA_STATUS_BAD_PAGE);
+                            for (int e = lane; e < kPageTile / 16; e += 32) {
+                                reinterpret_cast<uint4 *>(dst + half * kPageTile)[e] = make_uint4(0, 0, 0, 0);
+                                if (QUANT) reinterpret_cast<uint4 *>(dst + (2 + half) * kPageTile)[e] = make_uint4(0, 0, 0, 0);
+                            }
+                            if (QUANT)
+                                for (int e = lane; e < kP; e += 32)
+                                    dst[4 * kPageTile + half * kP + e] = dst[4 * kPageTile + (2 + half) * kP + e] = 0;
+                            fence_proxy_async();
                         }
                     }
+                    __syncwarp();
+                    if (issuer) {
+                        if (bytes > 0) mbar_arrive_expect_tx(full, bytes);
+                        else mbar_arrive(full);
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            if (krow[half] < 0) continue;
+                            const int vrow = krow[half] + p.Hkv * kP;
+                            tma_load_2d(smem_u32(dst + half * kPageTile), &kv_map, 0, part ? vrow : krow[half], full, policy);
+                            if (QUANT) {
+                                tma_load_2d(smem_u32(dst + (2 + half) * kPageTile), &kv_map, 0, vrow, full, policy);
+                                bulk_load(smem_u32(dst + 4 * kPageTile + half * kP), p.scales + krow[half], kP, full);
+                                bulk_load(smem_u32(dst + 4 * kPageTile + (2 + half) * kP), p.scales + vrow, kP, full);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    ++issued[part];
                 }
-                __syncwarp();
+                if (!alive) break;
             }
+            if (!alive) break;
             if (lane == 0) mbar_arrive(bar_pdone + 8 * (n % kRing));
         }
         // Loads in flight land before the CTA leaves (a wait gave up).
         if (*abort_flag) {
-            for (int j = x > S ? x - S : 0; j < x; ++j) {
-                const unsigned long long t0 = global_ns();
-                while (!mbar_try_wait(full + 8 * (j % S), (j / S) & 1) && global_ns() - t0 < kWaitLimitNs) {
+            auto land = [&](uint32_t full, int ring, int x) {
+                for (int j = x > ring ? x - ring : 0; j < x; ++j) {
+                    const unsigned long long t0 = global_ns();
+                    while (!mbar_try_wait(full + 8 * (j % ring), (j / ring) & 1) && global_ns() - t0 < kWaitLimitNs) {
+                    }
                 }
-            }
+            };
+            land(QUANT ? bar_rfull : bar_kfull, QUANT ? L::kRaw : L::kKs, issued[0]);
+            if (!QUANT) land(bar_vfull, L::kVs, issued[1]);
         }
     } else if (warp < kPrepWarp) {
         // ------------------------------------------------------ products --
@@ -654,11 +673,12 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
         const bool is_qk = warp == kQkWarp;
         const int s = is_qk ? 0 : warp - kPvWarp;
         const bool issuer = elect_one();
+        const int stages = is_qk ? L::kKs : L::kVs;
         int st = 0;       // the tile's stage
         uint32_t ph = 0;  // ... and how often the stages have come round, mod 2
         int items = 0;    // pieces with tiles for the slot so far
         uint32_t k[2] = {0, 0};  // tiles of each slot so far
-        const uint32_t kv = smem_u32(smem + L::kKv);
+        const uint32_t tiles = smem_u32(smem + (is_qk ? L::kKv : L::kV));
         for (int n = 0; alive; ++n) {
             const Piece &it = pieces[n % kRing];
             if (!mbar_wait(bar_piece + 8 * (n % kRing), (n / kRing) & 1, abort_flag, p.status)) break;
@@ -677,12 +697,12 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
             for (int t = t0; t < t1; ++t) {
                 // Every tile in turn, another slot's too: a phase is never
                 // waited for before the one before it is known to be over.
-                if (!mbar_wait((QUANT ? bar_prep : bar_full) + 8 * st, ph, abort_flag, p.status)) {
+                if (!mbar_wait((QUANT || !is_qk ? bar_prep : bar_kfull) + 8 * st, ph, abort_flag, p.status)) {
                     alive = false;
                     break;
                 }
                 if (is_qk) {
-                    const uint64_t kd = desc_sw128(kv + st * L::kStageBytes);
+                    const uint64_t kd = desc_sw128(tiles + st * L::kTileBytes);
                     // An alternate item's slots have the same Q.
                     for (int slot = alt || t >= t_end ? 1 : 0; slot < 2; ++slot, ++i) {
                         const uint32_t round = i / kBufs, buf = i - round * kBufs;
@@ -700,6 +720,7 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
                             const int of = alt ? (t - t0) & 1 : slot;
                             const uint32_t turn = of * kBufs + (of ? k[1] : k[0]) % kBufs;
                             mma_commit(bar_sfull + 8 * turn);
+                            if (!QUANT && slot == 1) mma_commit(bar_kempty + 8 * st);
                         }
                         if (alt ? (t - t0) & 1 : slot) ++k[1];
                         else ++k[0];
@@ -711,14 +732,13 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
                     const uint32_t round = k[0] / kBufs, turn = s * kBufs + k[0] - round * kBufs;
                     ++k[0];
                     if (!mbar_wait(bar_pfull + 8 * turn, round & 1, abort_flag, p.status) ||
-                        (!QUANT && !mbar_wait(bar_prep + 8 * st, ph, abort_flag, p.status)) ||
                         (t == from && items > 1 && !mbar_wait(bar_ofree + 8 * s, items & 1, abort_flag, p.status))) {
                         alive = false;
                         break;
                     }
                     fence_after();
                     if (issuer) {
-                        const uint64_t vd = desc_sw128(kv + st * L::kStageBytes + L::kVOff);
+                        const uint64_t vd = desc_sw128(tiles + st * L::kTileBytes);
 #pragma unroll
                         for (int kk = 0; kk < kTile / 16; ++kk)
                             mma_ts(tmem + col_o(s), tmem + col_s(buf) + 8 * kk + (kk >= 4 ? 32 : 0), vd + ((kk * 2048) >> 4),
@@ -730,7 +750,7 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
                 } else if (lane == 0) {
                     mbar_arrive(bar_empty + 8 * st);
                 }
-                if (++st == L::kStages) {
+                if (++st == stages) {
                     st = 0;
                     ph ^= 1;
                 }
@@ -768,8 +788,7 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
             const uint32_t tag = ~static_cast<uint32_t>(piece) << 8;
             const int least = keys_seen(p, it.ctx, it.n, it.tok0);  // keys that every row of the item sees
             for (int t = it.t0; t < t1; ++t) {
-                uint8_t *kt = smem + L::kKv + st * L::kStageBytes;
-                uint8_t *vt = kt + L::kVOff;
+                uint8_t *vt = smem + L::kV + st * L::kTileBytes;
                 if (QUANT) {
                     const uint8_t *raw = smem + L::kRawOff + rs * L::kRawBytes;
                     if (!mbar_wait(bar_rfull + 8 * rs, rph, abort_flag, p.status) ||
@@ -821,14 +840,14 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
                                     rec->piece = piece;
                                 }
                             }
-                            uint8_t *dst = kt + (is_v ? L::kVOff : 0);
+                            uint8_t *dst = is_v ? vt : smem + L::kKv + st * L::kTileBytes;
                             *reinterpret_cast<uint4 *>(dst + swz(row, 2 * quarter)) = make_uint4(o[0], o[1], o[2], o[3]);
                             *reinterpret_cast<uint4 *>(dst + swz(row, 2 * quarter + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
                         }
                     }
                     fence_proxy_async();
                 } else {
-                    if (!mbar_wait(bar_full + 8 * st, ph, abort_flag, p.status)) {
+                    if (!mbar_wait(bar_vfull + 8 * st, ph, abort_flag, p.status)) {
                         alive = false;
                         break;
                     }
@@ -870,7 +889,7 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
                     mbar_arrive(bar_prep + 8 * st);
                     if (QUANT) mbar_arrive(bar_rempty + 8 * rs);
                 }
-                if (++st == L::kStages) {
+                if (++st == L::kVs) {
                     st = 0;
                     ph ^= 1;
                 }

@@ -654,8 +654,7 @@ __global__ void __launch_bounds__(Smem<QUANT>::kThreads, 1)
     const int warp = __shfl_sync(kFull, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    build_plan<256>(p, pl, blockIdx.x == 0);
-    if (pl->prefix[p.R] == 0) {
+    if (!build_plan<256>(p, pl, blockIdx.x == 0)) {
         if (threadIdx.x == 0) p.cuts[blockIdx.x] = Cut{};
         asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
