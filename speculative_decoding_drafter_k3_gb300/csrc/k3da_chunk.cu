@@ -578,8 +578,9 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
     } else if (warp == kLoadWarp) {
         // ------------------------------------------------------ K/V loads --
         constexpr int kPageTile = kP * kD * (QUANT ? 1 : 2);  // bytes of a page's K or V of one head
-        uint64_t policy;  // pages are read again by the items of other token pairs
-        asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
+        uint64_t again, once;  // pages are read again where the request has more items
+        asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(again));
+        asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
         int issued[2] = {0, 0};  // tiles of K (codes: of both), of V
         const bool issuer = elect_one();
         for (int n = 0; alive; ++n) {
@@ -597,6 +598,7 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
                 return page < 0 ? -1 : static_cast<int>((page * 2 * p.Hkv + h) * kP);
             };
             int mine = -2, next = t0 < t1 ? rows_at(t0) : -2;
+            const uint64_t policy = it.n <= 2 * p.tpt ? once : again;
             for (int t = t0; t < t1; ++t) {
                 const int ahead = (t - t0) & 15;
                 if (ahead == 0) mine = next;
