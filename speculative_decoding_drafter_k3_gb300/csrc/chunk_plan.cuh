@@ -301,8 +301,8 @@ __device__ __forceinline__ uint32_t swz(int row, int chunk) {
     return static_cast<uint32_t>(row * 128 + ((chunk ^ (row & 7)) << 4));
 }
 
-// The small kernel (k3da_chunk_small.cu).  after_long: it follows the long
+// The small kernel (k3da_chunk_small.cu).  second: it follows the long
 // chunks' kernel on the stream and may start beside it.
-int launch_small(const ChunkParams &p, const void *kv_pool, bool quant, bool after_long, cudaStream_t stream);
+int launch_small(const ChunkParams &p, const void *kv_pool, bool quant, bool second, cudaStream_t stream);
 
 }  // namespace k3da_chunk

@@ -196,6 +196,7 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
 
     if (!build_plan<512>(p, pl, blockIdx.x == 0)) {  // every chunk is small
         if (threadIdx.x == 0) p.cuts[blockIdx.x] = Cut{};
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
     if (threadIdx.x == 0) {
@@ -910,6 +911,8 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
     fence_after();
     if (warp == kLoadWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    // The kernel this one may have started beside is complete before it is.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ----------------------------------------------------------------- combine --
@@ -1024,14 +1027,15 @@ __global__ void __launch_bounds__(kCombineThreads)
 // -------------------------------------------------------------------- host --
 
 template <bool QUANT>
-int launch_kernel(const CUtensorMap &kv_map, const CUtensorMap &q_map, const ChunkParams &prm, cudaStream_t st) {
+int launch_kernel(const CUtensorMap &kv_map, const CUtensorMap &q_map, const ChunkParams &prm, bool second,
+                  cudaStream_t st) {
     if (!allow_smem<QUANT>(reinterpret_cast<const void *>(k3da_chunk_kernel<QUANT>), Smem<QUANT>::kBytes))
         return K3DA_ECUDA;
-    k3da_chunk_kernel<QUANT><<<kCtas, threads_of(QUANT), Smem<QUANT>::kBytes, st>>>(kv_map, q_map, prm);
-    return cudaGetLastError() == cudaSuccess ? K3DA_OK : K3DA_ECUDA;
+    return launch_beside(k3da_chunk_kernel<QUANT>, dim3(kCtas), threads_of(QUANT), Smem<QUANT>::kBytes, second, st, kv_map,
+                         q_map, prm);
 }
 
-int launch_long(const ChunkParams &prm, const void *q, const void *kv_pool, bool quant, cudaStream_t st) {
+int launch_long(const ChunkParams &prm, const void *q, const void *kv_pool, bool quant, bool second, cudaStream_t st) {
     const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     CUtensorMap kv_map, q_map;
     if (encode == nullptr || !pool_map(encode, &kv_map, kv_pool, prm.num_pages, prm.Hkv, quant, !quant)) return K3DA_ECUDA;
@@ -1043,7 +1047,8 @@ int launch_long(const ChunkParams &prm, const void *q, const void *kv_pool, bool
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return K3DA_ECUDA;
-    return quant ? launch_kernel<true>(kv_map, q_map, prm, st) : launch_kernel<false>(kv_map, q_map, prm, st);
+    return quant ? launch_kernel<true>(kv_map, q_map, prm, second, st)
+                 : launch_kernel<false>(kv_map, q_map, prm, second, st);
 }
 
 }  // namespace
@@ -1125,12 +1130,15 @@ extern "C" int k3da_chunk_attn(void *out, float *lse, const void *q, int64_t q_r
     ChunkParams small = prm;
     small.pass = kSmall;
     parts_at(small, ws + part_bytes(2 * kSlotRows), kSmallRows);
-    if (can_be_long) {
-        const int launched = launch_long(prm, q, kv_pool, quant, st);
-        if (launched != K3DA_OK) return launched;
-    }
-    if (!one_kernel) {
-        const int launched = launch_small(small, kv_pool, quant, can_be_long, st);
+    // The pass that is more likely to have the work goes first: an empty one
+    // behind it starts where SMs fall free.
+    const bool small_first = num_tokens <= static_cast<long long>(num_requests) * (kSmallRows / prm.G);
+    for (int i = 0; i < 2; ++i) {
+        const bool is_small = (i == 0) == small_first;
+        if (is_small ? one_kernel : !can_be_long) continue;
+        const bool second = i == 1 && can_be_long && !one_kernel;
+        const int launched =
+            is_small ? launch_small(small, kv_pool, quant, second, st) : launch_long(prm, q, kv_pool, quant, second, st);
         if (launched != K3DA_OK) return launched;
     }
     // Where all there can be fits one slice, nothing is cut (a token over 300:
@@ -1144,15 +1152,7 @@ extern "C" int k3da_chunk_attn(void *out, float *lse, const void *q, int64_t q_r
     const long long bound = num_tokens <= prm.tpt ? num_tokens * prm.G : 2 * kSlotRows;
     int rows = static_cast<int>((bound * gx + 1215) / 1216);
     rows = rows < 2 ? 2 : rows;
-    cudaLaunchConfig_t lc;
-    std::memset(&lc, 0, sizeof lc);
-    lc.gridDim = dim3(gx, static_cast<unsigned>((bound + rows - 1) / rows), can_be_long && !one_kernel ? 2 : 1);
-    lc.blockDim = dim3(kCombineThreads);
-    lc.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    lc.attrs = attr;
-    lc.numAttrs = 1;
-    return cudaLaunchKernelEx(&lc, k3da_chunk_combine_kernel, one_kernel ? prm : small, prm, rows) == cudaSuccess ? K3DA_OK : K3DA_ECUDA;
+    return launch_beside(k3da_chunk_combine_kernel,
+                         dim3(gx, static_cast<unsigned>((bound + rows - 1) / rows), can_be_long && !one_kernel ? 2 : 1),
+                         kCombineThreads, 0, true, st, one_kernel ? prm : small, prm, rows);
 }

@@ -819,30 +819,20 @@ __global__ void __launch_bounds__(Smem<QUANT>::kThreads, 1)
 }
 
 template <bool QUANT>
-int launch(const CUtensorMap &kv_map, const ChunkParams &p, bool after_long, cudaStream_t stream) {
+int launch(const CUtensorMap &kv_map, const ChunkParams &p, bool second, cudaStream_t stream) {
     if (!allow_smem<2 + QUANT>(reinterpret_cast<const void *>(k3da_chunk_small_kernel<QUANT>), Smem<QUANT>::kBytes))
         return K3DA_ECUDA;
-    cudaLaunchConfig_t lc;
-    std::memset(&lc, 0, sizeof lc);
-    lc.gridDim = dim3(kCtas);
-    lc.blockDim = dim3(Smem<QUANT>::kThreads);
-    lc.dynamicSmemBytes = Smem<QUANT>::kBytes;
-    lc.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    lc.attrs = attr;
-    lc.numAttrs = after_long ? 1 : 0;
-    return cudaLaunchKernelEx(&lc, k3da_chunk_small_kernel<QUANT>, kv_map, p) == cudaSuccess ? K3DA_OK : K3DA_ECUDA;
+    return launch_beside(k3da_chunk_small_kernel<QUANT>, dim3(kCtas), Smem<QUANT>::kThreads, Smem<QUANT>::kBytes, second,
+                         stream, kv_map, p);
 }
 
 }  // namespace
 
-int launch_small(const ChunkParams &p, const void *kv_pool, bool quant, bool after_long, cudaStream_t stream) {
+int launch_small(const ChunkParams &p, const void *kv_pool, bool quant, bool second, cudaStream_t stream) {
     const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     CUtensorMap kv_map;
     if (encode == nullptr || !pool_map(encode, &kv_map, kv_pool, p.num_pages, p.Hkv, quant, true)) return K3DA_ECUDA;
-    return quant ? launch<true>(kv_map, p, after_long, stream) : launch<false>(kv_map, p, after_long, stream);
+    return quant ? launch<true>(kv_map, p, second, stream) : launch<false>(kv_map, p, second, stream);
 }
 
 }  // namespace k3da_chunk
