@@ -20,12 +20,12 @@
 // size meet no range.  q is scaled by a power of two into half precision's
 // range (exact but for dims 2^-39 below the row's largest).
 //
-// Measured (64 decoded tokens over 8000 each, 24/4 heads): e4m3 61 us, 4.4
-// TB/s of cache, where the long chunks' kernel takes 144; bf16 92 us, 5.7
-// TB/s, against 100.  bf16 is bound by the memory; codes by issue slots (740
-// instructions a page and warp, a third of them conversions and byte
-// permutations) and by instruction fetch.  12 and 15 warps had only 128
-// registers and spilled: 73 and 86 us.
+// Measured (64 decoded tokens over 8000 each, 24/4 heads): e4m3 57 us, 4.7
+// TB/s of cache, where the long chunks' kernel takes 144; bf16 91 us, 5.7
+// TB/s, against 100.  About 9 us of either are launches, plan, first loads
+// and the fold of cut items; the rest streams at 5.6 to 6.0 TB/s.  15 warps of
+// 128 registers take as long, and 53 instead of 43 us where two tiles of rows
+// spill (8 x 2 tokens over 60000, 16/2 heads, e4m3).
 //
 // Rounding: scores, statistics, O and partial results are fp32; weights are
 // rounded once (bf16, or half precision for codes), the output once.
@@ -331,13 +331,14 @@ struct Turn {
 // rows, so that the 4 to 8 rows of most items fill them: S^T = K q^T and
 // O^T += V^T w^T.  The thread has rows 8 n + 2 t4 and one more of each row
 // tile n, and of a 16-key tile i the keys 16 i + kg and + 8.
+template <int NT>
 struct Rows {
-    uint32_t q[2][8];  // of row 8 n + g: dims 16 t4 .. 16 t4 + 15 (and so of every key: a product's order of dims is free)
-    float scale[2][2];
-    int sees[2][2];
-    float m[2][2], l[2][2];
-    float mo[2][2];   // reference of O: m, or with codes the maximum of s + e
-    float o[2][4][4];
+    uint32_t q[NT][8];  // of row 8 n + g: dims 16 t4 .. 16 t4 + 15 (and so of every key: a product's order of dims is free)
+    float scale[NT][2];
+    int sees[NT][2];
+    float m[NT][2], l[NT][2];
+    float mo[NT][2];   // reference of O: m, or with codes the maximum of s + e
+    float o[NT][4][4];
     // Codes: while V's exponents in the piece are within kNear of one another.
     bool near;
     int e_hi, e_lo;
@@ -345,7 +346,7 @@ struct Rows {
 
 // One page, over NT tiles of 8 rows.
 template <bool QUANT, int NT>
-__device__ __forceinline__ bool take_page(Rows &R, Loader<QUANT> &load, const ChunkParams &p, const CUtensorMap &kv_map,
+__device__ __forceinline__ bool take_page(Rows<NT> &R, Loader<QUANT> &load, const ChunkParams &p, const CUtensorMap &kv_map,
                                           const Piece *pieces, uint32_t bar_piece, int n, Turn<QUANT> &turn, int key0,
                                           int least, int limit, Records *rec, int piece, int lane,
                                           volatile int *abort_flag) {
@@ -634,6 +635,94 @@ __device__ __forceinline__ bool take_page(Rows &R, Loader<QUANT> &load, const Ch
     return true;
 }
 
+// Piece n, over NT tiles of 8 rows, up to the warp's results in the merge
+// room.  False when a wait gave up.
+template <bool QUANT, int NT>
+__device__ __forceinline__ bool take_piece(const ChunkParams &p, const CUtensorMap &kv_map, const Piece *pieces,
+                                           uint32_t bar_piece, int n, Loader<QUANT> &load, Turn<QUANT> &turn,
+                                           Records *recs, float *merge_o, float4 *merge_s, uint32_t bar_merged, int warp,
+                                           int lane, volatile int *abort_flag) {
+    const int g = lane >> 2, t4 = lane & 3;  // a fragment's row or column group, and the thread in it
+    const Piece &it = pieces[n % kRing];
+    const int limit = it.limit, piece = it.seq;
+    const int page0 = 2 * it.t0, pages = pages_of(it);
+    const int least = keys_seen(p, it.ctx, it.n, 0);  // keys that every row sees
+    // The item's rows: token major, the heads of a token together.
+    Rows<NT> R;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int rho = g + 8 * nt, token = rho / p.G;
+        uint4 a = make_uint4(0, 0, 0, 0), b = a;
+        if (token < it.tokens) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                p.q + static_cast<long long>(it.row + token) * p.q_stride + (it.h * p.G + rho - token * p.G) * kD + 16 * t4);
+            a = __ldg(src);
+            b = __ldg(src + 1);
+        }
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        float scale = p.scale_log2;
+        if (QUANT) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = max(top, max((w[e] & 0x7fffu) << 16, w[e] & 0x7fff0000u));
+            top = max(top, __shfl_xor_sync(kFull, top, 1));
+            top = max(top, __shfl_xor_sync(kFull, top, 2));
+            // 2^(14 - e) for a largest magnitude of 2^e; as it is for
+            // a row that is zero or not finite.
+            const uint32_t ex = top >> 23;
+            const uint32_t f = ex == 0 || ex == 255 ? 127u : min(268u - ex, 253u);
+            const float up = __uint_as_float(f << 23);
+            scale *= __uint_as_float((254u - f) << 23);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) R.q[nt][e] = pack_half2(bf16_lo(w[e]) * up, bf16_hi(w[e]) * up);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) R.q[nt][e] = w[e];
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int mine = (8 * nt + 2 * t4 + c) / p.G;
+            R.scale[nt][c] = __shfl_sync(kFull, scale, 4 * (2 * t4 + c));
+            R.sees[nt][c] = mine < it.tokens ? keys_seen(p, it.ctx, it.n, mine) : 0;
+            R.m[nt][c] = R.mo[nt][c] = -INFINITY;
+            R.l[nt][c] = 0.f;
+        }
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) R.o[nt][d][e] = 0.f;
+    }
+    R.near = QUANT;
+    R.e_hi = -1;
+    R.e_lo = 256;
+    for (int j = first_page<QUANT>(warp, it.base); j < pages; j += Smem<QUANT>::kWarps) {
+        if (!take_page<QUANT, NT>(R, load, p, kv_map, pieces, bar_piece, n, turn, (page0 + j) * kP, least, limit,
+                                  recs + piece % kRecords, piece, lane, abort_flag))
+            return false;
+    }
+    // Into the merge room.
+    if (n > 0 && !warp_wait(bar_merged, (n - 1) & 1, abort_flag, p.status)) return false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        float *dst = merge_o + (warp * kSmallRows + 8 * nt + 2 * t4) * kORow;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const float sum = keys_sum(R.l[nt][c]);
+            if (g == 0)
+                merge_s[warp * kSmallRows + 8 * nt + 2 * t4 + c] =
+                    make_float4(R.m[nt][c], sum, QUANT ? R.mo[nt][c] : R.m[nt][c], 0.f);
+        }
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int dim = QUANT ? 32 * (d >> 1) + 4 * g + 2 * (d & 1) + (e >> 1) : 16 * d + g + 8 * (e >> 1);
+                dst[(e & 1) * kORow + dim] = R.o[nt][d][e];
+            }
+    }
+    return true;
+}
+
 template <bool QUANT>
 __global__ void __launch_bounds__(Smem<QUANT>::kThreads, 1)
     k3da_chunk_small_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ ChunkParams p) {
@@ -715,7 +804,6 @@ __global__ void __launch_bounds__(Smem<QUANT>::kThreads, 1)
         }
     } else {
         // ----------------------------------------------------- page warps --
-        const int g = lane >> 2, t4 = lane & 3;  // a fragment's row or column group, and the thread in it
         Loader<QUANT> load;
         load.begin(warp, lane, smem, bars);
         Turn<QUANT> turn;
@@ -723,92 +811,14 @@ __global__ void __launch_bounds__(Smem<QUANT>::kThreads, 1)
             const Piece &it = pieces[n % kRing];
             if (!warp_wait(bar_piece + 8 * (n % kRing), (n / kRing) & 1, abort_flag, p.status)) break;
             if (it.row < 0) break;
-            const int limit = it.limit, piece = it.seq;
-            const int page0 = 2 * it.t0, pages = pages_of(it);
             load.fill(p, kv_map, pieces, bar_piece, n, turn.done);
-            const int least = keys_seen(p, it.ctx, it.n, 0);  // keys that every row sees
-            // The item's rows: token major, the heads of a token together.
-            const bool wide = it.tokens * p.G > 8;
-            Rows R;
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-                const int rho = g + 8 * nt, token = rho / p.G;
-                uint4 a = make_uint4(0, 0, 0, 0), b = a;
-                if (token < it.tokens) {
-                    const uint4 *src = reinterpret_cast<const uint4 *>(
-                        p.q + static_cast<long long>(it.row + token) * p.q_stride + (it.h * p.G + rho - token * p.G) * kD + 16 * t4);
-                    a = __ldg(src);
-                    b = __ldg(src + 1);
-                }
-                const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-                float scale = p.scale_log2;
-                if (QUANT) {
-                    uint32_t top = 0;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) top = max(top, max((w[e] & 0x7fffu) << 16, w[e] & 0x7fff0000u));
-                    top = max(top, __shfl_xor_sync(kFull, top, 1));
-                    top = max(top, __shfl_xor_sync(kFull, top, 2));
-                    // 2^(14 - e) for a largest magnitude of 2^e; as it is for
-                    // a row that is zero or not finite.
-                    const uint32_t ex = top >> 23;
-                    const uint32_t f = ex == 0 || ex == 255 ? 127u : min(268u - ex, 253u);
-                    const float up = __uint_as_float(f << 23);
-                    scale *= __uint_as_float((254u - f) << 23);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) R.q[nt][e] = pack_half2(bf16_lo(w[e]) * up, bf16_hi(w[e]) * up);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) R.q[nt][e] = w[e];
-                }
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int mine = (8 * nt + 2 * t4 + c) / p.G;
-                    R.scale[nt][c] = __shfl_sync(kFull, scale, 4 * (2 * t4 + c));
-                    R.sees[nt][c] = mine < it.tokens ? keys_seen(p, it.ctx, it.n, mine) : 0;
-                    R.m[nt][c] = R.mo[nt][c] = -INFINITY;
-                    R.l[nt][c] = 0.f;
-                }
-#pragma unroll
-                for (int d = 0; d < 4; ++d)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) R.o[nt][d][e] = 0.f;
-            }
-            R.near = QUANT;
-            R.e_hi = -1;
-            R.e_lo = 256;
-            bool alive = true;
-            for (int j = first_page<QUANT>(warp, it.base); j < pages; j += kWarps) {
-                Records *rec = recs + piece % kRecords;
-                const int key0 = (page0 + j) * kP;
-                alive = __builtin_expect(wide, 0)
-                            ? take_page<QUANT, 2>(R, load, p, kv_map, pieces, bar_piece, n, turn, key0, least, limit, rec,
-                                                  piece, lane, abort_flag)
-                            : take_page<QUANT, 1>(R, load, p, kv_map, pieces, bar_piece, n, turn, key0, least, limit, rec,
-                                                  piece, lane, abort_flag);
-                if (!alive) break;
-            }
-            if (!alive) break;
-            // ---------------------------------------------------- merging --
-            if (n > 0 && !warp_wait(bar_merged, (n - 1) & 1, abort_flag, p.status)) break;
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-                if (nt == 1 && !wide) break;
-                float *dst = merge_o + (warp * kSmallRows + 8 * nt + 2 * t4) * kORow;
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const float sum = keys_sum(R.l[nt][c]);
-                    if (g == 0)
-                        merge_s[warp * kSmallRows + 8 * nt + 2 * t4 + c] =
-                            make_float4(R.m[nt][c], sum, QUANT ? R.mo[nt][c] : R.m[nt][c], 0.f);
-                }
-#pragma unroll
-                for (int d = 0; d < 4; ++d)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int dim = QUANT ? 32 * (d >> 1) + 4 * g + 2 * (d & 1) + (e >> 1) : 16 * d + g + 8 * (e >> 1);
-                        dst[(e & 1) * kORow + dim] = R.o[nt][d][e];
-                    }
-            }
+            // (The rare case is not in the way of the other's registers.)
+            const bool done = it.tokens * p.G > 8
+                                  ? take_piece<QUANT, 2>(p, kv_map, pieces, bar_piece, n, load, turn, recs, merge_o, merge_s,
+                                                         bar_merged, warp, lane, abort_flag)
+                                  : take_piece<QUANT, 1>(p, kv_map, pieces, bar_piece, n, load, turn, recs, merge_o, merge_s,
+                                                         bar_merged, warp, lane, abort_flag);
+            if (!done) break;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_left);
         }
