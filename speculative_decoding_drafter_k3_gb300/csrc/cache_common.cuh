@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <cstring>
+
 #include "k3da.h"
 
 namespace k3da_cache {
@@ -39,12 +41,39 @@ __device__ __forceinline__ long long page_of(const int32_t *page_table, int page
     return page < 0 || page >= num_pages ? -1 : page;
 }
 
+// The kernel in front of this one on the stream is complete, and what it
+// wrote can be read.
+__device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The kernel behind this one may start (once every CTA has said so or left).
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t *>(&v);
 }
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+// Launches `kernel` as a programmatic dependent: it may start before the
+// kernel in front of it on the stream is complete, and waits for that itself
+// (wait_for_stream), before it reads or writes anything or, where it only has
+// to be complete later, at its end.
+template <typename... Params, typename... Args>
+inline int launch_beside(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t stream,
+                         const Args &...args) {
+    cudaLaunchConfig_t lc;
+    std::memset(&lc, 0, sizeof lc);
+    lc.gridDim = grid;
+    lc.blockDim = dim3(static_cast<unsigned>(threads));
+    lc.dynamicSmemBytes = static_cast<size_t>(smem);
+    lc.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelEx(&lc, kernel, args...) == cudaSuccess ? K3DA_OK : K3DA_ECUDA;
+}
 
 inline bool aligned_to(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 

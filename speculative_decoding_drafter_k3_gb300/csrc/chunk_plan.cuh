@@ -41,6 +41,7 @@ struct ChunkParams {
     int mask;
     int pass;       // which items: kLong, kSmall or kAll
     int part_rows;  // rows of a partial result
+    int second;     // the other pass goes before this one
     float scale_log2;
 };
 
@@ -301,8 +302,7 @@ __device__ __forceinline__ uint32_t swz(int row, int chunk) {
     return static_cast<uint32_t>(row * 128 + ((chunk ^ (row & 7)) << 4));
 }
 
-// The small kernel (k3da_chunk_small.cu).  second: it follows the long
-// chunks' kernel on the stream and may start beside it.
-int launch_small(const ChunkParams &p, const void *kv_pool, bool quant, bool second, cudaStream_t stream);
+// The small kernel (k3da_chunk_small.cu).
+int launch_small(const ChunkParams &p, const void *kv_pool, bool quant, cudaStream_t stream);
 
 }  // namespace k3da_chunk

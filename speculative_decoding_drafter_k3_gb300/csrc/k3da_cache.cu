@@ -135,6 +135,9 @@ __global__ void __launch_bounds__(kAppendThreads) k3da_kv_append_kernel(const __
     __shared__ int32_t cu[kMaxRequests + 1];
     __shared__ long long slot[kAppendTokens];  // first row of the token's page and its slot, -1: nothing is written
     __shared__ bool real[kAppendTokens];       // the token is some request's
+    // Started beside the end of what is in front; what is behind starts only
+    // when these CTAs leave (let in at once, its CTAs took 4 of 13 us).
+    wait_for_stream();
     const int tid = threadIdx.x;
     const int t0 = blockIdx.x * p.tokens_per_cta;
     const int ntok = min(p.T - t0, p.tokens_per_cta);
@@ -307,6 +310,7 @@ template <bool QUANT>
 __global__ void __launch_bounds__(kGatherThreads) k3da_kv_gather_kernel(const __grid_constant__ GatherParams p) {
     __shared__ int32_t cu[kMaxRequests + 1];
     __shared__ long long slot[kGatherTokens];  // first row of the token's page and its slot, -1: zeros, -2: the row is left alone
+    wait_for_stream();
     const int tid = threadIdx.x;
     const int t0 = blockIdx.x * p.tokens_per_cta;
     const int ntok = min(p.T - t0, p.tokens_per_cta);
@@ -477,11 +481,10 @@ int launch_append(void *kv_pool, int cache_dtype, void *kv_scales, int64_t num_p
     const unsigned ctas = static_cast<unsigned>((static_cast<long long>(T) + prm.tokens_per_cta - 1) / prm.tokens_per_cta);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool quant = cache_dtype == K3DA_CACHE_E4M3;
-    if (norm && quant) k3da_kv_append_kernel<true, true><<<ctas, kAppendThreads, 0, st>>>(prm);
-    else if (norm) k3da_kv_append_kernel<true, false><<<ctas, kAppendThreads, 0, st>>>(prm);
-    else if (quant) k3da_kv_append_kernel<false, true><<<ctas, kAppendThreads, 0, st>>>(prm);
-    else k3da_kv_append_kernel<false, false><<<ctas, kAppendThreads, 0, st>>>(prm);
-    return cudaGetLastError() == cudaSuccess ? K3DA_OK : K3DA_ECUDA;
+    if (norm && quant) return launch_beside(k3da_kv_append_kernel<true, true>, dim3(ctas), kAppendThreads, 0, st, prm);
+    if (norm) return launch_beside(k3da_kv_append_kernel<true, false>, dim3(ctas), kAppendThreads, 0, st, prm);
+    if (quant) return launch_beside(k3da_kv_append_kernel<false, true>, dim3(ctas), kAppendThreads, 0, st, prm);
+    return launch_beside(k3da_kv_append_kernel<false, false>, dim3(ctas), kAppendThreads, 0, st, prm);
 }
 
 }  // namespace
@@ -545,7 +548,7 @@ extern "C" int k3da_kv_gather(void *k_out, void *v_out, const void *kv_pool, int
     const unsigned ctas =
         static_cast<unsigned>((static_cast<long long>(num_tokens) + prm.tokens_per_cta - 1) / prm.tokens_per_cta);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (cache_dtype == K3DA_CACHE_E4M3) k3da_kv_gather_kernel<true><<<ctas, kGatherThreads, 0, st>>>(prm);
-    else k3da_kv_gather_kernel<false><<<ctas, kGatherThreads, 0, st>>>(prm);
-    return cudaGetLastError() == cudaSuccess ? K3DA_OK : K3DA_ECUDA;
+    if (cache_dtype == K3DA_CACHE_E4M3)
+        return launch_beside(k3da_kv_gather_kernel<true>, dim3(ctas), kGatherThreads, 0, st, prm);
+    return launch_beside(k3da_kv_gather_kernel<false>, dim3(ctas), kGatherThreads, 0, st, prm);
 }

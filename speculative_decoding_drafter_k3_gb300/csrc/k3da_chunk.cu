@@ -194,9 +194,13 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
     const uint32_t bar_done = bar_xch + 8;                  // every issuer's products are complete
     const int warp = __shfl_sync(kFull, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
 
+    // The second pass's kernel starts beside the first's, which has waited
+    // for what came before both.
+    if (!p.second) wait_for_stream();
+    let_next_start();
     if (!build_plan<512>(p, pl, blockIdx.x == 0)) {  // every chunk is small
         if (threadIdx.x == 0) p.cuts[blockIdx.x] = Cut{};
-        asm volatile("griddepcontrol.wait;" ::: "memory");
+        wait_for_stream();
         return;
     }
     if (threadIdx.x == 0) {
@@ -248,7 +252,6 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
     __syncthreads();
     fence_after();
     const uint32_t tmem = *taddr_slot;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     bool alive = true;
     if (warp < 4 * kGroups) regs_raise<softmax_regs(QUANT)>();
     else regs_lower<other_regs(QUANT)>();
@@ -912,7 +915,7 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
     if (warp == kLoadWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
     // The kernel this one may have started beside is complete before it is.
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_stream();
 }
 
 // ----------------------------------------------------------------- combine --
@@ -934,7 +937,8 @@ __global__ void __launch_bounds__(kCombineThreads)
     __shared__ float2 part_ml[8][2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const ChunkParams &p = blockIdx.z == 0 ? first : second;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    let_next_start();
+    wait_for_stream();
     // The x-th CTA that left an item unfinished.
     static_assert(kCtas <= kCombineThreads, "one CTA a thread");
     const bool cut_here = tid < kCtas && p.cuts[tid].has[1];
@@ -1027,15 +1031,14 @@ __global__ void __launch_bounds__(kCombineThreads)
 // -------------------------------------------------------------------- host --
 
 template <bool QUANT>
-int launch_kernel(const CUtensorMap &kv_map, const CUtensorMap &q_map, const ChunkParams &prm, bool second,
-                  cudaStream_t st) {
+int launch_kernel(const CUtensorMap &kv_map, const CUtensorMap &q_map, const ChunkParams &prm, cudaStream_t st) {
     if (!allow_smem<QUANT>(reinterpret_cast<const void *>(k3da_chunk_kernel<QUANT>), Smem<QUANT>::kBytes))
         return K3DA_ECUDA;
-    return launch_beside(k3da_chunk_kernel<QUANT>, dim3(kCtas), threads_of(QUANT), Smem<QUANT>::kBytes, second, st, kv_map,
+    return launch_beside(k3da_chunk_kernel<QUANT>, dim3(kCtas), threads_of(QUANT), Smem<QUANT>::kBytes, st, kv_map,
                          q_map, prm);
 }
 
-int launch_long(const ChunkParams &prm, const void *q, const void *kv_pool, bool quant, bool second, cudaStream_t st) {
+int launch_long(const ChunkParams &prm, const void *q, const void *kv_pool, bool quant, cudaStream_t st) {
     const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     CUtensorMap kv_map, q_map;
     if (encode == nullptr || !pool_map(encode, &kv_map, kv_pool, prm.num_pages, prm.Hkv, quant, !quant)) return K3DA_ECUDA;
@@ -1047,8 +1050,7 @@ int launch_long(const ChunkParams &prm, const void *q, const void *kv_pool, bool
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return K3DA_ECUDA;
-    return quant ? launch_kernel<true>(kv_map, q_map, prm, second, st)
-                 : launch_kernel<false>(kv_map, q_map, prm, second, st);
+    return quant ? launch_kernel<true>(kv_map, q_map, prm, st) : launch_kernel<false>(kv_map, q_map, prm, st);
 }
 
 }  // namespace
@@ -1136,9 +1138,8 @@ extern "C" int k3da_chunk_attn(void *out, float *lse, const void *q, int64_t q_r
     for (int i = 0; i < 2; ++i) {
         const bool is_small = (i == 0) == small_first;
         if (is_small ? one_kernel : !can_be_long) continue;
-        const bool second = i == 1 && can_be_long && !one_kernel;
-        const int launched =
-            is_small ? launch_small(small, kv_pool, quant, second, st) : launch_long(prm, q, kv_pool, quant, second, st);
+        (is_small ? small : prm).second = i == 1 && can_be_long && !one_kernel;
+        const int launched = is_small ? launch_small(small, kv_pool, quant, st) : launch_long(prm, q, kv_pool, quant, st);
         if (launched != K3DA_OK) return launched;
     }
     // Where all there can be fits one slice, nothing is cut (a token over 300:
@@ -1154,5 +1155,5 @@ extern "C" int k3da_chunk_attn(void *out, float *lse, const void *q, int64_t q_r
     rows = rows < 2 ? 2 : rows;
     return launch_beside(k3da_chunk_combine_kernel,
                          dim3(gx, static_cast<unsigned>((bound + rows - 1) / rows), can_be_long && !one_kernel ? 2 : 1),
-                         kCombineThreads, 0, true, st, one_kernel ? prm : small, prm, rows);
+                         kCombineThreads, 0, st, one_kernel ? prm : small, prm, rows);
 }

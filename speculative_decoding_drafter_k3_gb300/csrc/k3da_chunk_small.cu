@@ -742,10 +742,13 @@ __global__ void __launch_bounds__(Smem<QUANT>::kThreads, 1)
     const uint32_t bar_merged = bar_left + 8;          // ... and read, and the piece's place is free
     const int warp = __shfl_sync(kFull, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // The second pass's kernel starts beside the first's, which has waited
+    // for what came before both.
+    if (!p.second) wait_for_stream();
+    let_next_start();
     if (!build_plan<256>(p, pl, blockIdx.x == 0)) {
         if (threadIdx.x == 0) p.cuts[blockIdx.x] = Cut{};
-        asm volatile("griddepcontrol.wait;" ::: "memory");
+        wait_for_stream();
         return;
     }
     if (threadIdx.x == 0) {
@@ -825,24 +828,24 @@ __global__ void __launch_bounds__(Smem<QUANT>::kThreads, 1)
         load.drain();
     }
     // The kernel this one may have started beside is complete before it is.
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_stream();
 }
 
 template <bool QUANT>
-int launch(const CUtensorMap &kv_map, const ChunkParams &p, bool second, cudaStream_t stream) {
+int launch(const CUtensorMap &kv_map, const ChunkParams &p, cudaStream_t stream) {
     if (!allow_smem<2 + QUANT>(reinterpret_cast<const void *>(k3da_chunk_small_kernel<QUANT>), Smem<QUANT>::kBytes))
         return K3DA_ECUDA;
-    return launch_beside(k3da_chunk_small_kernel<QUANT>, dim3(kCtas), Smem<QUANT>::kThreads, Smem<QUANT>::kBytes, second,
+    return launch_beside(k3da_chunk_small_kernel<QUANT>, dim3(kCtas), Smem<QUANT>::kThreads, Smem<QUANT>::kBytes,
                          stream, kv_map, p);
 }
 
 }  // namespace
 
-int launch_small(const ChunkParams &p, const void *kv_pool, bool quant, bool second, cudaStream_t stream) {
+int launch_small(const ChunkParams &p, const void *kv_pool, bool quant, cudaStream_t stream) {
     const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     CUtensorMap kv_map;
     if (encode == nullptr || !pool_map(encode, &kv_map, kv_pool, p.num_pages, p.Hkv, quant, true)) return K3DA_ECUDA;
-    return quant ? launch<true>(kv_map, p, second, stream) : launch<false>(kv_map, p, second, stream);
+    return quant ? launch<true>(kv_map, p, stream) : launch<false>(kv_map, p, stream);
 }
 
 }  // namespace k3da_chunk

@@ -1,5 +1,5 @@
-// tensor_maps.h -- host side of the chunk attention: TMA descriptors and
-// launches.
+// tensor_maps.h -- host side of the chunk attention's TMA descriptors and
+// kernel attributes.
 #pragma once
 
 #include <cuda.h>
@@ -7,11 +7,9 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <cstring>
 #include <mutex>
 
 #include "cache_common.cuh"
-#include "k3da.h"
 
 namespace k3da_chunk {
 
@@ -42,26 +40,6 @@ inline bool allow_smem(const void *kernel, int bytes) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
     done[dev / 64] |= 1ull << (dev % 64);
     return true;
-}
-
-// Launches `kernel`; `beside`: as a programmatic dependent, which starts
-// before the kernel in front of it on the stream is complete, and waits for
-// it by itself.
-template <typename... Params, typename... Args>
-inline int launch_beside(void (*kernel)(Params...), dim3 grid, int threads, int smem, bool beside, cudaStream_t stream,
-                         const Args &...args) {
-    cudaLaunchConfig_t lc;
-    std::memset(&lc, 0, sizeof lc);
-    lc.gridDim = grid;
-    lc.blockDim = dim3(static_cast<unsigned>(threads));
-    lc.dynamicSmemBytes = static_cast<size_t>(smem);
-    lc.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    lc.attrs = attr;
-    lc.numAttrs = beside ? 1 : 0;
-    return cudaLaunchKernelEx(&lc, kernel, args...) == cudaSuccess ? K3DA_OK : K3DA_ECUDA;
 }
 
 // A pool as rows of 64 dims, in boxes of a page's 64 slots: bf16 with the
