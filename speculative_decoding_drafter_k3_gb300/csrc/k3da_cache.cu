@@ -100,7 +100,11 @@ __device__ __forceinline__ uint2 values4(uint32_t c, float mul) {
 // holds the pairs (j, j + 32), 16 hp <= j < 16 hp + 16, read with 16-byte
 // loads that are issued before anything they do not depend on: the search
 // for the row's request, its page, the angles.  A CTA takes 128 rows' worth
-// of whole tokens.  Bound by memory: each row is read and written once.
+// of whole tokens at once, and the next ones' rows while it works on them.
+// Each row is read and written once; the shared-memory reads of cos, sin and
+// the weights bound it: 16.8k tokens in 8 requests, 24/4 heads, q out, e4m3:
+// 12.9 us where the bytes alone take 8.2.  Raw, bf16: 16k tokens 4.4 us
+// (2.7).
 constexpr int kAppendThreads = 256;
 constexpr int kAppendRows = kAppendThreads / 2;
 constexpr int kAppendTokens = 64;  // most tokens of a CTA
@@ -286,7 +290,8 @@ __global__ void __launch_bounds__(kAppendThreads) k3da_kv_append_kernel(const __
 //
 // Four threads per (token, K or V, head) row, 16 dims each: 32 bytes (bf16)
 // or 16 codes and the row's scale in, 32 bytes out.  A thread issues the
-// loads of all its rows before it stores any.  Bound by memory.
+// loads of all its rows before it stores any.  Bound by memory: 60k tokens,
+// 4 heads, e4m3: 18.4 us (the bytes alone 17.1); 2041 tokens, 1 head 2.3 us.
 constexpr int kGatherThreads = 256;
 constexpr int kGatherTokens = 256;  // most tokens of a CTA
 constexpr int kGatherWave = 4 * 152;  // CTAs that run at once
@@ -391,7 +396,8 @@ __global__ void __launch_bounds__(kGatherThreads) k3da_kv_gather_kernel(const __
 
 // Tokens of a CTA: as many as its threads take at once, and so many times
 // that where the call would fill the SMs more than once (what a CTA does
-// before its first row is two dependent loads and a search).
+// before its first row is two dependent loads and a search: with one round of
+// 4 tokens a CTA the 12.9 us of append were 19).
 inline int tokens_of(int T, int at_once, int most, int wave) {
     if (at_once < 1) at_once = 1;
     const long long ctas = (static_cast<long long>(T) + at_once - 1) / at_once;

@@ -18,9 +18,12 @@
 // the combine kernel folds in order.  Each CTA finds its slice by itself: a
 // scan over the requests, then closed forms.
 //
+// Chunks of at most 16 rows a kv head have a kernel of their own
+// (k3da_chunk_small.cu); what follows is the others'.
+//
 // Both slots of an item read the same K/V tiles (shared).  An item whose
-// tokens fit one slot (a decode step, a draft block, a chunk's tail) gives
-// its tiles to the two slots in turn (alternate), both with the same rows.
+// tokens fit one slot (a draft block, a chunk's tail) gives its tiles to the
+// two slots in turn (alternate), both with the same rows.
 // Either way a slot's tile is worked on by two softmax warpgroups, one for
 // each page: a thread has 64 scores of a row in registers.  The two share the
 // row's running maximum (each leaves its page's in shared memory, and reads
@@ -50,6 +53,12 @@
 //
 // Rounding: scores, softmax statistics and O are fp32 throughout (partials
 // too); P is rounded to bf16 once for the P V product, the output once.
+//
+// Measured: 2048 tokens over 6144 (24/4 heads) bf16 110 us, 820 TFLOP/s; e4m3
+// 140 us; 8192 over 8192 e4m3 780 us, 790 TFLOP/s.  Bound by issue slots (67%
+// taken; 73% with codes) and the slots' chain: two slots' tile takes 2100
+// cycles, its exponentials and its products 1024 each.  8 x 8 tokens over
+// 16k to 131k bf16: 105 us, 5.4 TB/s of cache.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
