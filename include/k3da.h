@@ -417,6 +417,21 @@ int k3da_chunk_attn(void *out, float *lse, const void *q, int64_t q_row_stride, 
                     int num_kv_heads, int head_dim, int mask, float softmax_scale,
                     void *workspace, size_t workspace_bytes, int32_t *status, void *stream);
 
+/*
+ * k3da_packed_call -- one of the calls above, its arguments in its order as
+ * 64-bit words: pointers and integers as they are, floats as doubles.  For
+ * bindings in which converting two dozen arguments takes as long as the call.
+ * K3DA_EINVAL for an unknown call, a wrong number of words, or an integer
+ * that does not fit its argument.
+ */
+typedef enum {
+    K3DA_CALL_KV_APPEND = 0,
+    K3DA_CALL_KV_APPEND_QKNORM = 1,
+    K3DA_CALL_KV_GATHER = 2,
+    K3DA_CALL_CHUNK_ATTN = 3
+} k3da_call;
+int k3da_packed_call(int call, const void *words, int num_words);
+
 /* Static description of a k3da_error or K3DA_STATUS_* bit set. */
 const char *k3da_error_string(int code);
 

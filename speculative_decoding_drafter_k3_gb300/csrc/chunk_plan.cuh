@@ -161,7 +161,8 @@ struct Piece {
     int t0, t1;
     int alt;     // one slot's worth of rows: the slots take the tiles in turn
     int seq;     // number of the piece among those with tiles
-    int q;       // where its Q is: slot 0's half of the Q room, and (bits 1, 2) how often the halves were filled before, mod 2
+    int q;       // where its Q is: slot 0's half of the Q room, and (bits 1, 2) how often
+                 // the halves were filled before, mod 2
     int base;    // steps (small kernel: pages) before it
     // The tiles of slot s: from, from + step, ... below end.
     __device__ __forceinline__ int from(int s) const { return alt ? t0 + s : t0; }

@@ -558,3 +558,102 @@ extern "C" int k3da_kv_gather(void *k_out, void *v_out, const void *kv_pool, int
         return launch_beside(k3da_kv_gather_kernel<true>, dim3(ctas), kGatherThreads, 0, st, prm);
     return launch_beside(k3da_kv_gather_kernel<false>, dim3(ctas), kGatherThreads, 0, st, prm);
 }
+
+// ------------------------------------------------------------ packed calls --
+
+namespace {
+
+// The words of a packed call, taken in turn.
+struct Words {
+    const unsigned char *at;
+    bool fits = true;
+
+    template <typename T>
+    T word() {
+        static_assert(sizeof(T) == 8, "a word");
+        T v;
+        std::memcpy(&v, at, 8);
+        at += 8;
+        return v;
+    }
+    int i() {
+        const int64_t v = word<int64_t>();
+        fits = fits && v >= INT32_MIN && v <= INT32_MAX;
+        return static_cast<int>(v);
+    }
+    int64_t l() { return word<int64_t>(); }
+    float f() { return static_cast<float>(word<double>()); }
+    void *p() { return reinterpret_cast<void *>(static_cast<uintptr_t>(word<uint64_t>())); }
+    int32_t *ints() { return static_cast<int32_t *>(p()); }
+};
+
+// The arguments from kv_pool to num_requests, as every cache call has them.
+struct CacheWords {
+    void *pool;
+    int dtype;
+    void *scales;
+    int64_t pages;
+    int32_t *table;
+    int stride;
+    int32_t *lens, *cu;
+    int R;
+    explicit CacheWords(Words &w)
+        : pool(w.p()), dtype(w.i()), scales(w.p()), pages(w.l()), table(w.ints()), stride(w.i()), lens(w.ints()),
+          cu(w.ints()), R(w.i()) {}
+};
+
+}  // namespace
+
+extern "C" int k3da_packed_call(int call, const void *words, int num_words) {
+    constexpr int kNumWords[4] = {16, 24, 16, 23};
+    if (call < 0 || call > 3 || words == nullptr || num_words != kNumWords[call]) return K3DA_EINVAL;
+    Words w{static_cast<const unsigned char *>(words)};
+    if (call == K3DA_CALL_KV_APPEND || call == K3DA_CALL_KV_APPEND_QKNORM) {
+        const CacheWords c(w);
+        void *qkv = w.p();
+        const int T = w.i(), hq = w.i(), hkv = w.i(), d = w.i();
+        if (call == K3DA_CALL_KV_APPEND) {
+            int32_t *status = w.ints();
+            void *stream = w.p();
+            if (!w.fits) return K3DA_EINVAL;
+            return k3da_kv_append(c.pool, c.dtype, c.scales, c.pages, c.table, c.stride, c.lens, c.cu, c.R, qkv, T, hq, hkv,
+                                  d, status, stream);
+        }
+        void *positions = w.p();
+        const int pos_dtype = w.i();
+        void *q_w = w.p(), *k_w = w.p();
+        const float eps = w.f(), base = w.f();
+        const k3da_yarn *yarn = static_cast<const k3da_yarn *>(w.p());
+        void *q_out = w.p();
+        int32_t *status = w.ints();
+        void *stream = w.p();
+        if (!w.fits) return K3DA_EINVAL;
+        return k3da_kv_append_qknorm(c.pool, c.dtype, c.scales, c.pages, c.table, c.stride, c.lens, c.cu, c.R, qkv, T, hq,
+                                     hkv, d, positions, pos_dtype, q_w, k_w, eps, base, yarn, q_out, status, stream);
+    }
+    if (call == K3DA_CALL_KV_GATHER) {
+        void *k = w.p(), *v = w.p();
+        const CacheWords c(w);
+        const int T = w.i(), hkv = w.i(), d = w.i();
+        int32_t *status = w.ints();
+        void *stream = w.p();
+        if (!w.fits) return K3DA_EINVAL;
+        return k3da_kv_gather(k, v, c.pool, c.dtype, c.scales, c.pages, c.table, c.stride, c.lens, c.cu, c.R, T, hkv, d,
+                              status, stream);
+    }
+    void *out = w.p();
+    float *lse = static_cast<float *>(w.p());
+    void *q = w.p();
+    const int64_t q_stride = w.l();
+    const int T = w.i();
+    const CacheWords c(w);
+    const int hq = w.i(), hkv = w.i(), d = w.i(), mask = w.i();
+    const float scale = w.f();
+    void *workspace = w.p();
+    const size_t bytes = static_cast<size_t>(w.l());
+    int32_t *status = w.ints();
+    void *stream = w.p();
+    if (!w.fits) return K3DA_EINVAL;
+    return k3da_chunk_attn(out, lse, q, q_stride, T, c.pool, c.dtype, c.scales, c.pages, c.table, c.stride, c.lens, c.cu,
+                           c.R, hq, hkv, d, mask, scale, workspace, bytes, status, stream);
+}

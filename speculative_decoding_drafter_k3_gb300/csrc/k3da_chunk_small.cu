@@ -76,11 +76,12 @@ struct Smem {
     static constexpr int kNumBars = kTiles + kRing + 2;
     static constexpr int kTail = kBars + kNumBars * 8;
     static constexpr int kBytes = kTail + 16 + 1024;
-    static_assert(kBytes <= 227 * 1024 && kMerge % 16 == 0 && kStats % 16 == 0 && kRec % 8 == 0 && kPlan % 8 == 0 && kBars % 8 == 0, "layout");
+    static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
+    static_assert(kMerge % 16 == 0 && kStats % 16 == 0 && kRec % 8 == 0 && kPlan % 8 == 0 && kBars % 8 == 0, "alignment");
 };
 
 template <bool HALF>
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
     if (HALF)
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -333,7 +334,9 @@ struct Turn {
 // tile n, and of a 16-key tile i the keys 16 i + kg and + 8.
 template <int NT>
 struct Rows {
-    uint32_t q[NT][8];  // of row 8 n + g: dims 16 t4 .. 16 t4 + 15 (and so of every key: a product's order of dims is free)
+    // Of row 8 n + g: dims 16 t4 .. 16 t4 + 15 (and so of every key: a
+    // product's order of dims is free).
+    uint32_t q[NT][8];
     float scale[NT][2];
     int sees[NT][2];
     float m[NT][2], l[NT][2];

@@ -149,3 +149,46 @@ def test_quantise_by_the_definition():
     assert byte[:5].tolist() == [127, 128, 119, 127, 127] and byte[5:].tolist() == [255, 255, 127, 0]
     assert v[0, 0] == 448 and v[1, 0] == 448 and v[2, 0] == 1 and v[3, 1] == 16 and v[4, 1] == 20 and v[7, 1] == 0
     assert v[5].isnan().all() and v[6].isnan().all() and (v[8] == 0).all()
+
+
+def packed(lib, what, args):
+    number, count, pack = k3da._PACKED[what]
+    return lib.k3da_packed_call(number, pack(*[0 if x is None else x for x in args]), count)
+
+
+ARGS = {
+    "k3da_kv_append": cache() + [FAR, 64, 24, 4, 64, None, None],
+    "k3da_kv_append_qknorm": cache() + [FAR, 64, 24, 4, 64, FAKE, k3da.POS_I32, FAKE, FAKE, 1e-5, 1e4, None, 2 * FAR, None,
+                                        None],
+    "k3da_kv_gather": [FAR, 2 * FAR] + cache() + [64, 4, 64, None, None],
+    "k3da_chunk_attn": [FAR, None, 2 * FAR, 24 * 64, 64] + cache() + [24, 4, 64, 0, 0.125, 3 * FAR, 1 << 30, None, None],
+}
+
+
+@pytest.mark.parametrize("what", sorted(ARGS))
+def test_a_packed_call_is_the_call(lib, what):
+    """Word by word: whatever one argument is changed to, both answer alike.
+    (All of them break something first, so that nothing is launched.)"""
+    assert len(ARGS[what]) == k3da._PACKED[what][1] == len(getattr(lib, what).argtypes)
+    pool = 2 if what == "k3da_kv_gather" else 5 if what == "k3da_chunk_attn" else 0
+    base = list(ARGS[what])
+    base[pool + 1] = 2  # no cache type
+    assert packed(lib, what, base) == getattr(lib, what)(*base) == k3da.EINVAL
+    for i, kind in enumerate(getattr(lib, what).argtypes):
+        if kind is not ctypes.c_int:
+            continue
+        for value in (-1, 0, 1 << 30, 4097):
+            args = list(ARGS[what])
+            args[pool] = FAKE + 8  # a pool that is not aligned
+            args[i] = value
+            assert packed(lib, what, args) == getattr(lib, what)(*args)
+        args = list(ARGS[what])
+        args[i] = (1 << 32) + args[i]  # would be right, cut to 32 bits
+        assert packed(lib, what, args) == k3da.EINVAL
+
+
+def test_packed_calls_refuse_what_is_no_call(lib):
+    words = bytes(8 * 24)
+    for number, count in ((-1, 16), (4, 16), (0, 15), (0, 17), (1, 16), (2, 24), (3, 22)):
+        assert lib.k3da_packed_call(number, words, count) == k3da.EINVAL
+    assert lib.k3da_packed_call(0, None, 16) == k3da.EINVAL
