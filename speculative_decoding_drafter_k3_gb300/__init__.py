@@ -435,7 +435,7 @@ def _enqueue(what, dev, stream, status, *args):
         words = pack(*args, 0 if status is None else status.data_ptr(), handle)
     except struct.error as e:
         raise K3daError(f"{what}: {e}") from None
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         rc = call(number, words, count)
     else:
         with torch.cuda.device(dev):

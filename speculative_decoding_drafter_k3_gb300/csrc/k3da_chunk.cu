@@ -205,6 +205,10 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
 
     // The second pass's kernel starts beside the first's, which has waited
     // for what came before both.
+    if (threadIdx.x == 0) {
+        prefetch_map(&kv_map);
+        prefetch_map(&q_map);
+    }
     if (!p.second) wait_for_stream();
     let_next_start();
     if (!build_plan<512>(p, pl, blockIdx.x == 0)) {  // every chunk is small

@@ -652,16 +652,24 @@ __device__ __forceinline__ bool take_piece(const ChunkParams &p, const CUtensorM
     const int least = keys_seen(p, it.ctx, it.n, 0);  // keys that every row sees
     // The item's rows: token major, the heads of a token together.
     Rows<NT> R;
+    uint4 qa[NT], qb[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int rho = g + 8 * nt, token = rho / p.G;
-        uint4 a = make_uint4(0, 0, 0, 0), b = a;
+        qa[nt] = qb[nt] = make_uint4(0, 0, 0, 0);
         if (token < it.tokens) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(
-                p.q + static_cast<long long>(it.row + token) * p.q_stride + (it.h * p.G + rho - token * p.G) * kD + 16 * t4);
-            a = __ldg(src);
-            b = __ldg(src + 1);
+            const uint4 *src =
+                reinterpret_cast<const uint4 *>(p.q + static_cast<long long>(it.row + token) * p.q_stride +
+                                                (it.h * p.G + rho - token * p.G) * kD + 16 * t4);
+            qa[nt] = __ldg(src);
+            qb[nt] = __ldg(src + 1);
         }
+    }
+    // While they come: the piece's first tiles.
+    load.fill(p, kv_map, pieces, bar_piece, n, turn.done);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const uint4 a = qa[nt], b = qb[nt];
         const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
         float scale = p.scale_log2;
         if (QUANT) {
@@ -747,6 +755,7 @@ __global__ void __launch_bounds__(Smem<QUANT>::kThreads, 1)
 
     // The second pass's kernel starts beside the first's, which has waited
     // for what came before both.
+    if (threadIdx.x == 0) prefetch_map(&kv_map);
     if (!p.second) wait_for_stream();
     let_next_start();
     if (!build_plan<256>(p, pl, blockIdx.x == 0)) {
@@ -817,7 +826,6 @@ __global__ void __launch_bounds__(Smem<QUANT>::kThreads, 1)
             const Piece &it = pieces[n % kRing];
             if (!warp_wait(bar_piece + 8 * (n % kRing), (n / kRing) & 1, abort_flag, p.status)) break;
             if (it.row < 0) break;
-            load.fill(p, kv_map, pieces, bar_piece, n, turn.done);
             // (The rare case is not in the way of the other's registers.)
             const bool done = it.tokens * p.G > 8
                                   ? take_piece<QUANT, 2>(p, kv_map, pieces, bar_piece, n, load, turn, recs, merge_o, merge_s,

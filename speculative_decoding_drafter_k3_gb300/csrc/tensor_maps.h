@@ -52,8 +52,8 @@ inline bool pool_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *map,
     const cuuint32_t box[2] = {kD, kP}, estrides[2] = {1, 1};
     return encode(map, quant ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
                   const_cast<void *>(pool), dims, strides, box, estrides, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  !swizzled ? CU_TENSOR_MAP_SWIZZLE_NONE : quant ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                  !swizzled ? CU_TENSOR_MAP_SWIZZLE_NONE : quant ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace k3da_chunk
