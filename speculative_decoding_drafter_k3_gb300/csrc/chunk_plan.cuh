@@ -192,21 +192,29 @@ __device__ __forceinline__ int keys_seen(const ChunkParams &p, int ctx, int n, i
 // The CTA's pieces, in order (the scheduler's).
 struct Walk {
     long long lo, hi;         // the slice
-    long long total, slices;
+    long long share;          // floor(total / slices)
+    int slices, rest_of;      // ... and what is left
     long long at;             // where the next item begins
     long long start, length;  // the last item
     int r, h, pair;
     Request q;  // r's
 
-    // Start of slice c: ceil(c * total / slices), without a wide product.
-    __device__ __forceinline__ long long slice(long long c) const {
-        const long long q = total / slices, rem = total - q * slices;
-        return c * q + (c * rem + slices - 1) / slices;
+    // Start of slice c: ceil(c * total / slices).
+    __device__ __forceinline__ long long slice(int c) const {
+        return c * share + (c * rest_of + slices - 1) / slices;
+    }
+    // (Wide divisions take hundreds of cycles, and nothing is loaded before
+    // this is done.)
+    __device__ __forceinline__ static long long quotient(long long a, long long b) {
+        if ((a | b) >> 31 == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+        return a / b;
     }
     __device__ void begin(const ChunkParams &p, const Plan *pl, int cta) {
-        total = pl->prefix[p.R];
-        slices = total / (p.pass == kSmall ? kMinSmallSlice : kMinSlice);
-        slices = slices < 1 ? 1 : slices > kCtas ? kCtas : slices;
+        const long long total = pl->prefix[p.R];
+        const long long most = p.pass == kSmall ? total / kMinSmallSlice : total / kMinSlice;
+        slices = most < 1 ? 1 : most > kCtas ? kCtas : static_cast<int>(most);
+        share = quotient(total, slices);
+        rest_of = static_cast<int>(total - share * slices);
         lo = hi = at = 0;
         r = h = pair = 0;
         if (cta >= slices || total == 0) return;
@@ -223,7 +231,7 @@ struct Walk {
         const long long keys = q.base(p);
         const long long head = line_of(p, keys, q.pairs(p));
         long long rest = lo - pl->prefix[r];
-        h = static_cast<int>(rest / head);
+        h = static_cast<int>(quotient(rest, head));
         rest -= h * head;
         int x = 0, y = q.pairs(p);
         while (y - x > 1) {
@@ -278,7 +286,7 @@ struct Walk {
 
     // The slice that holds this position of the line.
     __device__ int slice_of(long long pos) const {
-        int a = 0, b = static_cast<int>(slices);
+        int a = 0, b = slices;
         while (b - a > 1) {
             const int mid = (a + b) >> 1;
             if (slice(mid) <= pos) a = mid;

@@ -203,6 +203,24 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
     const uint32_t bar_done = bar_xch + 8;                  // every issuer's products are complete
     const int warp = __shfl_sync(kFull, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
 
+    // What needs none of the call's data, while the kernel in front ends.
+    if (threadIdx.x == 0) *abort_flag = 0;
+    if (threadIdx.x < L::kNumBars) {
+        const uint32_t bar = bars + 8 * threadIdx.x;
+        auto of = [&](uint32_t first, int n) { return bar >= first && bar < first + 8 * n; };
+        const int count = of(bar_prep, L::kVs) || of(bar_rempty, L::kRaw) ? kPrepWarps
+                          : of(bar_empty, L::kVs)                         ? 2
+                          : of(bar_pdone, kRing)                          ? kThreads / 32 - 1  // every warp but the scheduler
+                          : of(bar_pfull, 2 * kBufs) || of(bar_ofree, 2) || of(bar_sums, 2) || of(bar_xch, 1) ? 8
+                          : of(bar_done, 1)                                                                   ? 3
+                                                                                                              : 1;
+        mbar_init(bar, count);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    for (int e = threadIdx.x; e < kRecords; e += kThreads) recs[e].piece = -1;
+    for (int e = threadIdx.x; e < 2 * kGroups * kSlotRows; e += kThreads) xmax[e] = ~0ull;  // of no tile
+    for (int e = threadIdx.x; e < kRecords * 3 * kD; e += kThreads)
+        (&recs[e / (3 * kD)].first[0][0])[e % (3 * kD)] = 0xffffffffu;
     // The second pass's kernel starts beside the first's, which has waited
     // for what came before both.
     if (threadIdx.x == 0) {
@@ -216,45 +234,6 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
         wait_for_stream();
         return;
     }
-    if (threadIdx.x == 0) {
-        *abort_flag = 0;
-        for (int s = 0; s < L::kKs; ++s) {
-            mbar_init(bar_kfull + 8 * s, 1);
-            mbar_init(bar_kempty + 8 * s, 1);
-        }
-        for (int s = 0; s < L::kVs; ++s) {
-            mbar_init(bar_vfull + 8 * s, 1);
-            mbar_init(bar_prep + 8 * s, kPrepWarps);
-            mbar_init(bar_empty + 8 * s, 2);
-        }
-        for (int s = 0; s < L::kRaw; ++s) {
-            mbar_init(bar_rfull + 8 * s, 1);
-            mbar_init(bar_rempty + 8 * s, kPrepWarps);
-        }
-        for (int s = 0; s < kRing; ++s) {
-            mbar_init(bar_piece + 8 * s, 1);
-            mbar_init(bar_pdone + 8 * s, kThreads / 32 - 1);  // every warp but the scheduler
-        }
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(bar_qfull + 8 * s, 1);
-            mbar_init(bar_qempty + 8 * s, 1);
-            mbar_init(bar_ofree + 8 * s, 8);
-            mbar_init(bar_sums + 8 * s, 8);
-        }
-        for (int b = 0; b < 2 * kBufs; ++b) {
-            mbar_init(bar_sfull + 8 * b, 1);
-            mbar_init(bar_pfull + 8 * b, 8);
-            mbar_init(bar_pvdone + 8 * b, 1);
-        }
-        for (int b = 0; b < kBufs; ++b) mbar_init(bar_bfree + 8 * b, 1);
-        mbar_init(bar_xch, 8);
-        mbar_init(bar_done, 3);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    for (int e = threadIdx.x; e < kRecords; e += kThreads) recs[e].piece = -1;
-    for (int e = threadIdx.x; e < 2 * kGroups * kSlotRows; e += kThreads) xmax[e] = ~0ull;  // of no tile
-    for (int e = threadIdx.x; e < kRecords * 3 * kD; e += kThreads)
-        (&recs[e / (3 * kD)].first[0][0])[e % (3 * kD)] = 0xffffffffu;
     if (warp == kLoadWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(taddr_slot)),
                      "r"(kTmemCols)

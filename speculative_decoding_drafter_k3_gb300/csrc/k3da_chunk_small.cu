@@ -258,8 +258,8 @@ struct Loader {
     }
 };
 
-// The page warps' results of a piece, folded, and out: a row's four dims a
-// lane at a time.
+// The page warps' results of a piece, folded, and out: sixteen dims of a row
+// a lane, eight rows at a time.
 template <bool QUANT>
 __device__ __forceinline__ void merge_piece(const ChunkParams &p, const Piece &it, const float *merge_o,
                                             const float4 *merge_s, const Records *recs, int lane) {
@@ -267,49 +267,60 @@ __device__ __forceinline__ void merge_piece(const ChunkParams &p, const Piece &i
     const bool whole = it.t0 == 0 && it.t1 == it.nt;
     const Records &rec = recs[it.seq % kRecords];
     const bool hidden = !QUANT && it.t0 < it.t1 && rec.piece == it.seq;
-    const int dim = 4 * (lane & 15);
+    const int dim0 = 16 * (lane & 3);
 #pragma unroll 1
-    for (int rho = lane >> 4; rho < it.tokens * p.G; rho += 2) {
+    for (int rho = lane >> 2; rho < it.tokens * p.G; rho += 8) {
+        // (Unrolled no further: the page loops want the instruction cache.)
         float mt = -INFINITY;
-#pragma unroll
+#pragma unroll 4
         for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, merge_s[w * kSmallRows + rho].x);
         const float me = mt == -INFINITY ? 0.f : mt;
-        float lt = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
+        float lt = 0.f, v[16] = {};
+#pragma unroll 2
         for (int w = 0; w < kWarps; ++w) {
             const float4 st = merge_s[w * kSmallRows + rho];
-            const float4 part = *reinterpret_cast<const float4 *>(merge_o + (w * kSmallRows + rho) * kORow + dim);
+            const float4 *part = reinterpret_cast<const float4 *>(merge_o + (w * kSmallRows + rho) * kORow + dim0);
             const float f = exp2_approx(st.z - me);
             lt += st.y * exp2_approx(st.x - me);
-            v[0] += part.x * f;
-            v[1] += part.y * f;
-            v[2] += part.z * f;
-            v[3] += part.w * f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float4 x = part[q];
+                v[4 * q] += x.x * f;
+                v[4 * q + 1] += x.y * f;
+                v[4 * q + 2] += x.z * f;
+                v[4 * q + 3] += x.w * f;
+            }
         }
         const float norm = whole ? 1.f / lt : 1.f;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = lt == 0.f ? 0.f : v[q] * norm;
+        for (int q = 0; q < 16; ++q) v[q] = lt == 0.f ? 0.f : v[q] * norm;
         const int token = rho / p.G;
         if (hidden) {
             const int least = keys_seen(p, it.ctx, it.n, 0), sees = keys_seen(p, it.ctx, it.n, token);
             const uint32_t tag = ~static_cast<uint32_t>(it.seq) << 8;
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < 16; ++q)
+#pragma unroll 1
                 for (int kind = 0; kind < 3; ++kind) {
-                    const uint32_t e = rec.first[kind][dim + q];
+                    const uint32_t e = rec.first[kind][dim0 + q];
                     if ((e & 0xffffff00u) != tag || least + static_cast<int>(e & 0xffu) >= sees) continue;
                     v[q] = kind == 2 ? __uint_as_float(0x7fffffffu) : v[q] + (kind == 0 ? INFINITY : -INFINITY);
                 }
         }
         if (whole) {
             const long long at = static_cast<long long>(it.row + token) * p.Hq + it.h * p.G + rho - token * p.G;
-            *reinterpret_cast<uint2 *>(p.out + at * kD + dim) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
-            if (dim == 0 && p.lse) p.lse[at] = lt == 0.f ? -INFINITY : (mt + log2f(lt)) * 0.6931471805599453f;
+            uint4 *out = reinterpret_cast<uint4 *>(p.out + at * kD + dim0);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                out[q] = make_uint4(pack2(v[8 * q], v[8 * q + 1]), pack2(v[8 * q + 2], v[8 * q + 3]),
+                                    pack2(v[8 * q + 4], v[8 * q + 5]), pack2(v[8 * q + 6], v[8 * q + 7]));
+            if (dim0 == 0 && p.lse) p.lse[at] = lt == 0.f ? -INFINITY : (mt + log2f(lt)) * 0.6931471805599453f;
         } else {
             const int part = (blockIdx.x * 2 + (it.t0 > 0 ? 0 : 1)) * kSmallRows + rho;
-            *reinterpret_cast<float4 *>(p.part_o + static_cast<long long>(part) * kD + dim) =
-                make_float4(v[0], v[1], v[2], v[3]);
-            if (dim == 0) p.part_ml[part] = make_float2(mt, lt);
+            float4 *out = reinterpret_cast<float4 *>(p.part_o + static_cast<long long>(part) * kD + dim0);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) out[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            if (dim0 == 0) p.part_ml[part] = make_float2(mt, lt);
         }
     }
 }
@@ -753,6 +764,16 @@ __global__ void __launch_bounds__(Smem<QUANT>::kThreads, 1)
     const uint32_t bar_merged = bar_left + 8;          // ... and read, and the piece's place is free
     const int warp = __shfl_sync(kFull, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
 
+    // What needs none of the call's data, while the kernel in front ends.
+    if (threadIdx.x == 0) *abort_flag = 0;
+    if (threadIdx.x < L::kNumBars)
+        mbar_init(bars + 8 * threadIdx.x, threadIdx.x == (bar_left - bars) / 8 ? kWarps : 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    if (!QUANT) {
+        for (int e = threadIdx.x; e < kRecords; e += kThreads) recs[e].piece = -1;
+        for (int e = threadIdx.x; e < kRecords * 3 * kD; e += kThreads)
+            (&recs[e / (3 * kD)].first[0][0])[e % (3 * kD)] = 0xffffffffu;
+    }
     // The second pass's kernel starts beside the first's, which has waited
     // for what came before both.
     if (threadIdx.x == 0) prefetch_map(&kv_map);
@@ -763,20 +784,7 @@ __global__ void __launch_bounds__(Smem<QUANT>::kThreads, 1)
         wait_for_stream();
         return;
     }
-    if (threadIdx.x == 0) {
-        *abort_flag = 0;
-        for (int s = 0; s < L::kTiles; ++s) mbar_init(bars + 8 * s, 1);
-        for (int s = 0; s < kRing; ++s) mbar_init(bar_piece + 8 * s, 1);
-        mbar_init(bar_left, kWarps);
-        mbar_init(bar_merged, 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    if (!QUANT) {
-        for (int e = threadIdx.x; e < kRecords; e += kThreads) recs[e].piece = -1;
-        for (int e = threadIdx.x; e < kRecords * 3 * kD; e += kThreads)
-            (&recs[e / (3 * kD)].first[0][0])[e % (3 * kD)] = 0xffffffffu;
-    }
-    __syncthreads();
+    __syncthreads();  // (without it the loops below are compiled 7% slower: for warps that may have come apart)
 
     if (warp == kWarps) {
         // ------------------------------------ pieces, and what becomes of them --
