@@ -925,6 +925,8 @@ __global__ void __launch_bounds__(kCombineThreads)
     k3da_chunk_combine_kernel(const __grid_constant__ ChunkParams first, const __grid_constant__ ChunkParams second, int rows) {
     __shared__ int votes[kCombineThreads / 32];
     __shared__ int owner;
+    __shared__ Cut cut;
+    __shared__ bool continues[kCtas];  // the CTA's first piece belongs to an item begun before
     __shared__ float4 part[8][32];
     __shared__ float2 part_ml[8][2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -933,18 +935,28 @@ __global__ void __launch_bounds__(kCombineThreads)
     wait_for_stream();
     // The x-th CTA that left an item unfinished.
     static_assert(kCtas <= kCombineThreads, "one CTA a thread");
-    const bool cut_here = tid < kCtas && p.cuts[tid].has[1];
+    // Every cut is read at once: what follows depends on nothing but them.
+    Cut mine = {};
+    if (tid < kCtas) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.cuts + tid);
+        const uint4 c[2] = {src[0], src[1]};
+        std::memcpy(&mine, c, sizeof mine);
+        continues[tid] = mine.has[0];
+    }
+    const bool cut_here = tid < kCtas && mine.has[1];
     const unsigned vote = __ballot_sync(kFull, cut_here);
     if (lane == 0) votes[warp] = __popc(vote);
     if (tid == 0) owner = -1;
     __syncthreads();
     int rank = __popc(vote & ((1u << lane) - 1u));
     for (int w = 0; w < warp; ++w) rank += votes[w];
-    if (cut_here && rank == static_cast<int>(blockIdx.x)) owner = tid;
+    if (cut_here && rank == static_cast<int>(blockIdx.x)) {
+        owner = tid;
+        cut = mine;
+    }
     __syncthreads();
     const int a = owner;
     if (a < 0) return;
-    const Cut cut = p.cuts[a];
     const int pieces = cut.last - a + 1;
     const int lanes = pieces > 8 ? 8 : 1;
     const int dim = tid & 15;
@@ -969,7 +981,7 @@ __global__ void __launch_bounds__(kCombineThreads)
                     const int i = j + q * lanes;
                     ml[q] = make_float2(-INFINITY, 0.f);
                     v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (i >= pieces || (i > 0 && !p.cuts[a + i].has[0])) continue;
+                    if (i >= pieces || (i > 0 && !continues[a + i])) continue;
                     const long long at = (static_cast<long long>(a + i) * 2 + (i == 0 ? 1 : 0)) * p.part_rows + rho;
                     ml[q] = p.part_ml[at];
                     v[q] = reinterpret_cast<const float4 *>(p.part_o + at * kD)[dim];
