@@ -306,13 +306,19 @@ int k3da_qk_norm_rope_yarn(void *qkv, int num_tokens, int num_q_heads, int num_k
  * table row's page_stride * 64 (or before 0) BAD_LENGTH, a page id out of
  * range BAD_PAGE.  The first call on a device should come before any stream
  * capture.  num_tokens 0 is a call that does nothing.
+ *
+ * The kernels are launched as programmatic dependents: they may be resident
+ * while the kernel in front of them on the stream ends, and read and write
+ * nothing before it is complete.
  */
 #define K3DA_MAX_CHUNK_REQUESTS 1024
 
 /* What a pool holds.  E4M3: kv_pool is [num_pages, 2, Hkv, 64, 64] e4m3
  * codes and kv_scales [num_pages, 2, Hkv, 64] e8m0 bytes b, one for each
  * token's K or V of one head; the row's values are code * 2^(b - 127).
- * BF16: kv_scales is NULL. */
+ * BF16: kv_scales is NULL.  The appends write no code 0x7f or 0xff (e4m3's
+ * NaN); in a pool from elsewhere, what a row that sees one gets is left open,
+ * and no other row is touched. */
 typedef enum { K3DA_CACHE_BF16 = 0, K3DA_CACHE_E4M3 = 1 } k3da_cache_dtype;
 
 /* Cache tokens that token i of a request's chunk sees. */
