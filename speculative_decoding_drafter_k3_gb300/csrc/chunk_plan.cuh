@@ -17,9 +17,14 @@ using namespace k3da_cache;
 constexpr int kCtas = 152;         // slices of the line at most: one CTA an SM
 constexpr int kTile = 128;         // keys of a tile: two pages
 constexpr int kSlotRows = 128;     // query rows of a slot
-constexpr int kOverhead = 128;     // an item's fixed cost, in keys
-constexpr int kMinSlice = 256;     // shortest slice, in keys
-constexpr int kMinSmallSlice = 512;  // ... of the small kernel: a page for each of its warps
+// An item's fixed cost (its first loads, its epilogue or fold), and the
+// shortest slice, both in keys; below, of the small kernel's items and slices.
+// Swept: 64 items x up to 8191 keys, 4 heads, e4m3 39.7 us with 128, 36.5 with
+// 512, 35.9 with 768 (but then one token over 2000 10.1 or 12.2 us, by the
+// slices, instead of 9.7 to 10.5); ragged prefills 96.4 with 128, 91.4 with 384,
+// 94.5 with 1024.
+constexpr int kOverhead = 384, kMinSlice = 256;
+constexpr int kSmallOverhead = 512, kMinSmallSlice = 512;
 
 struct ChunkParams {
     __nv_bfloat16 *out;
@@ -77,11 +82,13 @@ struct Plan {
     long long warp_sum[16];
 };
 
+__device__ __forceinline__ int overhead(const ChunkParams &p) { return p.pass == kSmall ? kSmallOverhead : kOverhead; }
+
 // Length of the first `pairs` items of one head: each sees `base` keys (and,
-// causal, its own tokens and the ones before) and costs kOverhead.
+// causal, its own tokens and the ones before) and costs the overhead.
 __device__ __forceinline__ long long line_of(const ChunkParams &p, long long base, long long pairs) {
     const long long own = p.mask == K3DA_MASK_CAUSAL ? p.tpt * pairs * (pairs + 1) : 0;  // 2 tpt (1 + 2 + ... + pairs)
-    return pairs * (base + kOverhead) + own;
+    return pairs * (base + overhead(p)) + own;
 }
 
 // A request's first row, new and cached tokens, clamped to what the call has
@@ -244,9 +251,9 @@ struct Walk {
     }
 
     // First tile of an item's part from `offset` (in the item) on.
-    __device__ __forceinline__ static int tile_at(long long offset, int nt) {
-        const long long t = (offset - kOverhead + kTile - 1) / kTile;
-        return offset <= kOverhead ? 0 : t < nt ? static_cast<int>(t) : nt;
+    __device__ __forceinline__ static int tile_at(const ChunkParams &p, long long offset, int nt) {
+        const long long t = (offset - overhead(p) + kTile - 1) / kTile;
+        return offset <= overhead(p) ? 0 : t < nt ? static_cast<int>(t) : nt;
     }
 
     __device__ bool next(const ChunkParams &p, Piece &it) {
@@ -266,8 +273,8 @@ struct Walk {
             const int count = q.pairs(p);
             const long long keys = q.base(p);
             length = line_of(p, keys, pair + 1) - line_of(p, keys, pair);
-            it.t0 = lo <= at ? 0 : tile_at(lo - at, it.nt);
-            it.t1 = hi >= at + length ? it.nt : tile_at(hi - at, it.nt);
+            it.t0 = lo <= at ? 0 : tile_at(p, lo - at, it.nt);
+            it.t1 = hi >= at + length ? it.nt : tile_at(p, hi - at, it.nt);
             at += length;
             if (++pair == count) {
                 pair = 0;

@@ -1128,10 +1128,10 @@ extern "C" int k3da_chunk_attn(void *out, float *lse, const void *q, int64_t q_r
     // small, whatever their lengths, is bound by latency: one kernel for all
     // (8 x 6 tokens over up to 2041, 6/1 heads: 16.4 us, with both 18.6; the
     // small kernel's gain on 64 x 8000 codes comes to those 3 us at 75000 keys).
-    const long long line = static_cast<long long>(num_requests) * num_kv_heads *
-                           (static_cast<long long>(page_stride) * kP + kOverhead + 2 * prm.tpt + kSmallRows);
+    const long long heads = static_cast<long long>(num_requests) * num_kv_heads;
+    const long long keys = heads * page_stride * kP;
     const bool can_be_long = num_tokens > kSmallRows || num_tokens * prm.G > kSmallRows;
-    const bool one_kernel = can_be_long && line <= static_cast<long long>(kCtas) * kMinSmallSlice;
+    const bool one_kernel = can_be_long && keys <= 75000;
     prm.pass = one_kernel ? kAll : kLong;
     ChunkParams small = prm;
     small.pass = kSmall;
@@ -1148,6 +1148,7 @@ extern "C" int k3da_chunk_attn(void *out, float *lse, const void *q, int64_t q_r
     }
     // Where all there can be fits one slice, nothing is cut (a token over 300:
     // 8.5 instead of 9.6 us).
+    const long long line = keys + heads * (kSmallOverhead + 2 * prm.tpt + kSmallRows);
     if (!can_be_long && line < 2 * kMinSmallSlice) return K3DA_OK;
     // Items a cut can fall into, rows one can have: a grid of about 1200
     // CTAs over both.
