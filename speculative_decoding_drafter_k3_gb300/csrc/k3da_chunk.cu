@@ -54,11 +54,11 @@
 // Rounding: scores, softmax statistics and O are fp32 throughout (partials
 // too); P is rounded to bf16 once for the P V product, the output once.
 //
-// Measured: 2048 tokens over 6144 (24/4 heads) bf16 110 us, 820 TFLOP/s; e4m3
-// 140 us; 8192 over 8192 e4m3 780 us, 790 TFLOP/s.  Bound by issue slots (67%
-// taken; 73% with codes) and the slots' chain: two slots' tile takes 2100
+// Measured: 2048 tokens over 6144 (24/4 heads) bf16 105 us, 860 TFLOP/s; e4m3
+// 140 us; 8192 over 8192 e4m3 776 us, 800 TFLOP/s.  Bound by issue slots (67%
+// taken; 73% with codes) and the slots' chain: two slots' tile takes 2000
 // cycles, its exponentials and its products 1024 each.  8 x 8 tokens over
-// 16k to 131k bf16: 105 us, 5.4 TB/s of cache.
+// 16k to 131k bf16: 102.5 us, 5.6 TB/s of cache.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
