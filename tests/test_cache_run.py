@@ -116,3 +116,33 @@ def test_every_step_against_the_definition(cache):
         want, wv = last.cached(r, ctx[r] + 1)
         assert torch.equal(s.inputs[-1][7][r].double().cpu(), want[ctx[r], 0])
         assert torch.equal(s.inputs[-1][8][r].double().cpu(), wv[ctx[r], 0])
+
+
+def shifted(t):
+    """A copy 16 bytes past a 256-byte boundary."""
+    raw = torch.empty(t.numel() * t.element_size() + 16, dtype=torch.uint8, device="cuda")
+    assert raw.data_ptr() % 256 == 0
+    out = raw[16:].view(t.dtype if t.dtype.itemsize > 1 else torch.uint8).view(t.dtype).view(t.shape)
+    out.view(torch.uint8).copy_(t.view(torch.uint8))
+    return out
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_tensors_on_16_byte_boundaries(cache):
+    """Nothing needs more alignment than the 16 bytes the calls ask for."""
+    b = Batch([40, 1, 7], [300, 700, 5], 6, 1, cache, seed=33)
+    results = []
+    for place in (lambda t: t, shifted):
+        pool, scales, qkv, table, lens, cu = dev(b)
+        pool, qkv = place(pool), place(qkv)
+        scales = None if scales is None else place(scales)
+        q, out, k, v = (place(torch.zeros(b.T, n * D, dtype=torch.bfloat16, device="cuda")) for n in (6, 6, 1, 1))
+        kw = dict(num_kv_heads=1, kv_scales=scales)
+        k3da.k3da_kv_append_qknorm(pool, qkv, table, lens, cu, b.positions.cuda(), b.q_w.cuda(), b.k_w.cuda(), q_out=q,
+                                   num_q_heads=6, **kw)
+        ws = k3da.alloc_chunk_workspace(b.T, b.R, 6, 1, b.stride)
+        k3da.k3da_chunk_attn(out, q, pool, table, lens, cu, num_q_heads=6, workspace=ws, **kw)
+        k3da.k3da_kv_gather(k, v, pool, table, lens, cu, **kw)
+        results.append([t.contiguous().view(torch.uint8).clone() for t in (pool, q, out, k, v)])
+    for x, y in zip(*results):
+        assert torch.equal(x, y)

@@ -62,6 +62,15 @@ def test_mixed_batches(seed, hq, hkv, cache):
     assert int(status) == 0
 
 
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hq,hkv", [(g, 1) for g in range(1, 17)] + [(33, 11), (64, 64), (64, 4)])
+def test_every_group_of_heads(hq, hkv, cache):
+    """Rows to a slot and to a small chunk by the heads that share a kv head."""
+    b = Batch([1, 130 // hkv + 3, 2, 17, 0, 3], [70, 10, 200, 63, 5, 129], hq, hkv, cache, pad=1, seed=hq, stride=WIDE)
+    out, lse = call(b)
+    check(b, out, lse)
+
+
 def test_items_whose_slots_end_apart():
     """The second slot of an item sees a tile more than the first, behind
     items of one slot, over and over."""
@@ -193,3 +202,33 @@ def test_two_captured_graphs_share_a_workspace():
         torch.cuda.synchronize()
         for (o, l), (x, y) in zip(outs, want):
             assert torch.equal(o.view(torch.int16), x.view(torch.int16)) and torch.equal(l, y)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_small_chunks_far_into_a_large_pool(cache):
+    """Byte offsets past 2^32 (codes: past 2^31), and in the appends and the
+    read-back of the same pages."""
+    b = Batch([1, 2], [200, 77], 24, 4, cache, seed=10)
+    pool, scales, qkv, table, lens, cu = dev(b)
+    pages = 90000 if cache == "bf16" else 100000
+    shift = pages - b.pages
+    big = torch.zeros(pages, 2, 4, 64, D * pool.element_size(), dtype=torch.uint8, device="cuda")
+    big[shift:] = pool.view(torch.uint8).view(b.pages, 2, 4, 64, -1)
+    big = big.view(pool.dtype)
+    if scales is not None:
+        large = torch.zeros(pages, 2, 4, 64, dtype=torch.uint8, device="cuda")
+        large[shift:] = scales.view(torch.uint8)
+        large = large.view(scales.dtype)
+    moved = torch.where((table >= 0) & (table < b.pages), table + shift, table)
+    d = big, None if scales is None else large, qkv, moved, lens, cu
+    out, lse = call(b, d=d)
+    check(b, out, lse)
+    k3da.k3da_kv_append(big, qkv, moved, lens, cu, num_q_heads=24, num_kv_heads=4, kv_scales=d[1])
+    k3da.k3da_kv_append(pool, qkv, table, lens, cu, num_q_heads=24, num_kv_heads=4, kv_scales=scales)
+    assert torch.equal(big[shift:].view(torch.uint8), pool.view(torch.uint8)) and not big[:shift].view(torch.uint8).any()
+    got = [torch.zeros(3, 4 * D, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    k3da.k3da_kv_gather(*got[:2], big, moved, lens, cu, num_kv_heads=4, kv_scales=d[1])
+    k3da.k3da_kv_gather(*got[2:], pool, table, lens, cu, num_kv_heads=4, kv_scales=scales)
+    assert torch.equal(got[0], got[2]) and torch.equal(got[1], got[3]) and got[0].any()
+    del big, d
+    torch.cuda.empty_cache()

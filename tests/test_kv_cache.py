@@ -293,3 +293,45 @@ def test_a_captured_append_and_gather_follow_rewritten_lengths():
     code, byte = quantise(b2.qkv.view(9, -1, D)[:, 24:].double())
     want = dequantise(code, byte).reshape(9, 2, 4 * D)
     assert torch.equal(k.cpu().double(), want[:, 0]) and torch.equal(v.cpu().double(), want[:, 1])
+
+
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hq,hkv,new", [(24, 4, [2000, 0, 3000, 1001]), (6, 1, [20011, 3]), (64, 64, [300, 157]), (64, 4, [900])])
+def test_a_long_append_is_its_pieces(hq, hkv, new, cache, norm):
+    """Many tokens a CTA against few: one call against calls of 200 tokens,
+    bit for bit, and what a gather reads back against what was written."""
+    ctx = [37, 5, 0, 640][:len(new)]
+    b = Batch(new, ctx, hq, hkv, cache, pad=2, seed=hq)
+    pool, scales, qkv, table, lens, cu = dev(b)
+    w = b.q_w.cuda(), b.k_w.cuda()
+    pos = b.positions.cuda()
+
+    def append(pool, scales, rows, table, lens, cu, pos, q):
+        if norm:
+            k3da.k3da_kv_append_qknorm(pool, rows, table, lens, cu, pos, *w, q_out=q, kv_scales=scales, **heads(b))
+        else:
+            k3da.k3da_kv_append(pool, rows, table, lens, cu, kv_scales=scales, **heads(b))
+
+    whole = pool.clone(), None if scales is None else scales.view(torch.uint8).clone().view(torch.float8_e8m0fnu)
+    qs = [torch.full((b.T, hq * D), 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    append(*whole, qkv, table, lens, cu, pos, qs[0])
+    for r, n in enumerate(new):
+        for i in range(0, n, 200):
+            m, at = min(200, n - i), b.cu[r] + i
+            append(pool, scales, qkv[at:at + m], table[r:r + 1], torch.tensor([ctx[r] + i], dtype=torch.int32, device="cuda"),
+                   torch.tensor([0, m], dtype=torch.int32, device="cuda"), pos[at:at + m], qs[1][at:at + m])
+    assert torch.equal(bits(whole[0]), bits(pool)) and torch.equal(bits(qs[0]), bits(qs[1]))
+    assert scales is None or torch.equal(bits(whole[1]), bits(scales))
+    k, v = (torch.full((b.T, hkv * D), 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k3da.k3da_kv_gather(k, v, pool, table, lens, cu, num_kv_heads=hkv, kv_scales=scales)
+    # Values as the cache's definition has them; V is raw in either form.
+    t, page, slot = (torch.tensor(x, device="cuda") for x in zip(*b.where()))
+    if cache == "bf16":
+        want = pool[page, :, :, slot]
+        assert torch.equal(want[:, 1].reshape(-1, hkv * D), qkv[:b.rows, (hq + hkv) * D:])
+    else:
+        code, byte = bits(pool).view(pool.shape)[page, :, :, slot], scales.view(torch.uint8)[page, :, :, slot]
+        want = (code.cpu().view(torch.float8_e4m3fn).double() * torch.exp2(byte.cpu().double() - 127.0)[..., None]).to(torch.bfloat16).cuda()
+    assert torch.equal(k[t], want[:, 0].reshape(-1, hkv * D)) and torch.equal(v[t], want[:, 1].reshape(-1, hkv * D))
+    assert (k[b.rows:] == 3).all() and (v[b.rows:] == 3).all()
