@@ -913,16 +913,16 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
 // ----------------------------------------------------------------- combine --
 //
 // Folds the partial results of the items that a cut of the line fell into,
-// in the order of their pieces.  CTA (x, y) takes rows [y * rows, (y + 1) *
-// rows) of the x-th such item of a pass (z): 16 threads a row (4 dims each) times `lanes`
-// piece lanes, lane i folding the pieces i, i + lanes, ...; one lane where
-// there are few pieces (a long chunk: many rows, two or three pieces), eight
-// where one item spreads over many CTAs.  A programmatic dependent of the
-// main kernel: its launch overlaps that kernel's end.
+// in the order of their pieces.  CTA (x, y) takes `rows` rows of the x-th such
+// item of a pass, the few-rows kernel's first (y < small_y): 16 threads a row
+// (4 dims each) times `lanes` piece lanes, lane i folding the pieces i,
+// i + lanes, ...; one lane where there are few pieces (a long chunk: many
+// rows, two or three pieces), eight where one item spreads over many CTAs.
 constexpr int kCombineThreads = 256;
 
 __global__ void __launch_bounds__(kCombineThreads)
-    k3da_chunk_combine_kernel(const __grid_constant__ ChunkParams first, const __grid_constant__ ChunkParams second, int rows) {
+    k3da_chunk_combine_kernel(const __grid_constant__ ChunkParams small, const __grid_constant__ ChunkParams large,
+                              int small_y, int small_rows, int large_rows) {
     __shared__ int votes[kCombineThreads / 32];
     __shared__ int owner;
     __shared__ Cut cut;
@@ -930,7 +930,9 @@ __global__ void __launch_bounds__(kCombineThreads)
     __shared__ float4 part[8][32];
     __shared__ float2 part_ml[8][2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const ChunkParams &p = blockIdx.z == 0 ? first : second;
+    const bool is_small = static_cast<int>(blockIdx.y) < small_y;
+    const ChunkParams &p = is_small ? small : large;
+    const int y = is_small ? blockIdx.y : blockIdx.y - small_y, rows = is_small ? small_rows : large_rows;
     let_next_start();
     wait_for_stream();
     // The x-th CTA that left an item unfinished.
@@ -965,7 +967,7 @@ __global__ void __launch_bounds__(kCombineThreads)
     const int slot_rows = p.tpt * p.G;
     for (int base = 0; base < rows; base += per_pass) {
         const int local = lanes == 8 ? tid >> 7 : tid >> 4;
-        const int rho = blockIdx.y * rows + base + local;  // the item's row, slot by slot
+        const int rho = y * rows + base + local;  // the item's row, slot by slot
         const int s = rho / kSlotRows, in_slot = rho % kSlotRows;
         const int token = s * p.tpt + in_slot / p.G;
         const bool valid = base + local < rows && rho < p.part_rows && in_slot < slot_rows && token < cut.tokens;
@@ -1150,15 +1152,20 @@ extern "C" int k3da_chunk_attn(void *out, float *lse, const void *q, int64_t q_r
     // 8.5 instead of 9.6 us).
     const long long line = keys + heads * (kSmallOverhead + 2 * prm.tpt + kSmallRows);
     if (!can_be_long && line < 2 * kMinSmallSlice) return K3DA_OK;
-    // Items a cut can fall into, rows one can have: a grid of about 1200
-    // CTAs over both.
+    // Items a cut can fall into, rows one can have: a grid of about 1200 CTAs
+    // over the long chunks' (8 x 8 tokens over long contexts: 102.5 us, with
+    // half as many 107.5, with twice as many 102), 600 over the others'.
     const long long items =
         ((static_cast<long long>(num_tokens) + 2 * prm.tpt - 1) / (2 * prm.tpt) + num_requests) * num_kv_heads;
     const unsigned gx = static_cast<unsigned>(items < kCtas ? items : kCtas);
-    const long long bound = num_tokens <= prm.tpt ? num_tokens * prm.G : 2 * kSlotRows;
-    int rows = static_cast<int>((bound * gx + 1215) / 1216);
-    rows = rows < 2 ? 2 : rows;
-    return launch_beside(k3da_chunk_combine_kernel,
-                         dim3(gx, static_cast<unsigned>((bound + rows - 1) / rows), can_be_long && !one_kernel ? 2 : 1),
-                         kCombineThreads, 0, st, one_kernel ? prm : small, prm, rows);
+    auto rows_of = [&](int bound, int ctas) {
+        const int rows = static_cast<int>((bound * gx + ctas - 1) / ctas);
+        return rows < 2 ? 2 : rows;
+    };
+    const int rows_bound = num_tokens <= prm.tpt ? num_tokens * prm.G : 2 * kSlotRows;
+    const int small_rows = rows_of(kSmallRows, 608), rows = rows_of(rows_bound, 1216);
+    const int small_y = one_kernel ? 0 : (kSmallRows + small_rows - 1) / small_rows;
+    const int y = can_be_long ? (rows_bound + rows - 1) / rows : 0;
+    return launch_beside(k3da_chunk_combine_kernel, dim3(gx, static_cast<unsigned>(small_y + y)), kCombineThreads, 0, st,
+                         small, prm, small_y, small_rows, rows);
 }
