@@ -271,16 +271,23 @@ __device__ __forceinline__ void merge_piece(const ChunkParams &p, const Piece &i
 #pragma unroll 1
     for (int rho = lane >> 2; rho < it.tokens * p.G; rho += 8) {
         // (Unrolled no further: the page loops want the instruction cache.)
-        float mt = -INFINITY;
+        float mt = -INFINITY, zt = -INFINITY;
 #pragma unroll 4
-        for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, merge_s[w * kSmallRows + rho].x);
+        for (int w = 0; w < kWarps; ++w) {
+            mt = fmaxf(mt, merge_s[w * kSmallRows + rho].x);
+            if (QUANT) zt = fmaxf(zt, merge_s[w * kSmallRows + rho].z);
+        }
         const float me = mt == -INFINITY ? 0.f : mt;
+        // With codes the O are folded at the largest of their references: the
+        // way from there to the scores' maximum is as far as V's scales reach,
+        // past what one factor can hold, and comes last, in two.
+        const float ze = !QUANT ? me : zt == -INFINITY ? 0.f : zt;
         float lt = 0.f, v[16] = {};
 #pragma unroll 2
         for (int w = 0; w < kWarps; ++w) {
             const float4 st = merge_s[w * kSmallRows + rho];
             const float4 *part = reinterpret_cast<const float4 *>(merge_o + (w * kSmallRows + rho) * kORow + dim0);
-            const float f = exp2_approx(st.z - me);
+            const float f = exp2_approx(st.z - ze);
             lt += st.y * exp2_approx(st.x - me);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -294,6 +301,11 @@ __device__ __forceinline__ void merge_piece(const ChunkParams &p, const Piece &i
         const float norm = whole ? 1.f / lt : 1.f;
 #pragma unroll
         for (int q = 0; q < 16; ++q) v[q] = lt == 0.f ? 0.f : v[q] * norm;
+        if (QUANT) {
+            const float half_way = exp2_approx(0.5f * (ze - me));
+#pragma unroll
+            for (int q = 0; q < 16; ++q) v[q] = v[q] * half_way * half_way;
+        }
         const int token = rho / p.G;
         if (hidden) {
             const int least = keys_seen(p, it.ctx, it.n, 0), sees = keys_seen(p, it.ctx, it.n, token);
