@@ -15,10 +15,12 @@
 // conversion for two), K's scale multiplies a finished score, and V's goes
 // into the weight: w = 2^(s + e - m'), with a reference m' beside the maximum
 // m of s that the sum keeps.  As a rule V's exponents e of a piece lie close
-// together, and m' = m + max e, so that one exp serves sum and weight; else
-// m' is the running maximum of s + e.  Both are exponents, so scales of any
-// size meet no range.  q is scaled by a power of two into half precision's
-// range (exact but for dims 2^-39 below the row's largest).
+// together, and m' = m + max e - 15, so that one exp serves sum and weight;
+// else m' is 15 below the running maximum of s + e.  (15: half precision then
+// holds weights down to 2^-39 of the largest.)  Both are exponents, so scales
+// of any size meet no range.  q is scaled by a power of two into half
+// precision's range (exact but for dims 2^-31 below the row's largest, which
+// lose bits, and are gone 2^-39 below).
 //
 // Measured (64 decoded tokens over 8000 each, 24/4 heads): e4m3 57 us, 4.7
 // TB/s of cache, where the long chunks' kernel takes 144; bf16 91 us, 5.7
@@ -28,7 +30,7 @@
 // spill (8 x 2 tokens over 60000, 16/2 heads, e4m3).
 //
 // Rounding: scores, statistics, O and partial results are fp32; weights are
-// rounded once (bf16, or half precision for codes), the output once.
+// rounded once (bf16, or half precision for codes: see kHead), the output once.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -51,9 +53,16 @@ using namespace sm103;
 constexpr int page_warps(bool quant) { return quant ? 11 : 8; }
 constexpr int kRing = 4;     // pieces published ahead
 constexpr int kRecords = 8;  // pieces whose non-finite records are alive at once
+// With codes, the largest weight is 2^kHead in half precision (its largest
+// number is 65504): a weight is off by 2^-12 of itself, or, where half's
+// numbers are subnormal, by 2^-25 of 2^-kHead of the reference, 2^-40.  Keys
+// that are alike all err one way, so it is their sum that counts: with the
+// reference at 1 instead, 60000 keys of 2^-15.3 next to a key of 1 were lost,
+// 8% of the output.
+constexpr int kHead = 15;
 // Spread of V's exponents up to which one reference exponent serves a piece's
-// keys: a weight then is off by 2^-25 of a reference that is at most 2^10
-// above the largest, 2^-15 of that, where a half's own rounding is 2^-12.
+// keys.  The reference then is at most 2^10 above the largest weight, and n
+// keys lose n 2^-30 of that at most: 2^-13 of 131072.
 constexpr int kNear = 10;
 constexpr int kORow = kD + 4;  // floats of a row in the merge room (the pad spreads rows over the banks)
 
@@ -363,7 +372,7 @@ struct Rows {
     float scale[NT][2];
     int sees[NT][2];
     float m[NT][2], l[NT][2];
-    float mo[NT][2];   // reference of O: m, or with codes the maximum of s + e
+    float mo[NT][2];   // reference of O: m, or with codes kHead below the maximum of s + e
     float o[NT][4][4];
     // Codes: while V's exponents in the piece are within kNear of one another.
     bool near;
@@ -550,8 +559,8 @@ __device__ __forceinline__ bool take_page(Rows<NT> &R, Loader<QUANT> &load, cons
                 for (int h = 0; h < 2; ++h) {
                     u64 w = exp2_f32x2(add_f32x2(pack_f32x2(s[nt][i][2 * h], s[nt][i][2 * h + 1]), nb));
                     sum = add_f32x2(sum, w);
-                    if (QUANT) {  // 2^(e - e_hi)
-                        const float f = __uint_as_float((vs[16 * i + 8 * h + kg] + 127u - R.e_hi) << 23);
+                    if (QUANT) {  // 2^(e - e_hi + kHead)
+                        const float f = __uint_as_float((vs[16 * i + 8 * h + kg] + 127u + kHead - R.e_hi) << 23);
                         w = mul_f32x2(w, pack_f32x2(f, f));
                     }
                     const float2 v = unpack_f32x2(w);
@@ -564,7 +573,7 @@ __device__ __forceinline__ bool take_page(Rows<NT> &R, Loader<QUANT> &load, cons
             if (QUANT) {
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const float mn = R.m[nt][c] + static_cast<float>(R.e_hi - 127);
+                    const float mn = R.m[nt][c] + static_cast<float>(R.e_hi - 127 - kHead);
                     fo[nt][c] = exp2_approx(R.mo[nt][c] - (mn == -INFINITY ? 0.f : mn));
                     R.mo[nt][c] = mn;
                 }
@@ -588,7 +597,7 @@ __device__ __forceinline__ bool take_page(Rows<NT> &R, Loader<QUANT> &load, cons
                             if (v != -INFINITY) v += exponent_of(vs[16 * i + 8 * h + kg]);
                             top_o = fmaxf(top_o, v);
                         }
-                    const float mn = fmaxf(R.mo[nt][c], keys_max(top_o));
+                    const float mn = fmaxf(R.mo[nt][c], keys_max(top_o) - kHead);
                     base_o = mn == -INFINITY ? 0.f : mn;
                     fo[nt][c] = exp2_approx(R.mo[nt][c] - base_o);
                     R.mo[nt][c] = mn;
