@@ -15,7 +15,7 @@ ROOT = os.path.dirname(PKG)
 SOURCES = [os.path.join(PKG, "csrc", f) for f in
            ("k3da.cu", "k3da_norm_rope.cu", "k3da_cache.cu", "k3da_chunk.cu", "k3da_chunk_small.cu")]
 HEADERS = [os.path.join(ROOT, "include", "k3da.h")] + [os.path.join(PKG, "csrc", f) for f in
-           ("rope_table.h", "cache_common.cuh", "chunk_plan.cuh", "sm103.cuh", "tensor_maps.h")]
+           ("rope_table.h", "cache_common.cuh", "chunk_cut.h", "chunk_plan.cuh", "sm103.cuh", "tensor_maps.h")]
 LIB = os.path.join(PKG, "libk3da.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

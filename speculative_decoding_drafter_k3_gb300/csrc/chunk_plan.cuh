@@ -8,13 +8,13 @@
 #include <stdint.h>
 
 #include "cache_common.cuh"
+#include "chunk_cut.h"
 #include "k3da.h"
 
 namespace k3da_chunk {
 
 using namespace k3da_cache;
 
-constexpr int kCtas = 152;         // slices of the line at most: one CTA an SM
 constexpr int kTile = 128;         // keys of a tile: two pages
 constexpr int kSlotRows = 128;     // query rows of a slot
 // An item's fixed cost (its first loads, its epilogue or fold), and the
@@ -55,18 +55,6 @@ struct ChunkParams {
 constexpr int kSmallRows = 16;
 enum { kLong, kSmall, kAll };
 
-// What a CTA leaves for the combine kernel.  part 0: the piece it began with
-// belongs to an item begun before; part 1: the item it ended with goes on in
-// later CTAs, up to `last`.
-struct Cut {
-    int has[2];
-    int row;     // first row of the item that goes on
-    int tokens;  // its tokens
-    int head;    // its kv head
-    int last;
-    int pad[2];
-};
-static_assert(sizeof(Cut) == 32, "cuts are 32 bytes");
 constexpr size_t kCutBytes = 8192;
 static_assert(kCtas * sizeof(Cut) <= kCutBytes, "room for the cuts");
 // Workspace of a pass whose partial results have `rows` rows.

@@ -958,7 +958,7 @@ __global__ void __launch_bounds__(kCombineThreads)
     }
     __syncthreads();
     const int a = owner;
-    if (a < 0) return;
+    if (a < 0 || !cut_fits(cut, a, p.T, p.Hkv, 2 * p.tpt)) return;
     const int pieces = cut.last - a + 1;
     const int lanes = pieces > 8 ? 8 : 1;
     const int dim = tid & 15;

@@ -841,7 +841,12 @@ __global__ void __launch_bounds__(Smem<QUANT>::kThreads, 1)
                 ++published;
             }
             if (n == published - 1) break;  // the end's mark
-            if (!warp_wait(bar_left, n & 1, abort_flag, p.status)) break;
+            if (!warp_wait(bar_left, n & 1, abort_flag, p.status)) {
+                // The combine reads every CTA's cut: where this one's is not
+                // known yet, none.
+                if (lane == 0 && more) p.cuts[blockIdx.x] = Cut{};
+                break;
+            }
             merge_piece<QUANT>(p, pieces[n % kRing], merge_o, merge_s, recs, lane);
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_merged);
