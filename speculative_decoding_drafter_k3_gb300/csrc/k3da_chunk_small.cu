@@ -307,14 +307,10 @@ __device__ __forceinline__ void merge_piece(const ChunkParams &p, const Piece &i
                 v[4 * q + 3] += x.w * f;
             }
         }
-        const float norm = whole ? 1.f / lt : 1.f;
+        const float half_way = QUANT ? exp2_approx(0.5f * (ze - me)) : 1.f;
+        const float norm = (whole ? 1.f / lt : 1.f) * half_way;
 #pragma unroll
-        for (int q = 0; q < 16; ++q) v[q] = lt == 0.f ? 0.f : v[q] * norm;
-        if (QUANT) {
-            const float half_way = exp2_approx(0.5f * (ze - me));
-#pragma unroll
-            for (int q = 0; q < 16; ++q) v[q] = v[q] * half_way * half_way;
-        }
+        for (int q = 0; q < 16; ++q) v[q] = lt == 0.f ? 0.f : QUANT ? v[q] * norm * half_way : v[q] * norm;
         const int token = rho / p.G;
         if (hidden) {
             const int least = keys_seen(p, it.ctx, it.n, 0), sees = keys_seen(p, it.ctx, it.n, token);
