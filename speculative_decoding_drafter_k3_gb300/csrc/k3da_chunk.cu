@@ -160,6 +160,9 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     return d;
 }
 
+// True where every lane of the (converged) warp says so.
+__device__ __forceinline__ bool agreed(bool mine) { return __all_sync(kFull, mine); }
+
 template <bool QUANT>
 __global__ void __launch_bounds__(threads_of(QUANT), 1)
     k3da_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap q_map,
@@ -327,7 +330,7 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
         int merges = 0;  // alternate pieces with tiles for both slots so far
         for (int n = 0; alive; ++n) {
             const Piece &it = pieces[n % kRing];
-            if (!mbar_wait(bar_piece + 8 * (n % kRing), (n / kRing) & 1, abort_flag, p.status)) break;
+            if (!agreed(mbar_wait(bar_piece + 8 * (n % kRing), (n / kRing) & 1, abort_flag, p.status))) break;
             if (it.row < 0) break;
             const int alt = it.alt;
             const int token = (alt ? 0 : s * p.tpt) + ti;  // in the item
@@ -341,7 +344,7 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
             const int shared_end = alt ? 0 : it.end(0);
             uint32_t buf = mine ? static_cast<uint32_t>(it.step_of(s, from)) % kBufs : 0;
             for (int t = from; t < t_end; t += step) {
-                if (!mbar_wait(bar_sfull + 8 * (s * kBufs + turn), round, abort_flag, p.status)) {
+                if (!agreed(mbar_wait(bar_sfull + 8 * (s * kBufs + turn), round, abort_flag, p.status))) {
                     alive = false;
                     break;
                 }
@@ -417,7 +420,8 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
                     // A row's two threads scale one half of its O each, once
                     // the slot's last P V is complete.
                     const uint32_t last = k - 2;
-                    if (!mbar_wait(bar_pvdone + 8 * (s * kBufs + last % kBufs), last / kBufs & 1, abort_flag, p.status)) {
+                    if (!agreed(mbar_wait(bar_pvdone + 8 * (s * kBufs + last % kBufs), last / kBufs & 1,
+                                                           abort_flag, p.status))) {
                         alive = false;
                         break;
                     }
@@ -466,7 +470,8 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
             // ------------------------------------------------- epilogue --
             if (mine) {
                 const uint32_t last = k - 1;
-                if (!mbar_wait(bar_pvdone + 8 * (s * kBufs + last % kBufs), last / kBufs & 1, abort_flag, p.status)) break;
+                if (!agreed(mbar_wait(bar_pvdone + 8 * (s * kBufs + last % kBufs), last / kBufs & 1, abort_flag, p.status)))
+                    break;
                 xl[u * kSlotRows + rho] = l;
                 if (s == 1 && page == 0) xm[rho] = m;
             }
@@ -484,14 +489,14 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
             if (mine) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_sums + 8 * s);
-                if (!mbar_wait(bar_sums + 8 * s, sums & 1, abort_flag, p.status)) break;
+                if (!agreed(mbar_wait(bar_sums + 8 * s, sums & 1, abort_flag, p.status))) break;
                 ++sums;
                 l = xl[2 * s * kSlotRows + rho] + xl[(2 * s + 1) * kSlotRows + rho];
             }
             const bool both = alt && it.from(1) < it.end(1);
             float wa = 1.f, wb = 0.f;
             if (both) {
-                if (!mbar_wait(bar_xch, merges & 1, abort_flag, p.status)) break;
+                if (!agreed(mbar_wait(bar_xch, merges & 1, abort_flag, p.status))) break;
                 ++merges;
                 const float mb = xm[rho], lb = xl[2 * kSlotRows + rho] + xl[3 * kSlotRows + rho];
                 const float mt = fmaxf(m, mb);
@@ -581,7 +586,7 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
         const bool issuer = elect_one();
         for (int n = 0; alive; ++n) {
             const Piece &it = pieces[n % kRing];
-            if (!mbar_wait(bar_piece + 8 * (n % kRing), (n / kRing) & 1, abort_flag, p.status)) break;
+            if (!agreed(mbar_wait(bar_piece + 8 * (n % kRing), (n / kRing) & 1, abort_flag, p.status))) break;
             if (it.row < 0) break;
             const int t0 = it.t0, t1 = it.t1, pages = min((it.limit + kP - 1) / kP, 2 * t1), r = it.r, h = it.h;
             // 32 pages at a time, one a lane: row of its K, -1 where the id
@@ -604,8 +609,8 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
                 for (int part = 0; part < (QUANT ? 1 : 2); ++part) {
                     const int ring = QUANT ? L::kRaw : part ? L::kVs : L::kKs, x = issued[part], st = x % ring;
                     const uint32_t full = (QUANT ? bar_rfull : part ? bar_vfull : bar_kfull) + 8 * st;
-                    if (!mbar_wait((QUANT ? bar_rempty : part ? bar_empty : bar_kempty) + 8 * st, ((x / ring) & 1) ^ 1,
-                                   abort_flag, p.status)) {
+                    if (!agreed(mbar_wait((QUANT ? bar_rempty : part ? bar_empty : bar_kempty) + 8 * st, ((x / ring) & 1) ^ 1,
+                                          abort_flag, p.status))) {
                         alive = false;
                         break;
                     }
@@ -679,19 +684,21 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
         const uint32_t tiles = smem_u32(smem + (is_qk ? L::kKv : L::kV));
         for (int n = 0; alive; ++n) {
             const Piece &it = pieces[n % kRing];
-            if (!mbar_wait(bar_piece + 8 * (n % kRing), (n / kRing) & 1, abort_flag, p.status)) break;
+            if (!agreed(mbar_wait(bar_piece + 8 * (n % kRing), (n / kRing) & 1, abort_flag, p.status))) break;
             if (it.row < 0) break;
             const int t0 = it.t0, t1 = it.t1, alt = it.alt;
             const int from = it.from(s), t_end = it.end(s), step = it.step();
             const int half = it.q & 1;
             const uint64_t qd = desc_sw128(smem_u32(smem + L::kQ) + half * L::kQBytes);
             if (is_qk && t0 < t1) {
-                if ((!alt || half == 0) && !mbar_wait(bar_qfull, it.q >> 1 & 1, abort_flag, p.status)) break;
-                if ((!alt || half == 1) && !mbar_wait(bar_qfull + 8, it.q >> 2 & 1, abort_flag, p.status)) break;
+                if ((!alt || half == 0) && !agreed(mbar_wait(bar_qfull, it.q >> 1 & 1, abort_flag, p.status))) break;
+                if ((!alt || half == 1) && !agreed(mbar_wait(bar_qfull + 8, it.q >> 2 & 1, abort_flag, p.status))) break;
             }
             items += from < t_end;
             int next = from;  // the slot's next tile
             uint32_t i = it.base;
+            // (Nothing in this loop is an operation of the whole warp: its
+            // lanes agree behind it.)
             for (int t = t0; t < t1; ++t) {
                 // Every tile in turn, another slot's too: a phase is never
                 // waited for before the one before it is known to be over.
@@ -753,6 +760,7 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
                     ph ^= 1;
                 }
             }
+            alive = agreed(alive);
             if (!alive) break;
             if (is_qk && t0 < t1) {
                 // Q is free once the products that read it are complete.
@@ -779,7 +787,7 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
         uint32_t ph = 0, rph = 0;  // rounds of the stages, mod 2
         for (int n = 0; alive; ++n) {
             const Piece &it = pieces[n % kRing];
-            if (!mbar_wait(bar_piece + 8 * (n % kRing), (n / kRing) & 1, abort_flag, p.status)) break;
+            if (!agreed(mbar_wait(bar_piece + 8 * (n % kRing), (n / kRing) & 1, abort_flag, p.status))) break;
             if (it.row < 0) break;
             const int piece = it.seq, limit = it.limit, t1 = it.t1;
             Records *rec = recs + piece % kRecords;
@@ -789,11 +797,9 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
                 uint8_t *vt = smem + L::kV + st * L::kTileBytes;
                 if (QUANT) {
                     const uint8_t *raw = smem + L::kRawOff + rs * L::kRawBytes;
-                    if (!mbar_wait(bar_rfull + 8 * rs, rph, abort_flag, p.status) ||
-                        !mbar_wait(bar_empty + 8 * st, ph ^ 1, abort_flag, p.status)) {
-                        alive = false;
-                        break;
-                    }
+                    alive = agreed(mbar_wait(bar_rfull + 8 * rs, rph, abort_flag, p.status) &&
+                                   mbar_wait(bar_empty + 8 * st, ph ^ 1, abort_flag, p.status));
+                    if (!alive) break;
                     // 1024 pieces of 16 codes (K's 512, then V's), four a
                     // row; loads of a few of them first.
                     constexpr int kStep = 32 * kPrepWarps, kBatch = 3;
@@ -845,10 +851,8 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
                     }
                     fence_proxy_async();
                 } else {
-                    if (!mbar_wait(bar_vfull + 8 * st, ph, abort_flag, p.status)) {
-                        alive = false;
-                        break;
-                    }
+                    alive = agreed(mbar_wait(bar_vfull + 8 * st, ph, abort_flag, p.status));
+                    if (!alive) break;
                     if ((t + 1) * static_cast<long long>(kTile) > least) {
                         for (int row = tid; row < kTile; row += 32 * kPrepWarps) {
                             const int key = t * kTile + row;

@@ -66,6 +66,9 @@ __device__ __forceinline__ unsigned long long global_ns() {
 // Gives up when another warp of the CTA has (abort flag) or after
 // kWaitLimitNs, raising the flag and the TIMEOUT status bit.  The caller then
 // leaves its loop, so that every warp reaches the CTA's last barrier.
+// Each lane's own answer: lanes of a warp may differ where a wait gives up, so
+// a warp agrees (in a vote) before it leaves a loop or comes to an operation
+// of all its lanes.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, int32_t *status) {
     if (mbar_try_wait(bar, parity)) return true;
     const unsigned long long t0 = global_ns();
