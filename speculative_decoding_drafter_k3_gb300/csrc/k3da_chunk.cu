@@ -160,6 +160,13 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     return d;
 }
 
+// Waits, with a limit, until a load that was issued has arrived.
+__device__ __forceinline__ void land(uint32_t full, uint32_t parity) {
+    const unsigned long long t0 = global_ns();
+    while (!mbar_try_wait(full, parity) && global_ns() - t0 < kWaitLimitNs) {
+    }
+}
+
 // True where every lane of the (converged) warp says so.
 __device__ __forceinline__ bool agreed(bool mine) { return __all_sync(kFull, mine); }
 
@@ -306,15 +313,11 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
                 }
             }
             p.cuts[blockIdx.x] = cut;
-            // Loads in flight land before the CTA leaves (a wait gave up).
-            if (!alive) {
-                for (int s = 0; s < 2; ++s) {
-                    const uint32_t n_fills = s ? fills[1] : fills[0];
-                    const unsigned long long t0 = global_ns();
-                    while (n_fills > 0 && !mbar_try_wait(bar_qfull + 8 * s, (n_fills - 1) & 1) &&
-                           global_ns() - t0 < kWaitLimitNs) {
-                    }
-                }
+            // Loads in flight land before the CTA leaves: the warps that use
+            // them may give up, now or later.
+            for (int s = 0; s < 2; ++s) {
+                const uint32_t n_fills = s ? fills[1] : fills[0];
+                if (n_fills > 0) land(bar_qfull + 8 * s, (n_fills - 1) & 1);
             }
         }
         __syncwarp();
@@ -658,18 +661,12 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
             if (!alive) break;
             if (lane == 0) mbar_arrive(bar_pdone + 8 * (n % kRing));
         }
-        // Loads in flight land before the CTA leaves (a wait gave up).
-        if (*abort_flag) {
-            auto land = [&](uint32_t full, int ring, int x) {
-                for (int j = x > ring ? x - ring : 0; j < x; ++j) {
-                    const unsigned long long t0 = global_ns();
-                    while (!mbar_try_wait(full + 8 * (j % ring), (j / ring) & 1) && global_ns() - t0 < kWaitLimitNs) {
-                    }
-                }
-            };
-            land(QUANT ? bar_rfull : bar_kfull, QUANT ? L::kRaw : L::kKs, issued[0]);
-            if (!QUANT) land(bar_vfull, L::kVs, issued[1]);
-        }
+        // Loads in flight land before the CTA leaves, as the scheduler's do.
+        auto land_ring = [&](uint32_t full, int ring, int x) {
+            for (int j = x > ring ? x - ring : 0; j < x; ++j) land(full + 8 * (j % ring), (j / ring) & 1);
+        };
+        land_ring(QUANT ? bar_rfull : bar_kfull, QUANT ? L::kRaw : L::kKs, issued[0]);
+        if (!QUANT) land_ring(bar_vfull, L::kVs, issued[1]);
     } else if (warp < kPrepWarp) {
         // ------------------------------------------------------ products --
         // One warp issues Q K^T of every step, one P V of each slot.

@@ -71,3 +71,21 @@ def test_a_missing_vote_behind_the_products_is_seen():
     at = src.index("for (int t = t0; t < t1; ++t) {", src.index("next += step") - 3000)
     i, _ = span(src, at, "{", "}")
     assert waits_outside(src[:i + 1] + " __syncwarp(); " + src[i + 1:])
+
+
+def test_loads_land_whatever_gives_up_when():
+    """A copy that is still on its way must not outlive its CTA, also where a
+    warp gives up after the one that issued the copy is done: what waits for
+    the last copies stands behind the issuers' loops, under no condition on
+    who gave up so far."""
+    src = read("k3da_chunk.cu")
+    assert "if (*abort_flag)" not in src and "if (!alive) {" not in src
+    scheduler = src[src.index("Walk walk;"):src.index("const int u = warp >> 2")]
+    tail = scheduler[scheduler.index("p.cuts[blockIdx.x] = cut;"):]
+    assert re.search(r"for \(int s = 0; s < 2; \+\+s\) \{[^{}]*if \(n_fills > 0\) land\(bar_qfull", tail)
+    a, b = span(src, src.index("for (int n = 0; alive; ++n) {", src.index("int issued[2]")), "{", "}")
+    behind = src[b:src.index("} else if (warp < kPrepWarp)")]
+    assert "land_ring(QUANT ? bar_rfull : bar_kfull" in behind and "if (!QUANT) land_ring(bar_vfull" in behind
+    small = read("k3da_chunk_small.cu")
+    a, b = span(small, small.index("for (int n = 0;; ++n) {", small.index("load.begin(warp")), "{", "}")
+    assert small[b:].lstrip().startswith("load.drain();")
