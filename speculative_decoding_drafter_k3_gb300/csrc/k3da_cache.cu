@@ -14,7 +14,8 @@
 // back as NaN, and no other row is touched.
 //
 // Rounding: bf16 inputs are widened exactly, norm and RoPE run in fp32, and
-// each value is rounded once, to bf16 or (from fp32) to its e4m3 code.
+// each value is rounded once, to bf16 or (from fp32) to its e4m3 code.  What
+// goes into a bf16 cache as it is keeps its bits, those of a NaN too.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -41,6 +42,11 @@ __device__ __forceinline__ void store32(uint4 *dst, uint4 a, uint4 b, bool whole
         dst[0] = a;
         dst[1] = b;
     }
+}
+
+// Two bf16 that were widened, as they were.
+__device__ __forceinline__ uint32_t bits2(float lo, float hi) {
+    return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
 }
 
 // -------------------------------------------------------------- quantising --
@@ -273,12 +279,23 @@ __global__ void __launch_bounds__(kAppendThreads) k3da_kv_append_kernel(const __
         if (dst != nullptr) {
             const bool whole = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
             uint4 w[4];
+            if (!NORM || (!QUANT && h >= p.Hq + p.Hkv)) {
+                // As they came, a NaN's bits too: rounding would give them up.
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                w[c] = make_uint4(pack2(lo[8 * c], lo[8 * c + 1]), pack2(lo[8 * c + 2], lo[8 * c + 3]),
-                                  pack2(lo[8 * c + 4], lo[8 * c + 5]), pack2(lo[8 * c + 6], lo[8 * c + 7]));
-                w[2 + c] = make_uint4(pack2(hi[8 * c], hi[8 * c + 1]), pack2(hi[8 * c + 2], hi[8 * c + 3]),
-                                      pack2(hi[8 * c + 4], hi[8 * c + 5]), pack2(hi[8 * c + 6], hi[8 * c + 7]));
+                for (int c = 0; c < 2; ++c) {
+                    w[c] = make_uint4(bits2(lo[8 * c], lo[8 * c + 1]), bits2(lo[8 * c + 2], lo[8 * c + 3]),
+                                      bits2(lo[8 * c + 4], lo[8 * c + 5]), bits2(lo[8 * c + 6], lo[8 * c + 7]));
+                    w[2 + c] = make_uint4(bits2(hi[8 * c], hi[8 * c + 1]), bits2(hi[8 * c + 2], hi[8 * c + 3]),
+                                          bits2(hi[8 * c + 4], hi[8 * c + 5]), bits2(hi[8 * c + 6], hi[8 * c + 7]));
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    w[c] = make_uint4(pack2(lo[8 * c], lo[8 * c + 1]), pack2(lo[8 * c + 2], lo[8 * c + 3]),
+                                      pack2(lo[8 * c + 4], lo[8 * c + 5]), pack2(lo[8 * c + 6], lo[8 * c + 7]));
+                    w[2 + c] = make_uint4(pack2(hi[8 * c], hi[8 * c + 1]), pack2(hi[8 * c + 2], hi[8 * c + 3]),
+                                          pack2(hi[8 * c + 4], hi[8 * c + 5]), pack2(hi[8 * c + 6], hi[8 * c + 7]));
+                }
             }
             store32(dst + 2 * hp, w[0], w[1], whole);
             store32(dst + 4 + 2 * hp, w[2], w[3], whole);

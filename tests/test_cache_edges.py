@@ -1,0 +1,49 @@
+"""The cache calls at the edges of what their documentation allows (GPU)."""
+import pytest
+import torch
+
+import speculative_decoding_drafter_k3_gb300 as k3da
+from cache_cases import Batch, D
+from test_chunk_attn import dev
+from test_kv_cache import bits, expected_plain, heads
+
+pytestmark = pytest.mark.gpu
+
+
+def with_odd_bits(b):
+    """NaN of both signs with payloads, infinities, zeros, subnormal numbers
+    among the rows."""
+    odd = [0x7F81, 0xFF81, 0x7FC0, 0xFFC0, 0x7FFF, 0xFFFF, 0x7FA5, 0x7F80, 0xFF80, 0x8000, 0x0001, 0x807F]
+    raw = b.qkv.view(torch.int16)
+    g = torch.Generator().manual_seed(5)
+    for x in odd:
+        at = torch.randint(0, raw.numel(), (200,), generator=g)
+        raw.view(-1)[at] = x - 0x10000 if x >= 0x8000 else x
+    return b
+
+
+@pytest.mark.parametrize("hq,hkv", [(6, 1), (24, 4)])
+def test_a_plain_append_copies_every_bit(hq, hkv):
+    b = with_odd_bits(Batch([60, 3, 200], [5, 64, 1000], hq, hkv, "bf16", 1, seed=41))
+    pool, _, qkv, table, lens, cu = dev(b)
+    k3da.k3da_kv_append(pool, qkv, table, lens, cu, **heads(b))
+    want, _ = expected_plain(b)
+    assert torch.equal(bits(pool.cpu()), bits(want))
+    k, v = (torch.zeros(b.T, hkv * D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k3da.k3da_kv_gather(k, v, pool, table, lens, cu, num_kv_heads=hkv)
+    assert torch.equal(bits(k[:b.rows]), bits(qkv[:b.rows, hq * D:(hq + hkv) * D]))
+    assert torch.equal(bits(v[:b.rows]), bits(qkv[:b.rows, (hq + hkv) * D:]))
+
+
+@pytest.mark.parametrize("hq,hkv", [(6, 1), (24, 4)])
+def test_append_qknorm_copies_every_bit_of_v(hq, hkv):
+    """The norm+RoPE cell, then a plain append, with NaN in V."""
+    b = with_odd_bits(Batch([60, 3], [5, 64], hq, hkv, "bf16", 1, seed=42))
+    b.qkv[:, :(hq + hkv) * D] = 1.5
+    pool, _, qkv, table, lens, cu = dev(b)
+    two = pool.clone()
+    args = b.positions.cuda(), b.q_w.cuda(), b.k_w.cuda()
+    k3da.k3da_kv_append_qknorm(pool, qkv, table, lens, cu, *args, **heads(b))
+    cell = k3da.k3da_qk_norm_rope(qkv.clone(), *args, **heads(b))
+    k3da.k3da_kv_append(two, cell, table, lens, cu, **heads(b))
+    assert torch.equal(bits(pool), bits(two))
