@@ -54,6 +54,13 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
+// A runtime call failed: its error is taken back from the thread, where the
+// library's other calls would find it behind launches of their own.
+inline int cuda_failed() {
+    cudaGetLastError();
+    return K3DA_ECUDA;
+}
+
 // Launches `kernel` as a programmatic dependent: it may start before the
 // kernel in front of it on the stream is complete, and waits for that itself
 // (wait_for_stream), before it reads or writes anything or, where it only has
@@ -72,7 +79,7 @@ inline int launch_beside(void (*kernel)(Params...), dim3 grid, int threads, int 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = attr;
     lc.numAttrs = 1;
-    return cudaLaunchKernelEx(&lc, kernel, args...) == cudaSuccess ? K3DA_OK : K3DA_ECUDA;
+    return cudaLaunchKernelEx(&lc, kernel, args...) == cudaSuccess ? K3DA_OK : cuda_failed();
 }
 
 inline bool aligned_to(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }

@@ -1040,7 +1040,7 @@ __global__ void __launch_bounds__(kCombineThreads)
 template <bool QUANT>
 int launch_kernel(const CUtensorMap &kv_map, const CUtensorMap &q_map, const ChunkParams &prm, cudaStream_t st) {
     if (!allow_smem<QUANT>(reinterpret_cast<const void *>(k3da_chunk_kernel<QUANT>), Smem<QUANT>::kBytes))
-        return K3DA_ECUDA;
+        return cuda_failed();
     return launch_beside(k3da_chunk_kernel<QUANT>, dim3(kCtas), threads_of(QUANT), Smem<QUANT>::kBytes, st, kv_map,
                          q_map, prm);
 }
@@ -1048,7 +1048,7 @@ int launch_kernel(const CUtensorMap &kv_map, const CUtensorMap &q_map, const Chu
 int launch_long(const ChunkParams &prm, const void *q, const void *kv_pool, bool quant, cudaStream_t st) {
     const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     CUtensorMap kv_map, q_map;
-    if (encode == nullptr || !pool_map(encode, &kv_map, kv_pool, prm.num_pages, prm.Hkv, quant, !quant)) return K3DA_ECUDA;
+    if (encode == nullptr || !pool_map(encode, &kv_map, kv_pool, prm.num_pages, prm.Hkv, quant, !quant)) return cuda_failed();
     const cuuint64_t dims[3] = {kD, static_cast<cuuint64_t>(prm.Hq), static_cast<cuuint64_t>(prm.T)};
     const cuuint64_t strides[2] = {kD * 2, static_cast<cuuint64_t>(prm.q_stride) * 2};
     const cuuint32_t box[3] = {kD, static_cast<cuuint32_t>(prm.G), static_cast<cuuint32_t>(prm.tpt)};
@@ -1056,7 +1056,7 @@ int launch_long(const ChunkParams &prm, const void *q, const void *kv_pool, bool
     if (encode(&q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box, estrides,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return K3DA_ECUDA;
+        return cuda_failed();
     return quant ? launch_kernel<true>(kv_map, q_map, prm, st) : launch_kernel<false>(kv_map, q_map, prm, st);
 }
 

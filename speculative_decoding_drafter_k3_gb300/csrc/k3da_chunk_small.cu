@@ -875,7 +875,7 @@ __global__ void __launch_bounds__(Smem<QUANT>::kThreads, 1)
 template <bool QUANT>
 int launch(const CUtensorMap &kv_map, const ChunkParams &p, cudaStream_t stream) {
     if (!allow_smem<2 + QUANT>(reinterpret_cast<const void *>(k3da_chunk_small_kernel<QUANT>), Smem<QUANT>::kBytes))
-        return K3DA_ECUDA;
+        return cuda_failed();
     return launch_beside(k3da_chunk_small_kernel<QUANT>, dim3(kCtas), Smem<QUANT>::kThreads, Smem<QUANT>::kBytes,
                          stream, kv_map, p);
 }
@@ -885,7 +885,7 @@ int launch(const CUtensorMap &kv_map, const ChunkParams &p, cudaStream_t stream)
 int launch_small(const ChunkParams &p, const void *kv_pool, bool quant, cudaStream_t stream) {
     const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     CUtensorMap kv_map;
-    if (encode == nullptr || !pool_map(encode, &kv_map, kv_pool, p.num_pages, p.Hkv, quant, true)) return K3DA_ECUDA;
+    if (encode == nullptr || !pool_map(encode, &kv_map, kv_pool, p.num_pages, p.Hkv, quant, true)) return cuda_failed();
     return quant ? launch<true>(kv_map, p, stream) : launch<false>(kv_map, p, stream);
 }
 

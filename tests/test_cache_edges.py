@@ -1,4 +1,8 @@
 """The cache calls at the edges of what their documentation allows (GPU)."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -8,6 +12,7 @@ from test_chunk_attn import dev
 from test_kv_cache import bits, expected_plain, heads
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def with_odd_bits(b):
@@ -47,3 +52,48 @@ def test_append_qknorm_copies_every_bit_of_v(hq, hkv):
     cell = k3da.k3da_qk_norm_rope(qkv.clone(), *args, **heads(b))
     k3da.k3da_kv_append(two, cell, table, lens, cu, **heads(b))
     assert torch.equal(bits(pool), bits(two))
+
+
+def child(code):
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-4000:]
+
+
+def test_a_refused_launch_leaves_no_error_behind():
+    """The runtime refuses a launch on a stream whose capture has become
+    invalid; the library's next call must not report that."""
+    child("""
+import sys; sys.path[:0] = ['.', 'tests']
+import torch
+import speculative_decoding_drafter_k3_gb300 as k3da
+from cache_cases import Batch
+from test_chunk_attn import dev
+b = Batch([4], [100], 6, 1, "bf16", seed=1)
+pool, scales, qkv, table, lens, cu = dev(b)
+pos, qw, kw = b.positions.cuda(), b.q_w.cuda(), b.k_w.cuda()
+heads = dict(num_q_heads=6, num_kv_heads=1)
+k3da.k3da_qk_norm_rope(qkv.clone(), pos, qw, kw, **heads)
+k3da.k3da_kv_append(pool, qkv, table, lens, cu, **heads)
+spare = qkv.clone()
+torch.cuda.synchronize()
+side = torch.cuda.Stream()
+graph = torch.cuda.CUDAGraph()
+refused = False
+with torch.cuda.stream(side):
+    graph.capture_begin()
+    try:
+        side.synchronize()  # not allowed now: the capture ends here
+    except Exception:
+        pass
+    try:
+        k3da.k3da_kv_append(pool, qkv, table, lens, cu, **heads)
+    except k3da.K3daError:
+        refused = True
+    try:
+        graph.capture_end()
+    except Exception:
+        pass
+assert refused
+k3da.k3da_qk_norm_rope(spare, pos, qw, kw, **heads)
+torch.cuda.synchronize()
+""")
