@@ -84,7 +84,7 @@ __device__ __forceinline__ long long line_of(const ChunkParams &p, long long bas
 struct Request {
     int row, n, ctx;
     __device__ __forceinline__ bool fetch(const ChunkParams &p, int r) {
-        const int a = __ldg(p.cu_seqlens + r), b = __ldg(p.cu_seqlens + r + 1), c = __ldg(p.ctx_lens + r);
+        const int a = load_here(p.cu_seqlens + r), b = load_here(p.cu_seqlens + r + 1), c = load_here(p.ctx_lens + r);
         const int cap = p.page_stride * kP;
         row = min(max(a, 0), p.T);
         n = min(max(b, row), p.T) - row;

@@ -164,10 +164,10 @@ __global__ void __launch_bounds__(kAppendThreads) k3da_kv_append_kernel(const __
         a0 = a1 = b0 = b1 = make_uint4(0, 0, 0, 0);
         if (tl >= ntok) return;
         const uint4 *x = reinterpret_cast<const uint4 *>(p.qkv + (static_cast<long long>(t0 + tl) * heads + h) * kD);
-        a0 = __ldg(x + 2 * hp);
-        a1 = __ldg(x + 2 * hp + 1);
-        b0 = __ldg(x + 4 + 2 * hp);
-        b1 = __ldg(x + 4 + 2 * hp + 1);
+        a0 = x[2 * hp];
+        a1 = x[2 * hp + 1];
+        b0 = x[4 + 2 * hp];
+        b1 = x[4 + 2 * hp + 1];
     };
     load(next_tl, next_h);
     if (NORM) {
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kAppendThreads) k3da_kv_append_kernel(const __
         }
         if (tid < 2 * kD) wsm[tid] = __bfloat162float(tid < kD ? p.q_w[tid] : p.k_w[tid - kD]);
     }
-    for (int e = tid; e <= p.R; e += kAppendThreads) cu[e] = __ldg(p.cu_seqlens + e);
+    for (int e = tid; e <= p.R; e += kAppendThreads) cu[e] = load_here(p.cu_seqlens + e);
     __syncthreads();
     if (tid < ntok) {
         const int t = t0 + tid;
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kAppendThreads) k3da_kv_append_kernel(const __
         long long at = -1;
         const bool mine = t >= cu[r] && t < cu[r + 1];
         if (mine) {
-            const long long c = static_cast<long long>(__ldg(p.ctx_lens + r)) + (t - cu[r]);
+            const long long c = static_cast<long long>(load_here(p.ctx_lens + r)) + (t - cu[r]);
             if (c < t - cu[r] || c >= static_cast<long long>(p.page_stride) * kP) {
                 if (p.status) atomicOr(p.status, K3DA_STATUS_BAD_LENGTH);
             } else {
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kGatherThreads) k3da_kv_gather_kernel(const __
     const int tid = threadIdx.x;
     const int t0 = blockIdx.x * p.tokens_per_cta;
     const int ntok = min(p.T - t0, p.tokens_per_cta);
-    for (int e = tid; e <= p.R; e += kGatherThreads) cu[e] = __ldg(p.cu_seqlens + e);
+    for (int e = tid; e <= p.R; e += kGatherThreads) cu[e] = load_here(p.cu_seqlens + e);
     __syncthreads();
     if (tid < ntok) {
         const int t = t0 + tid;
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kGatherThreads) k3da_kv_gather_kernel(const __
         long long at = -2;
         if (t >= cu[r] && t < cu[r + 1]) {
             at = -1;
-            const long long c = static_cast<long long>(__ldg(p.starts + r)) + (t - cu[r]);
+            const long long c = static_cast<long long>(load_here(p.starts + r)) + (t - cu[r]);
             if (c < t - cu[r] || c >= static_cast<long long>(p.page_stride) * kP) {
                 if (p.status) atomicOr(p.status, K3DA_STATUS_BAD_LENGTH);
             } else {
@@ -378,12 +378,12 @@ __global__ void __launch_bounds__(kGatherThreads) k3da_kv_gather_kernel(const __
                     const long long row = at + (rest >> 2) * kP;
                     const int quarter = rest & 3;
                     if (QUANT) {
-                        x[k] = __ldg(reinterpret_cast<const uint4 *>(p.pool + row * kD) + quarter);
-                        sc[k] = __ldg(p.scales + row);
+                        x[k] = reinterpret_cast<const uint4 *>(p.pool + row * kD)[quarter];
+                        sc[k] = p.scales[row];
                     } else {
                         const uint4 *src = reinterpret_cast<const uint4 *>(p.pool + row * (kD * 2)) + 2 * quarter;
-                        x[k] = __ldg(src);
-                        y[k] = __ldg(src + 1);
+                        x[k] = src[0];
+                        y[k] = src[1];
                     }
                 }
             }

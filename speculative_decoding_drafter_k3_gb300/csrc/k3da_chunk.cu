@@ -231,8 +231,9 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
     for (int e = threadIdx.x; e < 2 * kGroups * kSlotRows; e += kThreads) xmax[e] = ~0ull;  // of no tile
     for (int e = threadIdx.x; e < kRecords * 3 * kD; e += kThreads)
         (&recs[e / (3 * kD)].first[0][0])[e % (3 * kD)] = 0xffffffffu;
-    // The second pass's kernel starts beside the first's, which has waited
-    // for what came before both.
+    // The second pass's kernel starts once every CTA of the first has let it,
+    // which each does behind its own wait: what came before both is complete
+    // when the second begins.  It waits for the first at its end alone.
     if (threadIdx.x == 0) {
         prefetch_map(&kv_map);
         prefetch_map(&q_map);

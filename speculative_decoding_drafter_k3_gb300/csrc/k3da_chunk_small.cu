@@ -689,8 +689,8 @@ __device__ __forceinline__ bool take_piece(const ChunkParams &p, const CUtensorM
             const uint4 *src =
                 reinterpret_cast<const uint4 *>(p.q + static_cast<long long>(it.row + token) * p.q_stride +
                                                 (it.h * p.G + rho - token * p.G) * kD + 16 * t4);
-            qa[nt] = __ldg(src);
-            qb[nt] = __ldg(src + 1);
+            qa[nt] = load_here(src);
+            qb[nt] = load_here(src + 1);
         }
     }
     // While they come: the piece's first tiles.
@@ -791,8 +791,9 @@ __global__ void __launch_bounds__(Smem<QUANT>::kThreads, 1)
         for (int e = threadIdx.x; e < kRecords * 3 * kD; e += kThreads)
             (&recs[e / (3 * kD)].first[0][0])[e % (3 * kD)] = 0xffffffffu;
     }
-    // The second pass's kernel starts beside the first's, which has waited
-    // for what came before both.
+    // The second pass's kernel starts once every CTA of the first has let it,
+    // which each does behind its own wait: what came before both is complete
+    // when the second begins.  It waits for the first at its end alone.
     if (threadIdx.x == 0) prefetch_map(&kv_map);
     if (!p.second) wait_for_stream();
     let_next_start();
