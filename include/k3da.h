@@ -299,7 +299,8 @@ int k3da_qk_norm_rope_yarn(void *qkv, int num_tokens, int num_q_heads, int num_k
  * there.  Any number of query heads per kv head from 1 to 16, at most 64 kv
  * heads, head_dim 64.
  *
- * Every pointer is device memory of the current device.  As above: nothing
+ * Every pointer is device memory of the current device.  Memory that a call
+ * writes overlaps nothing else that it is given (K3DA_EINVAL).  As above: nothing
  * is allocated or synchronised, lengths and pages are read by the kernels (a
  * captured graph replays with them rewritten), and a violation only they can
  * see sets a K3DA_STATUS_* bit and skips the access: a token past its page
@@ -334,7 +335,7 @@ typedef enum {
  *   kv_pool      [num_pages, 2, Hkv, 64, 64], written at the chunk's tokens
  *                only.  16-byte aligned.  cache_dtype, kv_scales: above.
  *   qkv          [num_tokens, (Hq + 2*Hkv)*64] bf16, k already normalised
- *                and roped.  16-byte aligned.  Must not overlap kv_pool.
+ *                and roped.  16-byte aligned.
  *   others       as for k3da_attn.
  *
  * bf16: the bits are copied.  e4m3: 2^(b - 127) is the smallest power of two
@@ -360,7 +361,7 @@ int k3da_kv_append(void *kv_pool, int cache_dtype, void *kv_scales, int64_t num_
  *                sequence are read and not used.
  *   yarn         YaRN RoPE, or NULL for plain NeoX RoPE.
  *   q_out        [num_tokens, Hq*64] bf16, 16-byte aligned, or NULL: no q
- *                wanted.  Must not overlap qkv or kv_pool.
+ *                wanted.
  */
 int k3da_kv_append_qknorm(void *kv_pool, int cache_dtype, void *kv_scales, int64_t num_pages,
                           const int32_t *page_table, int page_stride, const int32_t *ctx_lens,
@@ -373,10 +374,10 @@ int k3da_kv_append_qknorm(void *kv_pool, int cache_dtype, void *kv_scales, int64
 /*
  * k3da_kv_gather -- read cached tokens back as dense bf16 rows: row
  * cu_seqlens[r] + i of k_out and v_out ([num_tokens, Hkv*64] each, 16-byte
- * aligned, not overlapping) becomes token starts[r] + i of request r's
- * cache.  Exact for both cache types (a quantised value has 4 significant
- * bits), but for values below bf16's smallest normal, which round.  Tokens
- * that fail a device check read as zeros.
+ * aligned) becomes token starts[r] + i of request r's cache.  Exact for both
+ * cache types (a quantised value has 4 significant bits), but for values below
+ * bf16's smallest normal, which round.  Tokens that fail a device check read
+ * as zeros.
  */
 int k3da_kv_gather(void *k_out, void *v_out, const void *kv_pool, int cache_dtype,
                    const void *kv_scales, int64_t num_pages, const int32_t *page_table,
@@ -401,8 +402,7 @@ size_t k3da_chunk_workspace_bytes(int num_tokens, int num_requests, int num_q_he
  * sees nothing gets out = 0 and lse = -inf.  Chunks of any length from a
  * single decoded token on, mixed in one call.
  *
- *   out          [num_tokens, Hq*64] bf16, written; 16-byte aligned; must
- *                not overlap q or kv_pool.
+ *   out          [num_tokens, Hq*64] bf16, written; 16-byte aligned.
  *   lse          [num_tokens, Hq] fp32, or NULL.
  *   q            [num_tokens, Hq*64] bf16 rows q_row_stride elements apart
  *                (>= Hq*64, a multiple of 8, at most 2^31): the q heads of

@@ -106,6 +106,20 @@ inline bool overlap(const void *a, size_t na, const void *b, size_t nb) {
     return x < y + nb && y < x + na;
 }
 
+// Memory a call is given.
+struct Span {
+    const void *at;  // NULL: not given
+    size_t bytes;
+};
+
+// One of the first `written` of n spans overlaps another of the n.
+inline bool written_overlap(const Span *spans, int written, int n) {
+    for (int i = 0; i < written; ++i)
+        for (int j = i + 1; j < n; ++j)
+            if (spans[i].at && spans[j].at && overlap(spans[i].at, spans[i].bytes, spans[j].at, spans[j].bytes)) return true;
+    return false;
+}
+
 inline bool heads_ok(int hq, int hkv) {
     return hkv >= 1 && hkv <= kMaxKvHeads && hq >= hkv && hq % hkv == 0 && hq / hkv <= kMaxGroup;
 }
@@ -113,6 +127,10 @@ inline bool heads_ok(int hq, int hkv) {
 inline size_t pool_bytes(int64_t num_pages, int hkv, int cache_dtype) {
     return static_cast<size_t>(num_pages) * 2 * hkv * kP * kD * (cache_dtype == K3DA_CACHE_BF16 ? 2 : 1);
 }
+
+inline size_t scale_bytes(int64_t num_pages, int hkv) { return static_cast<size_t>(num_pages) * 2 * hkv * kP; }
+
+inline size_t table_bytes(int R, int page_stride) { return static_cast<size_t>(R) * page_stride * sizeof(int32_t); }
 
 // The arguments every cache call has.
 inline int check_cache(const void *pool, int cache_dtype, const void *scales, int64_t num_pages,

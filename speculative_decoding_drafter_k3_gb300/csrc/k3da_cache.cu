@@ -465,13 +465,21 @@ int launch_append(void *kv_pool, int cache_dtype, void *kv_scales, int64_t num_p
         if (yarn != nullptr && !k3da_host::yarn_valid(yarn)) return K3DA_EINVAL;
     }
     if (T == 0) return K3DA_OK;
-    // Nothing that is written may overlap what other threads still read.
-    const size_t in_bytes = static_cast<size_t>(T) * (Hq + 2 * Hkv) * kD * 2;
-    const size_t q_bytes = static_cast<size_t>(T) * Hq * kD * 2;
-    const size_t cache_bytes = pool_bytes(num_pages, Hkv, cache_dtype);
-    if (overlap(qkv, in_bytes, kv_pool, cache_bytes)) return K3DA_EINVAL;
-    if (q_out && (overlap(qkv, in_bytes, q_out, q_bytes) || overlap(kv_pool, cache_bytes, q_out, q_bytes)))
-        return K3DA_EINVAL;
+    // Nothing that is written may overlap what other threads still read, or
+    // write.
+    const size_t rows = static_cast<size_t>(T), ints = sizeof(int32_t);
+    const Span spans[] = {{kv_pool, pool_bytes(num_pages, Hkv, cache_dtype)},
+                          {kv_scales, scale_bytes(num_pages, Hkv)},
+                          {q_out, rows * Hq * kD * 2},
+                          {qkv, rows * (Hq + 2 * Hkv) * kD * 2},
+                          {page_table, table_bytes(R, page_stride)},
+                          {ctx_lens, R * ints},
+                          {cu_seqlens, (R + 1) * ints},
+                          {positions, rows * (pos_dtype == K3DA_POS_I64 ? 8 : 4)},
+                          {q_norm_w, kD * 2},
+                          {k_norm_w, kD * 2},
+                          {status, ints}};
+    if (written_overlap(spans, 3, sizeof spans / sizeof spans[0])) return K3DA_EINVAL;
 
     AppendParams prm;
     std::memset(&prm, 0, sizeof prm);
@@ -543,11 +551,16 @@ extern "C" int k3da_kv_gather(void *k_out, void *v_out, const void *kv_pool, int
     if (!aligned_to(k_out, 16) || !aligned_to(v_out, 16)) return K3DA_EINVAL;
     if (num_tokens == 0) return K3DA_OK;
     if (!k_out || !v_out) return K3DA_EINVAL;
-    const size_t out_bytes = static_cast<size_t>(num_tokens) * num_kv_heads * kD * 2;
-    const size_t cache_bytes = pool_bytes(num_pages, num_kv_heads, cache_dtype);
-    if (overlap(k_out, out_bytes, v_out, out_bytes) || overlap(k_out, out_bytes, kv_pool, cache_bytes) ||
-        overlap(v_out, out_bytes, kv_pool, cache_bytes))
-        return K3DA_EINVAL;
+    const size_t out_bytes = static_cast<size_t>(num_tokens) * num_kv_heads * kD * 2, ints = sizeof(int32_t);
+    const Span spans[] = {{k_out, out_bytes},
+                          {v_out, out_bytes},
+                          {kv_pool, pool_bytes(num_pages, num_kv_heads, cache_dtype)},
+                          {kv_scales, scale_bytes(num_pages, num_kv_heads)},
+                          {page_table, table_bytes(num_requests, page_stride)},
+                          {starts, num_requests * ints},
+                          {cu_seqlens, (num_requests + 1) * ints},
+                          {status, ints}};
+    if (written_overlap(spans, 2, sizeof spans / sizeof spans[0])) return K3DA_EINVAL;
     GatherParams prm;
     std::memset(&prm, 0, sizeof prm);
     prm.k_out = static_cast<__nv_bfloat16 *>(k_out);

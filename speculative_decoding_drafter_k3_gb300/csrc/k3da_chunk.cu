@@ -1089,11 +1089,18 @@ extern "C" int k3da_chunk_attn(void *out, float *lse, const void *q, int64_t q_r
     if (!workspace || !aligned_to(workspace, 256) || workspace_bytes < kWorkspace) return K3DA_EWORKSPACE;
     if (num_tokens == 0) return K3DA_OK;
     if (!out || !q) return K3DA_EINVAL;
-    const size_t out_bytes = static_cast<size_t>(num_tokens) * width * 2;
-    const size_t q_bytes = (static_cast<size_t>(num_tokens - 1) * q_row_stride + width) * 2;
-    if (overlap(out, out_bytes, q, q_bytes) ||
-        overlap(out, out_bytes, kv_pool, pool_bytes(num_pages, num_kv_heads, cache_dtype)))
-        return K3DA_EINVAL;
+    const size_t tokens = static_cast<size_t>(num_tokens), ints = sizeof(int32_t);
+    const Span spans[] = {{out, tokens * width * 2},
+                          {lse, tokens * num_q_heads * sizeof(float)},
+                          {workspace, kWorkspace},
+                          {q, ((tokens - 1) * q_row_stride + width) * 2},
+                          {kv_pool, pool_bytes(num_pages, num_kv_heads, cache_dtype)},
+                          {kv_scales, scale_bytes(num_pages, num_kv_heads)},
+                          {page_table, table_bytes(num_requests, page_stride)},
+                          {ctx_lens, num_requests * ints},
+                          {cu_seqlens, (num_requests + 1) * ints},
+                          {status, ints}};
+    if (written_overlap(spans, 3, sizeof spans / sizeof spans[0])) return K3DA_EINVAL;
 
     ChunkParams prm;
     std::memset(&prm, 0, sizeof prm);
