@@ -342,7 +342,9 @@ typedef enum {
  * that brings the row's largest magnitude to at most 448 (b = 0 for rows
  * below 448 * 2^-127), codes are rounded to nearest even; a row with an
  * infinity or a NaN gets b = 255 and reads back as NaN.  Two tokens of a
- * call that share a cache slot (a page listed twice) leave one of the two.
+ * call that share a cache slot (a page listed twice) leave that row undefined:
+ * it may hold parts of both, or one's codes under the other's scale.  No other
+ * row is touched.
  */
 int k3da_kv_append(void *kv_pool, int cache_dtype, void *kv_scales, int64_t num_pages,
                    const int32_t *page_table, int page_stride, const int32_t *ctx_lens,

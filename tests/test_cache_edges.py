@@ -54,6 +54,31 @@ def test_append_qknorm_copies_every_bit_of_v(hq, hkv):
     assert torch.equal(bits(pool), bits(two))
 
 
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_tokens_of_one_slot_leave_every_other_row_alone(cache):
+    """A page in the tables of two requests, and twice in one: the rows that
+    two tokens share are anything; the others are what they should be."""
+    b = Batch([300, 300, 200], [0, 0, 0], 24, 4, cache, seed=43)
+    b.table[1, 2] = b.table[0, 2]
+    b.table[2, 3] = b.table[2, 1]
+    pool, scales, qkv, table, lens, cu = dev(b)
+    shared = [int(b.table[0, 2]), int(b.table[2, 1])]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    want_pool, want_scales = expected_plain(b)
+    for _ in range(5):
+        k3da.k3da_kv_append(pool, qkv, table, lens, cu, kv_scales=scales, status=status, **heads(b))
+    assert int(status) == 0
+    fine = [p for p in range(b.pages) if p not in shared]
+    got, want = (bits(t.cpu()).view(*t.shape[:-1], -1) for t in (pool, want_pool))
+    assert torch.equal(got[fine], want[fine])
+    # Request 2's second table entry of the page has tokens 192 to 199 only.
+    rest = shared[1]
+    assert torch.equal(got[rest, :, :, 8:], want[rest, :, :, 8:])
+    if scales is not None:
+        got, want = scales.view(torch.uint8).cpu(), want_scales.view(torch.uint8)
+        assert torch.equal(got[fine], want[fine]) and torch.equal(got[rest, :, :, 8:], want[rest, :, :, 8:])
+
+
 def child(code):
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-4000:]
