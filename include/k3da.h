@@ -295,8 +295,8 @@ int k3da_qk_norm_rope_yarn(void *qkv, int num_tokens, int num_q_heads, int num_k
  * n_r >= 0 tokens, rows cu_seqlens[r] .. cu_seqlens[r+1] of the packed
  * [num_tokens, ...] tensors (cu_seqlens: R + 1 int32, rising from 0); its
  * token i is token ctx_lens[r] + i of its cache.  Rows from cu_seqlens[R] on
- * belong to nobody: they are not read and what is written is left as it was
- * there.  Any number of query heads per kv head from 1 to 16, at most 64 kv
+ * belong to nobody: what they hold makes no difference (it may be read), and
+ * what is written is left as it was there.  Any number of query heads per kv head from 1 to 16, at most 64 kv
  * heads, head_dim 64.
  *
  * Every pointer is device memory of the current device.  Memory that a call
@@ -359,8 +359,7 @@ int k3da_kv_append(void *kv_pool, int cache_dtype, void *kv_scales, int64_t num_
  * bits of k3da_qk_norm_rope followed by k3da_kv_append.
  *
  *   positions, pos_dtype, q_norm_w, k_norm_w, eps, rope_base
- *                as for k3da_qk_norm_rope; positions of rows behind the last
- *                sequence are read and not used.
+ *                as for k3da_qk_norm_rope.
  *   yarn         YaRN RoPE, or NULL for plain NeoX RoPE.
  *   q_out        [num_tokens, Hq*64] bf16, 16-byte aligned, or NULL: no q
  *                wanted.

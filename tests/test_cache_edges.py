@@ -79,6 +79,37 @@ def test_tokens_of_one_slot_leave_every_other_row_alone(cache):
         assert torch.equal(got[fine], want[fine]) and torch.equal(got[rest, :, :, 8:], want[rest, :, :, 8:])
 
 
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_rows_behind_the_last_sequence_make_no_difference(cache):
+    """They hold NaN and infinities, and positions from nowhere."""
+    b = Batch([3, 70, 1], [500, 0, 63], 6, 1, cache, 30, seed=46, stride=1300)
+    clean = dev(b)
+    b.qkv[b.rows:] = torch.tensor([float("nan"), float("inf"), float("-inf"), 3e38]).repeat(128)[:b.qkv.shape[1]].to(torch.bfloat16)
+    dirty = dev(b)
+    pos = b.positions.to(torch.int64)
+    far = pos.clone()
+    far[b.rows:] = torch.tensor([-1, 2 ** 62, -2 ** 63]).repeat(10)
+    results = []
+    for d, where in ((clean, pos), (dirty, far)):
+        pool, scales, qkv, table, lens, cu = d
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        kw = dict(kv_scales=scales, status=status)
+        q, out = (torch.full((b.T, 6 * D), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        k, v = (torch.full((b.T, D), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        lse = torch.full((b.T, 6), 7.0, device="cuda")
+        ws = k3da.alloc_chunk_workspace(b.T, b.R, 6, 1, b.stride)
+        k3da.k3da_kv_append_qknorm(pool, qkv, table, lens, cu, where.cuda(), b.q_w.cuda(), b.k_w.cuda(), q_out=q, **heads(b), **kw)
+        k3da.k3da_kv_append(pool, qkv, table, lens, cu, **heads(b), **kw)
+        k3da.k3da_chunk_attn(out, qkv[:, :6 * D], pool, table, lens, cu, lse=lse, workspace=ws, **heads(b), **kw)
+        k3da.k3da_kv_gather(k, v, pool, table, lens, cu, num_kv_heads=1, **kw)
+        assert int(status) == 0
+        for t in (q, out, k, v, lse):
+            assert (t[b.rows:] == 7).all() and not (t[:b.rows] == 7).all()
+        results.append([bits(t) for t in (pool, q, out, k, v, lse)])
+    for x, y in zip(*results):
+        assert torch.equal(x, y)
+
+
 def child(code):
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-4000:]
