@@ -400,8 +400,8 @@ size_t k3da_chunk_workspace_bytes(int num_tokens, int num_requests, int num_q_he
  *   lse[t, h] = log sum_c exp(softmax_scale * q[t, h] . K_c)
  * over the cache tokens c that `mask` shows (the chunk's own K and V were
  * appended before; with K3DA_MASK_CONTEXT they need not be).  A row that
- * sees nothing gets out = 0 and lse = -inf.  Chunks of any length from a
- * single decoded token on, mixed in one call.
+ * sees nothing, or whose every score is -inf, gets out = 0 and lse = -inf.
+ * Chunks of any length from a single decoded token on, mixed in one call.
  *
  *   out          [num_tokens, Hq*64] bf16, written; 16-byte aligned.
  *   lse          [num_tokens, Hq] fp32, or NULL.

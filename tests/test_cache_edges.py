@@ -8,7 +8,7 @@ import torch
 
 import speculative_decoding_drafter_k3_gb300 as k3da
 from cache_cases import Batch, D
-from test_chunk_attn import dev
+from test_chunk_attn import call, check, dev
 from test_kv_cache import bits, expected_plain, heads
 
 pytestmark = pytest.mark.gpu
@@ -110,6 +110,71 @@ def test_rows_behind_the_last_sequence_make_no_difference(cache):
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("new,ctx", [([1, 2], [100, 30]), ([1], [20000]), ([40], [100]), ([30], [9000])])
+def test_scores_that_are_all_minus_infinity(new, ctx):
+    """Such a row's weights are all zero: out 0 and lse -inf, as for a row
+    that sees nothing."""
+    b = Batch(new, ctx, 6, 1, "bf16", seed=44, stride=1300)
+    b.pool[:, 0] = 0
+    b.pool[:, 0, :, :, 0] = float("-inf")
+    b.qkv[:, :6 * D] = 1.0
+    out, lse = call(b)
+    assert (out == 0).all() and (lse == float("-inf")).all()
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_a_capture_that_forks_and_joins(cache):
+    """Two requests' appends on two streams, joined before the attention over
+    both, which a torch kernel on a third stream precedes too."""
+    b = Batch([40, 130], [300, 70], 6, 1, cache, seed=45)
+    pool, scales, qkv, table, lens, cu = dev(b)
+    ws = k3da.alloc_chunk_workspace(b.T, b.R, 6, 1, b.stride)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kw = dict(kv_scales=scales, status=status)
+    halves = [(table[r:r + 1], lens[r:r + 1], torch.tensor([0, n], dtype=torch.int32, device="cuda"),
+               qkv[b.cu[r]:b.cu[r + 1]].clone()) for r, n in enumerate(b.new)]
+    staged = qkv.clone()
+
+    def work(out, lse, source):
+        main = torch.cuda.current_stream()
+        sides = [torch.cuda.Stream() for _ in range(3)]
+        for s in sides:
+            s.wait_stream(main)
+        for s, (t, l, c, rows) in zip(sides, halves):
+            with torch.cuda.stream(s):
+                k3da.k3da_kv_append(pool, rows, t, l, c, **heads(b), **kw)
+        with torch.cuda.stream(sides[2]):
+            staged.copy_(source)
+            staged.mul_(1.0)
+        for s in sides:
+            main.wait_stream(s)
+        k3da.k3da_chunk_attn(out, staged[:, :6 * D], pool, table, lens, cu, num_q_heads=6, num_kv_heads=1, lse=lse,
+                             workspace=ws, **kw)
+
+    want_pool, want_scales = expected_plain(b)
+    out = torch.full((b.T, 6 * D), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((b.T, 6), 7.0, device="cuda")
+    work(out, lse, qkv)
+    torch.cuda.synchronize()
+    first = out.clone(), lse.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        work(out, lse, qkv)
+    start = b.pool.cuda()
+    for _ in range(5):
+        pool.view(torch.uint8).copy_(start.view(torch.uint8))
+        staged.zero_()
+        out.zero_()
+        lse.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(bits(out), bits(first[0])) and torch.equal(lse, first[1])
+    assert int(status) == 0
+    assert torch.equal(bits(pool.cpu()), bits(want_pool))
+    b.pool, b.scales = want_pool, want_scales
+    check(b, out, lse)
+
+
 def child(code):
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-4000:]
@@ -123,7 +188,7 @@ import sys; sys.path[:0] = ['.', 'tests']
 import torch
 import speculative_decoding_drafter_k3_gb300 as k3da
 from cache_cases import Batch
-from test_chunk_attn import dev
+from test_chunk_attn import call, check, dev
 b = Batch([4], [100], 6, 1, "bf16", seed=1)
 pool, scales, qkv, table, lens, cu = dev(b)
 pos, qw, kw = b.positions.cuda(), b.q_w.cuda(), b.k_w.cuda()
@@ -152,4 +217,56 @@ with torch.cuda.stream(side):
 assert refused
 k3da.k3da_qk_norm_rope(spare, pos, qw, kw, **heads)
 torch.cuda.synchronize()
+""")
+
+
+def test_the_calls_go_on_after_a_device_reset():
+    """The device's context made anew (cudaDeviceReset, which ends this
+    process's own context, with nothing in flight): kernels' attributes are
+    set up again."""
+    child("""
+import ctypes, glob, os, sys
+sys.path[:0] = ['.']
+import torch
+import speculative_decoding_drafter_k3_gb300 as k3da
+names = ["libcudart.so.13"] + glob.glob("/usr/local/cuda*/lib64/libcudart.so*")
+rt = None
+for name in names:
+    try:
+        rt = ctypes.CDLL(name)
+        break
+    except OSError:
+        pass
+assert rt is not None
+driver, lib = ctypes.CDLL("libcuda.so.1"), k3da.load_library()
+
+def ok(rc):
+    assert rc == 0, rc
+
+def context():
+    number = ctypes.c_ulonglong()
+    ok(driver.cuCtxGetId(None, ctypes.byref(number)))
+    return number.value
+
+def run():
+    ok(rt.cudaSetDevice(0))
+    base = ctypes.c_void_p()
+    ok(rt.cudaMalloc(ctypes.byref(base), ctypes.c_size_t(1 << 28)))
+    ok(rt.cudaMemset(base, 0, ctypes.c_size_t(1 << 28)))
+    at, mb = base.value, 1 << 20
+    cu = (ctypes.c_int32 * 2)(0, 40)
+    ok(rt.cudaMemcpy(ctypes.c_void_p(at), cu, ctypes.c_size_t(8), 1))
+    pool, table, lens, q, out, ws = (at + k * mb for k in (1, 32, 33, 34, 40, 64))
+    need = lib.k3da_chunk_workspace_bytes(40, 1, 6, 1, 2000)
+    for tokens in (40, 1):  # both kernels
+        rc = lib.k3da_chunk_attn(out, None, q, 384, tokens, pool, 0, None, 64, table, 2000, lens, at, 1, 6, 1, 64, 0, 0.125,
+                                 ws, need, None, None)
+        assert rc == 0, k3da.load_library().k3da_error_string(rc)
+    ok(rt.cudaDeviceSynchronize())
+
+run()
+first = context()
+ok(rt.cudaDeviceReset())
+run()
+assert context() != first  # it was another context
 """)
