@@ -270,3 +270,41 @@ ok(rt.cudaDeviceReset())
 run()
 assert context() != first  # it was another context
 """)
+
+
+def test_more_elements_than_32_bits_count():
+    """1024 requests of 4200 tokens, 16 heads: rows of q, out, lse and qkv past
+    2^32 elements.  The last request's against the definition, and against
+    itself in a call of its own."""
+    R, n, hq = 1024, 4200, 16
+    T, stride = R * n, -(-n // 64)
+    g = torch.Generator(device="cuda").manual_seed(47)
+    qkv = torch.randn(T, (hq + 2) * D, generator=g, device="cuda", dtype=torch.bfloat16)
+    pool, _ = k3da.alloc_cache(R * stride, 1)
+    table = torch.arange(R * stride, dtype=torch.int32, device="cuda").view(R, stride)
+    lens = torch.zeros(R, dtype=torch.int32, device="cuda")
+    cu = torch.arange(0, T + 1, n, dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kw = dict(num_q_heads=hq, num_kv_heads=1, status=status)
+    out, lse = torch.empty(T, hq * D, dtype=torch.bfloat16, device="cuda"), torch.empty(T, hq, device="cuda")
+    assert out.numel() > 1 << 32
+    k3da.k3da_kv_append(pool, qkv, table, lens, cu, **kw)
+    ws = k3da.alloc_chunk_workspace(T, R, hq, 1, stride)
+    k3da.k3da_chunk_attn(out, qkv[:, :hq * D], pool, table, lens, cu, lse=lse, workspace=ws, **kw)
+    k, v = (torch.empty(T, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k3da.k3da_kv_gather(k, v, pool, table, lens, cu, num_kv_heads=1, status=status)
+    assert int(status) == 0
+    assert torch.equal(k[-n:], qkv[-n:, hq * D:(hq + 1) * D]) and torch.equal(v[-n:], qkv[-n:, (hq + 1) * D:])
+    alone, alse = torch.empty_like(out[:n]), torch.empty_like(lse[:n])
+    k3da.k3da_chunk_attn(alone, qkv[-n:, :hq * D], pool, table[-1:].contiguous(), lens[:1], cu[:2], lse=alse, workspace=ws, **kw)
+    kd, vd = k[-n:].double(), v[-n:].double()
+    for i in (0, 1, 63, 2000, n - 1):
+        q = qkv[T - n + i, :hq * D].double().view(hq, D)
+        x = q @ kd[:i + 1].T * 0.125
+        p = torch.softmax(x, -1)
+        want, mag = p @ vd[:i + 1], p @ vd[:i + 1].abs()
+        for got, l in ((out[T - n + i], lse[T - n + i]), (alone[i], alse[i])):
+            err = (got.double().view(hq, D) - want).abs() - (2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -10) * mag)
+            assert err.max() <= 1e-7
+            # Scores: 64 terms of |q k| / 8 below 64; sums of 4200; ex2, log2.
+            assert (l.double() - torch.logsumexp(x, -1)).abs().max() <= (64 * 64 + n) * 2.0 ** -24 + 2.0 ** -17
