@@ -109,8 +109,8 @@ __device__ __forceinline__ uint2 values4(uint32_t c, float mul) {
 // of whole tokens at once, and the next ones' rows while it works on them.
 // Each row is read and written once; the shared-memory reads of cos, sin and
 // the weights bound it: 16.8k tokens in 8 requests, 24/4 heads, q out, e4m3:
-// 12.9 us where the bytes alone take 8.2.  Raw, bf16: 16k tokens 4.4 us
-// (2.7).
+// 12.8 us where the bytes alone take 8.2; bf16 14.3 (8.7).  Raw, up to 8192
+// tokens in each of 4: bf16 4.3 us (2.7), e4m3 4.5 (2.0).
 constexpr int kAppendThreads = 256;
 constexpr int kAppendRows = kAppendThreads / 2;
 constexpr int kAppendTokens = 64;  // most tokens of a CTA
@@ -308,7 +308,8 @@ __global__ void __launch_bounds__(kAppendThreads) k3da_kv_append_kernel(const __
 // Four threads per (token, K or V, head) row, 16 dims each: 32 bytes (bf16)
 // or 16 codes and the row's scale in, 32 bytes out.  A thread issues the
 // loads of all its rows before it stores any.  Bound by memory: 60k tokens,
-// 4 heads, e4m3: 18.4 us (the bytes alone 17.1); 2041 tokens, 1 head 2.3 us.
+// 4 heads, e4m3: 18.6 us (the bytes alone 17.1), bf16 27.8 (22.7); 2041
+// tokens, 1 head 2.3 us.
 constexpr int kGatherThreads = 256;
 constexpr int kGatherTokens = 256;  // most tokens of a CTA
 constexpr int kGatherWave = 4 * 152;  // CTAs that run at once

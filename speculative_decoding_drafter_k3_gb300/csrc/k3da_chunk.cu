@@ -13,8 +13,8 @@
 // item's keys come in tiles of 128 (two pages).  All items are laid on one
 // line, request by request, head by head, each as long as the keys its last
 // row sees plus a constant, and the line is cut into equal slices, one a
-// CTA: every CTA has the same number of key tiles to within one, whatever
-// the lengths.  An item that a cut falls into leaves partial results, which
+// CTA: equal in keys and fixed costs together, whatever the lengths (a CTA
+// with more items has a few tiles less).  An item that a cut falls into leaves partial results, which
 // the combine kernel folds in order.  Each CTA finds its slice by itself: a
 // scan over the requests, then closed forms.
 //
@@ -54,11 +54,12 @@
 // Rounding: scores, softmax statistics and O are fp32 throughout (partials
 // too); P is rounded to bf16 once for the P V product, the output once.
 //
-// Measured: 2048 tokens over 6144 (24/4 heads) bf16 105 us, 860 TFLOP/s; e4m3
-// 140 us; 8192 over 8192 e4m3 776 us, 800 TFLOP/s.  Bound by issue slots (67%
+// Measured: 2048 tokens over 6144 (24/4 heads) bf16 106 us, 850 TFLOP/s; e4m3
+// 135 us; 8192 over 8192 e4m3 784 us, 790 TFLOP/s.  Bound by issue slots (67%
 // taken; 73% with codes) and the slots' chain: two slots' tile takes 2000
 // cycles, its exponentials and its products 1024 each.  8 x 8 tokens over
-// 16k to 131k bf16: 102.5 us, 5.6 TB/s of cache.
+// 16k to 131k bf16: 102.6 us, 5.6 TB/s of cache.  (0.7% of a prefill and 1% of
+// this are the votes in which a warp agrees on its waits.)
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -1137,8 +1138,9 @@ extern "C" int k3da_chunk_attn(void *out, float *lse, const void *q, int64_t q_r
     // Which requests are small is known to the kernels alone; that none can
     // be long is known from the number of tokens.  A call whose caches are
     // small, whatever their lengths, is bound by latency: one kernel for all
-    // (8 x 6 tokens over up to 2041, 6/1 heads: 16.4 us, with both 18.6; the
-    // small kernel's gain on 64 x 8000 codes comes to those 3 us at 75000 keys).
+    // (8 x 6 tokens over up to 2041, 6/1 heads: 13.7 us, with both 15.8; what the
+    // small kernel gains on 64 x 8000 keys a head, 80 us with codes and 2 with
+    // bf16, comes to those 2 us at 55000 keys of codes, 2 million of bf16).
     const long long heads = static_cast<long long>(num_requests) * num_kv_heads;
     const long long keys = heads * page_stride * kP;
     const bool can_be_long = num_tokens > kSmallRows || num_tokens * prm.G > kSmallRows;
@@ -1158,12 +1160,12 @@ extern "C" int k3da_chunk_attn(void *out, float *lse, const void *q, int64_t q_r
         if (launched != K3DA_OK) return launched;
     }
     // Where all there can be fits one slice, nothing is cut (a token over 300:
-    // 8.5 instead of 9.6 us).
+    // 7.2 instead of 8.6 us).
     const long long line = keys + heads * (kSmallOverhead + 2 * prm.tpt + kSmallRows);
     if (!can_be_long && line < 2 * kMinSmallSlice) return K3DA_OK;
     // Items a cut can fall into, rows one can have: a grid of about 1200 CTAs
-    // over the long chunks' (8 x 8 tokens over long contexts: 102.5 us, with
-    // half as many 107.5, with twice as many 102), 600 over the others'.
+    // over the long chunks' (8 x 8 tokens over long contexts: 102.6 us; with
+    // half as many 5 more, with twice as many the same), 600 over the others'.
     const long long items =
         ((static_cast<long long>(num_tokens) + 2 * prm.tpt - 1) / (2 * prm.tpt) + num_requests) * num_kv_heads;
     const unsigned gx = static_cast<unsigned>(items < kCtas ? items : kCtas);

@@ -22,12 +22,12 @@
 // precision's range (exact but for dims 2^-31 below the row's largest, which
 // lose bits, and are gone 2^-39 below).
 //
-// Measured (64 decoded tokens over 8000 each, 24/4 heads): e4m3 57 us, 4.7
-// TB/s of cache, where the long chunks' kernel takes 144; bf16 91 us, 5.7
-// TB/s, against 100.  About 9 us of either are launches, plan, first loads
+// Measured (64 decoded tokens over 8000 each, 24/4 heads): e4m3 54 us, 4.9
+// TB/s of cache, where the long chunks' kernel takes 133; bf16 90 us, 5.8
+// TB/s, against 92.  About 9 us of either are launches, plan, first loads
 // and the fold of cut items; the rest streams at 5.6 to 6.0 TB/s.  15 warps of
-// 128 registers take as long, and 53 instead of 43 us where two tiles of rows
-// spill (8 x 2 tokens over 60000, 16/2 heads, e4m3).
+// 128 registers took as long, and a quarter more where two tiles of rows spill
+// (8 x 2 tokens over 60000, 16/2 heads, e4m3: 37 us with 11).
 //
 // Rounding: scores, statistics, O and partial results are fp32; weights are
 // rounded once (bf16, or half precision for codes: see kHead), the output once.
