@@ -1,6 +1,6 @@
 // chunk_cut.h -- what a CTA of the chunk attention leaves for the combine
-// kernel, and what the combine asks of it before it uses it as an index.
-// (No CUDA here: the check is tested on the host.)
+// kernel, and what the combine asks of it before it uses it as an index; which
+// pages need a mask.  (No CUDA here: tested on the host.)
 #pragma once
 
 #ifdef __CUDACC__
@@ -33,5 +33,11 @@ K3DA_HOST_DEVICE inline bool cut_fits(const Cut &cut, int owner, int rows, int h
     return cut.last >= owner && cut.last < kCtas && cut.tokens >= 0 && cut.tokens <= most && cut.row >= 0 &&
            cut.row <= rows && cut.tokens <= rows - cut.row && cut.head >= 0 && cut.head < heads;
 }
+
+// A page whose first key is `first` has keys that not all of the rows see,
+// who see `least` keys at least.  (The last page of the longest table ends 64
+// keys before 2^31: a tile's second page begins there, and first + 64 is no
+// int.)
+K3DA_HOST_DEVICE inline bool page_masked(int first, int least) { return least - first < 64; }
 
 }  // namespace k3da_chunk

@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(threads_of(QUANT), 1)
                 tmem_wait_ld();
                 pin32(x);
                 pin32(x + 32);
-                if (key0 + kP > least) {
+                if (page_masked(key0, least)) {
                     const int lim = sees - key0;
 #pragma unroll
                     for (int j = 0; j < kP; ++j) x[j] = j < lim ? x[j] : 0xff800000u;

@@ -385,7 +385,7 @@ __device__ __forceinline__ bool take_page(Rows<NT> &R, Loader<QUANT> &load, cons
     const int g = lane >> 2, t4 = lane & 3;
     if (!warp_wait(load.bars + 8 * turn.place, turn.phase, abort_flag, p.status)) return false;
     const uint8_t *kt = load.tiles + turn.place * L::kTileBytes, *ks = load.scales + turn.place * kP;
-    const bool masked = key0 + kP > least;
+    const bool masked = page_masked(key0, least);
     // Code tiles have rows of 64 bytes, 16-byte chunks swizzled by bits 1 and
     // 2 of the row.  With keys 2 and 3 of every four exchanged, a thread's
     // loads of V (below) meet no bank twice.

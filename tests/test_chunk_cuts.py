@@ -83,3 +83,33 @@ def test_every_way_out_of_a_kernel_leaves_a_cut():
     assert "return" not in loop
     for m in re.finditer(r"if \(!warp_wait\([^;]*?\)\)\s*(\{.*?\}|break;)", loop, re.S):
         assert "if (lane == 0 && more) p.cuts[blockIdx.x] = Cut{" in m.group(1)
+
+
+PAGES_HARNESS = r"""
+#include <cstdio>
+#include <cstdlib>
+#include "chunk_cut.h"
+int main(int argc, char **argv) {
+    for (int i = 1; i + 1 < argc; i += 2)
+        std::printf("%d\n", k3da_chunk::page_masked(std::atoi(argv[i]), std::atoi(argv[i + 1])));
+    return 0;
+}
+"""
+
+
+def test_pages_at_the_end_of_the_longest_table(tmp_path):
+    """In 32 bits, with overflows trapped: every page a tile can begin up to
+    2^31 - 64 keys, against whole numbers."""
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("g++ not available")
+    (tmp_path / "p.cpp").write_text(PAGES_HARNESS)
+    subprocess.run([gxx, "-std=c++17", "-O0", "-ftrapv", "-I", CSRC, str(tmp_path / "p.cpp"), "-o", str(tmp_path / "p")], check=True)
+    end = (2 ** 25 - 1) * 64
+    pages = [0, 64, 128, end - 192, end - 128, end - 64, end]
+    cases = [(p, n) for p in pages for q in pages for n in (q - 1, q, q + 1, q + 63, q + 64, q + 65) if 0 <= n <= end]
+    out = subprocess.run([str(tmp_path / "p")] + [str(v) for c in cases for v in c], check=True, capture_output=True, text=True).stdout.split()
+    assert out == ["1" if p + 64 > n else "0" for p, n in cases]
+    for name in ("k3da_chunk.cu", "k3da_chunk_small.cu"):
+        src = open(os.path.join(CSRC, name)).read()
+        assert "page_masked(key0, least)" in src and "key0 + kP" not in src
