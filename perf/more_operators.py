@@ -297,7 +297,6 @@ def _prepare_book(case, seed, s):
     for part, v in zip(_parts(case, flat), (table, np.array(lens, np.int32), refs)):
         part.copy_(torch.from_numpy(v))
     s["start"], s["now"] = flat, flat.clone()
-    s["held"] = _parts(case, s["now"])  # what a user of the calls has in hand
     if case["op"] == "resize":
         s["new_lens"], s["copies"] = _ints(new), _ints([[-1] * R] * 3)
     elif case["op"] == "fork":
@@ -510,7 +509,7 @@ def _own_run(s):
         k3da.k3da_kv_copy(s["pool"], s["copies"], kv_scales=s["scales"])
         return {"pool": s["pool"]} if s["scales"] is None else {"pool": s["pool"], "scales": s["scales"]}
     s["now"].copy_(s["start"])  # the calls change the pages in place: each pass starts from the same
-    table, lens, refs = s["held"]
+    table, lens, refs = _parts(s["case"], s["now"])
     if op == "resize":
         k3da.k3da_pages_resize(table, lens, refs, s["new_lens"], s["copies"])
         return {"page_table": table, "lens": lens, "refs": refs, "copies": s["copies"]}
