@@ -249,6 +249,10 @@ struct Stat {
     };
 };
 __device__ __forceinline__ float finite(float top) { return fmaxf(top, -3.402823466e38f); }
+// Bit for bit the same if a and b change places: two lanes that join each
+// other's get one result, and so all threads of the row do.  (Contracted, one
+// of the products would not be rounded, and equal logits would differ by the
+// thread that holds them.)
 template <bool EXACT>
 __device__ __forceinline__ Stat join(Stat a, Stat b, bool greedy, Slope half) {
     Stat r;
@@ -259,7 +263,7 @@ __device__ __forceinline__ Stat join(Stat a, Stat b, bool greedy, Slope half) {
     }
     const Pair e = roots<EXACT>(pair_of(a.top, b.top), finite(r.top), half);
     const float2 w = both_of(mul2(e, e));
-    r.sum = a.sum * (a.top == r.top ? 1.f : w.x) + b.sum * (b.top == r.top ? 1.f : w.y);
+    r.sum = __fadd_rn(__fmul_rn(a.sum, a.top == r.top ? 1.f : w.x), __fmul_rn(b.sum, b.top == r.top ? 1.f : w.y));
     return r;
 }
 
