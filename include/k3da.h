@@ -454,7 +454,10 @@ typedef enum { K3DA_LOGITS_BF16 = 0, K3DA_LOGITS_FP16 = 1, K3DA_LOGITS_FP32 = 2 
  *
  * Logits that are -inf have probability 0; a row of nothing else is all 0.
  * Logits of +inf share the row.  A row with a NaN becomes NaN.  (All
- * zeros and NaN: BAD_TOKEN.)  The exponent is rounded once to fp32, sums are fp32.
+ * zeros and NaN: BAD_TOKEN.)  Arithmetic is fp32: x - top is rounded (where it
+ * is not exact), the exponent E = (x - top) / tau is, and for 16-bit logits
+ * 1 / tau; with n of these roundings a weight exp(E) is off by less than
+ * (n |E| + 9) 2^-24 of itself.  Sums are fp32.
  */
 int k3da_token_probs(float *probs, int64_t probs_row_stride, const void *logits, int logits_dtype,
                      int64_t logits_row_stride, int num_tokens, int vocab, const float *temperatures,

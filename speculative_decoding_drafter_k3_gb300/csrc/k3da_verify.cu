@@ -82,6 +82,7 @@ struct ProbParams {
 struct Slope {
     float hi, lo;
 };
+template <bool EXACT>
 __device__ __forceinline__ Slope half_slope(float temperature) {
     constexpr float kHalfHi = 0.721347510814666748046875f, kHalfLo = 9.6298149556330875e-9f;  // log2(e) / 2
     const float r = __frcp_rn(temperature);
@@ -92,6 +93,7 @@ __device__ __forceinline__ Slope half_slope(float temperature) {
     // Not at the ends of the range, and not where its product with a distance could
     // be infinite and hide the other one.
     if (!(fabsf(s.lo) < s.hi) || s.hi > 0x1p23f) s.lo = 0.f;
+    if (!EXACT) s.hi = __fadd_rn(s.hi, s.lo);  // rounded once
     s.hi = fminf(fmaxf(s.hi, 0x1p-149f), 3.402823466e38f);
     return s;
 }
@@ -134,9 +136,10 @@ __device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
 // finite `top`: with half the slope the hardware's power of two gives no
 // subnormal, and the square rounds those that the result has; its error
 // (2^-22) counts twice.  -inf, and a difference that passes fp32's range, give 0.
-// Logits of 16 bits are apart by whole numbers of their own steps, so the
-// slope's rounding is the only one in front of the exponent's; with fp32
-// (EXACT) it is made up for.
+// What is rounded in front of that: the exponent; the difference, which is exact
+// for 16-bit logits of about the same size; and for those the slope.  With fp32
+// (EXACT) that is made up for by its low part, an instruction a logit: 16-bit logits
+// with it 46.2 us instead of 43.6 (301 rows of 128,003).
 template <bool EXACT>
 __device__ __forceinline__ Pair roots(Pair x, float top, Slope half) {
     const Pair d = add2(x, pair_of(-top, -top)), hi = pair_of(half.hi, half.hi);
@@ -367,7 +370,7 @@ __global__ void __launch_bounds__(THREADS, (K * Logits<L>::kWords == 8 ? 5 : 4) 
     if (p.cluster > 1) cluster_wait();  // all of the cluster's CTAs run
     if (owner[0] == 0.f) return;        // all CTAs of the row alike
     const bool greedy = !(owner[1] > 0.f);
-    const Slope half = half_slope(greedy ? 1.0f : owner[1]);
+    const Slope half = half_slope<kExact>(greedy ? 1.0f : owner[1]);
 
     Stat s;
     s.top = -INFINITY;

@@ -1,4 +1,9 @@
-"""Probabilities within a row (GPU): what is equal stays equal."""
+"""Probabilities within a row (GPU): what is equal stays equal, and each is as
+near to its definition as the header says, at any distance below the largest
+logit and any temperature."""
+import math
+
+import numpy as np
 import pytest
 import torch
 
@@ -27,3 +32,44 @@ def test_equal_logits_have_equal_probabilities(T, V, dtype):
     out = out.gather(-1, at)
     alike, same = x[:, 1:] == x[:, :-1], out[:, 1:] == out[:, :-1]
     assert alike.any() and same[alike].all(), (int((~same)[alike].sum()), int(alike.sum()))
+
+
+def check_near(got, x, t):
+    """x [T, 8] as given, t [T].  With E = (x - top) / t a weight exp(E) is off by
+    less than (n |E| + 9) 2^-24 of itself: half a step of each rounding in front
+    of the power of two counts |E| 2^-24, the exponent's, the difference's where it
+    is not exact, and with 16-bit logits that of 1 / t; the power of two's 2^-22
+    counts twice, and its square is rounded.  The sum's terms bring theirs along,
+    and up to 6 additions; 1 / sum and the product are rounded too."""
+    short, top = x.dtype != torch.float32, x.float().amax(-1, keepdim=True)
+    n = 1 + int(short) + (x.double() - top.double() != (x.float() - top).double()).numpy()
+    x, t = x.double().numpy(), np.array(t, np.float32).astype(np.float64)[:, None]
+    with np.errstate(invalid="ignore", over="ignore"):
+        e = np.where(x == -math.inf, -math.inf, (x - x.max(-1, keepdims=True)) / t)
+    w = np.exp(e)
+    off = np.where(e < 0, n * np.abs(np.where(w > 0, e, 0)) + 9, 0)
+    total = w.sum(-1, keepdims=True)
+    rel = 2.0 ** -24 * (off + (w * off).sum(-1, keepdims=True) / total + 8)
+    want = w / total
+    got = got.double().cpu().numpy()
+    err = np.abs(got - want) / np.maximum(want, 2.0 ** -126)  # below, steps no longer shrink
+    bad = err > rel + 2.0 ** -20 * (want < 2.0 ** -126)
+    assert not bad.any(), (int(bad.sum()), t[bad.any(-1)][:3].tolist(), x[bad][:3], (err / rel).max())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_far_below_the_largest_logit(dtype):
+    """Distances of up to 87 temperatures, large ones next to small ones, at
+    temperatures of which some are those where log2(e) / t is furthest from
+    fp32."""
+    g = torch.Generator().manual_seed(1)
+    t = torch.exp(torch.rand(200000, generator=g) * math.log(8.0)) * 0.3
+    slope = 1 / (math.log(2.0) * t.double())
+    off = ((slope.float().double() - slope) / slope).abs()
+    t = torch.cat([torch.tensor([0.71901906]), t[:511], t[off.topk(512).indices]])
+    x = torch.empty(1024, 8)
+    x[:, 0] = 8 * torch.rand(1024, generator=g) * (torch.rand(1024, generator=g) < 0.5) + 8e-3 * torch.rand(1024, generator=g)
+    x[:, 1:] = x[:, :1] - 87 * t[:, None] * torch.rand(1024, 7, generator=g)
+    x[0, 0], x[0, 1:] = 8, -26.25
+    x = x.to(DTYPES[dtype])
+    check_near(probs_of(x, list(range(1025)), t.tolist()), x, t.tolist())
