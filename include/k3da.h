@@ -450,14 +450,15 @@ typedef enum { K3DA_LOGITS_BF16 = 0, K3DA_LOGITS_FP16 = 1, K3DA_LOGITS_FP32 = 2 
  *   vocab        1 .. 2^22.
  *   temperatures [num_requests] fp32, tau of request r's rows, or NULL: 1.
  *                Where tau is not above 0, the row is 1 at its first largest
- *                logit and 0 elsewhere.
+ *                logit and 0 elsewhere; above 0 it counts as 2^-126 at least.
  *
  * Logits that are -inf have probability 0; a row of nothing else is all 0.
  * Logits of +inf share the row.  A row with a NaN becomes NaN.  (All
  * zeros and NaN: BAD_TOKEN.)  Arithmetic is fp32: x - top is rounded (where it
  * is not exact), the exponent E = (x - top) / tau is, and for 16-bit logits
  * 1 / tau; with n of these roundings a weight exp(E) is off by less than
- * (n |E| + 9) 2^-24 of itself.  Sums are fp32.
+ * (n |E| + 9) 2^-24 of itself.  (tau up to 2^120; above, 2^-18 is added.)  A
+ * difference that passes fp32's range counts as infinite.  Sums are fp32.
  */
 int k3da_token_probs(float *probs, int64_t probs_row_stride, const void *logits, int logits_dtype,
                      int64_t logits_row_stride, int num_tokens, int vocab, const float *temperatures,

@@ -77,24 +77,23 @@ struct ProbParams {
 };
 
 // Half of what turns a distance below the row's largest logit into a power of
-// two, log2(e) / temperature, as the sum of two floats.  Kept inside fp32's range: at
-// an infinite temperature the longest distance still counts 2^-21.
+// two, log2(e) / temperature, as the sum of two floats, both above 0: -inf stays
+// -inf, and products that leave fp32's range leave it on the same side.  (EXACT:
+// used as such; else their sum, rounded once.)  At an infinite temperature the
+// longest distance still counts 2^-20.
 struct Slope {
     float hi, lo;
 };
 template <bool EXACT>
 __device__ __forceinline__ Slope half_slope(float temperature) {
-    constexpr float kHalfHi = 0.721347510814666748046875f, kHalfLo = 9.6298149556330875e-9f;  // log2(e) / 2
-    const float r = __frcp_rn(temperature);
-    const float e = __fmaf_rn(-r, temperature, 1.0f);  // 1/temperature = r + r e
+    constexpr float kHi = 0x1.715470p-1f, kLo = 0x1.94ae0cp-23f;  // log2(e) / 2: hi is so far below it that lo is never below 0
+    const float t = fmaxf(temperature, 0x1p-126f), r = __frcp_rn(t);
+    const float e = __fmaf_rn(-r, t, 1.0f);  // 1/t = r + r e
     Slope s;
-    s.hi = __fmul_rn(kHalfHi, r);
-    s.lo = __fmaf_rn(kHalfHi, r, -s.hi) + __fmaf_rn(s.hi, e, __fmul_rn(kHalfLo, r));
-    // Not at the ends of the range, and not where its product with a distance could
-    // be infinite and hide the other one.
-    if (!(fabsf(s.lo) < s.hi) || s.hi > 0x1p23f) s.lo = 0.f;
-    if (!EXACT) s.hi = __fadd_rn(s.hi, s.lo);  // rounded once
-    s.hi = fminf(fmaxf(s.hi, 0x1p-149f), 3.402823466e38f);
+    s.hi = __fmul_rn(kHi, r);
+    s.lo = __fadd_rn(__fmaf_rn(kHi, r, -s.hi), __fmaf_rn(s.hi, e, __fmul_rn(kLo, r)));
+    s.lo = fmaxf(s.lo, 0x1p-149f);  // (infinity: no number so far)
+    s.hi = EXACT ? fmaxf(s.hi, 0x1p-149f) : __fadd_rn(s.hi, s.lo);
     return s;
 }
 
@@ -143,12 +142,7 @@ __device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
 template <bool EXACT>
 __device__ __forceinline__ Pair roots(Pair x, float top, Slope half) {
     const Pair d = add2(x, pair_of(-top, -top)), hi = pair_of(half.hi, half.hi);
-    const Pair a = EXACT ? fma2(d, hi, mul2(d, pair_of(half.lo, half.lo))) : mul2(d, hi);
-    float2 e = both_of(a);
-    if (EXACT) {  // (-inf times a low part that is not above 0 gives no number)
-        e.x = fmaxf(e.x, -100.f);
-        e.y = fmaxf(e.y, -100.f);
-    }
+    float2 e = both_of(EXACT ? fma2(d, hi, mul2(d, pair_of(half.lo, half.lo))) : mul2(d, hi));
     asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
     asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
     return pair_of(e.x, e.y);

@@ -73,3 +73,32 @@ def test_far_below_the_largest_logit(dtype):
     x[0, 0], x[0, 1:] = 8, -26.25
     x = x.to(DTYPES[dtype])
     check_near(probs_of(x, list(range(1025)), t.tolist()), x, t.tolist())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_logits_and_temperatures_over_the_whole_range(dtype):
+    """Temperatures of 2^-126 to 2^120, logits of their size and of the type's."""
+    most = torch.finfo(DTYPES[dtype]).max
+    parts = torch.tensor([1.0, -1.0, 0.0, 0.5, -0.25, 1e-3, -0.75, -math.inf], dtype=torch.float64)
+    rows, t = [], []
+    for tau in (2.0 ** -126, 1.7e-38, 1e-37, 2.0 ** -100, 1e-20, 2e-8, 1e-7, 1e-6, 0.9, 2.0 ** 24, 1e20, 2.0 ** 64, 1.2e30, 2.0 ** 120):
+        for size in (most / 2, 20 * tau, 7 * tau, tau, 1.0, 2.0 ** -124):
+            rows.append(parts * min(size, most / 2))
+            t.append(tau)
+    x, cu = torch.stack(rows).to(torch.float32).to(DTYPES[dtype]), list(range(len(t) + 1))
+    check_near(probs_of(x, cu, t), x, t)
+    # Below 2^-126 a temperature counts as that.
+    least = probs_of(x, cu, [2.0 ** -126] * len(t))
+    for tau in (1e-38, 1e-42, 2.0 ** -149):
+        assert torch.equal(probs_of(x, cu, [tau] * len(t)), least)
+    # At an infinite one the words that are not masked share the row: the longest
+    # difference, 2^128, counts 2^-20 times log(2), twice.
+    out = probs_of(x, cu, [math.inf] * len(t))
+    assert (out[:, 7] == 0).all() and ((out[:, :7] - 1 / 7).abs() < 2.0 ** -19 / 7).all()
+
+
+def test_a_difference_beyond_fp32_counts_as_infinite():
+    most = torch.finfo(torch.float32).max
+    x = torch.tensor([[most, -most, -0.5 * most, 0.0, -math.inf]])
+    out = probs_of(x, [0, 1], [1e38])[0].tolist()
+    assert out[1] == out[2] == out[4] == 0 and abs(out[3] / out[0] - math.exp(-most / float(torch.tensor(1e38)))) < 1e-6
