@@ -577,6 +577,8 @@ size_t k3da_compact_workspace_bytes(int64_t num_pages);
  *                the GPU need one each.
  *
  * Pages counted in refs but listed in no row move too: copies says where.
+ * The call may be two launches; where it fails (K3DA_ECUDA) the state is as it
+ * was, unless the failure is the context's.
  */
 int k3da_pages_compact(int32_t *page_table, int page_stride, int32_t *lens, int num_requests, int32_t *refs,
                        int64_t num_pages, int32_t *copies, int max_copies, int32_t *num_copies, void *workspace,

@@ -524,9 +524,12 @@ __global__ void __launch_bounds__(kForkThreads) k3da_pages_fork_kernel(const __g
 // ones below n: the k-th highest goes into the k-th lowest.  A limit on the
 // moves so frees the pool's end first.  A cluster counts, lists the moves, and
 // leaves in `to` where each page at n and above is afterwards; a second kernel
-// rewrites the rows.  Bound by latency: counts, n, places and moves follow one
+// moves the counts and rewrites the rows.  (All that it changes of the book it
+// changes there: should its launch be refused, rows and counts still belong
+// together.)  Bound by latency: counts, n, places and moves follow one
 // another with a barrier between each.  262,144 pages, 23,666 moved,
-// 276,897 entries of 1024 rows looked at: 13.8 us (one CTA: 153); 512 pages: 5.7.
+// 276,897 entries of 1024 rows looked at: 13.2 us (one CTA: 153; counts moved by the
+// first kernel: 14.0); 512 pages: 5.9.
 
 struct CompactParams {
     Book b;
@@ -542,6 +545,12 @@ struct CompactParams {
 // thread: 8 rows of 40 entries, 512 pages: 5.7 us instead of 6.1, and a launch less on
 // the host.  (Three entries a thread: 64 rows of 40 6.9 us instead of 6.1.)
 constexpr int kRowsToo = kThreads;
+
+// A page's count goes with it.  (No page is moved from and to.)
+__device__ __forceinline__ void move_count(const Book &b, int from, int to) {
+    b.refs[to] = load_now(b.refs + from);
+    b.refs[from] = 0;
+}
 
 __global__ void __launch_bounds__(kThreads) k3da_pages_compact_kernel(const __grid_constant__ CompactParams p) {
     __shared__ Counts counts[2];
@@ -613,8 +622,7 @@ __global__ void __launch_bounds__(kThreads) k3da_pages_compact_kernel(const __gr
         const int x = load_now(from_list + k), y = load_now(to_list + k);
         tokens[k] = kP;
         p.to[x] = y;
-        b.refs[y] = load_now(b.refs + x);
-        b.refs[x] = 0;
+        if (p.rows_too) move_count(b, x, y);
     }
     if (rank == 0 && tid == 0) {
         p.num_copies[0] = moves;
@@ -644,6 +652,9 @@ __global__ void __launch_bounds__(kRenameThreads) k3da_pages_rename_kernel(const
     const int len = load_here(b.lens + blockIdx.y);
     const int live = load_here(p.to + b.num_pages), moves = load_here(p.to + b.num_pages + 1);
     if (moves == 0) return;
+    for (long long k = (static_cast<long long>(blockIdx.x) * gridDim.y + blockIdx.y) * kRenameThreads + threadIdx.x; k < moves;
+         k += static_cast<long long>(gridDim.x) * gridDim.y * kRenameThreads)
+        move_count(b, load_here(p.copies + k), load_here(p.copies + p.max_copies + k));
     if (len < 0 || len > b.page_stride * kP) {
         if (threadIdx.x == 0) flag(b.status, K3DA_STATUS_BAD_LENGTH);
         return;
