@@ -522,7 +522,12 @@ int k3da_verify(void *out_tokens, int32_t *num_out, const void *tokens, int toke
  *
  * A violation that only the kernels see: a length outside [0, page_stride *
  * 64] BAD_LENGTH (the request is left out), an entry that is no page
- * BAD_PAGE (skipped), a count below the page's holders BAD_COUNT.  With a state
+ * BAD_PAGE (skipped), a count below the page's holders BAD_COUNT (below 0: the
+ * page is never given).  Reported is what a call comes across: resize and
+ * compact look at all lengths, and at all counts for those below 0; fork at its
+ * requests' lengths; all of them at the entries that change hands or move (compact:
+ * at all entries, if any page moves); and resize compares counts and holders
+ * of pages that are given back or parted.  With a state
  * that violates this, which pages are given is left open; nothing outside
  * the arrays is touched.
  *

@@ -92,10 +92,11 @@ __device__ __forceinline__ Stretch stretch_of(int num_pages, int part, int parts
     return s;
 }
 
-// What the lane finds from `base` on, in steps of 128 pages.
-__device__ __forceinline__ void look(const int32_t *refs, Stretch s, int base, unsigned (&used)[kAhead],
+// What the lane finds from `base` on, in steps of 128 pages.  A count below 0 is
+// reported; its page stays out of use.
+__device__ __forceinline__ void look(const Book &b, Stretch s, int base, unsigned (&used)[kAhead],
                                      unsigned (&there)[kAhead]) {
-    int32_t n[kAhead][4];
+    int32_t n[kAhead][4], all = 0;
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
         const int page = base + 128 * i;
@@ -103,11 +104,11 @@ __device__ __forceinline__ void look(const int32_t *refs, Stretch s, int base, u
         if (page + 4 <= s.hi) {
             asm volatile("ld.relaxed.gpu.global.v4.b32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(n[i][0]), "=r"(n[i][1]), "=r"(n[i][2]), "=r"(n[i][3])
-                         : "l"(refs + page)
+                         : "l"(b.refs + page)
                          : "memory");
         } else {
             for (int k = 0; k < 4; ++k)
-                if (page + k < s.hi) n[i][k] = load_now(refs + page + k);
+                if (page + k < s.hi) n[i][k] = load_now(b.refs + page + k);
         }
     }
 #pragma unroll
@@ -115,10 +116,12 @@ __device__ __forceinline__ void look(const int32_t *refs, Stretch s, int base, u
         used[i] = there[i] = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
+            all |= n[i][k];
             used[i] |= n[i][k] != 0 ? 1u << k : 0u;
             there[i] |= base + 128 * i + k < s.hi ? 1u << k : 0u;
         }
     }
+    if (all < 0) flag(b.status, K3DA_STATUS_BAD_COUNT);
 }
 
 // What was found at a stretch's start can be kept (up to 262,144 pages that is
@@ -129,7 +132,7 @@ struct Seen {
     unsigned used[kAhead], there[kAhead];
 };
 template <typename F>
-__device__ __forceinline__ void walk(const int32_t *refs, Stretch s, const Seen *seen, F f) {
+__device__ __forceinline__ void walk(const Book &b, Stretch s, const Seen *seen, F f) {
     const int lane = threadIdx.x & 31;
     for (int base = s.lo; base < s.hi; base += 128 * kAhead) {
         unsigned used[kAhead], there[kAhead];
@@ -140,7 +143,7 @@ __device__ __forceinline__ void walk(const int32_t *refs, Stretch s, const Seen 
                 there[i] = seen->there[i];
             }
         }
-        if (seen == nullptr || base != s.lo) look(refs, s, base + 4 * lane, used, there);
+        if (seen == nullptr || base != s.lo) look(b, s, base + 4 * lane, used, there);
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             if (base + 128 * i >= s.hi) break;
@@ -400,7 +403,7 @@ __global__ void __launch_bounds__(kThreads) k3da_pages_resize_kernel(const __gri
     first_page[tid] = moves ? len / kP : held;
     const Stretch mine = stretch_of(b.num_pages, part_of(rank, warp, cluster), cluster * kWarps);
     int free_here = 0;
-    walk(b.refs, mine, nullptr, [&](int, unsigned used, unsigned there) { free_here += __popc(there & ~used); });
+    walk(b, mine, nullptr, [&](int, unsigned used, unsigned there) { free_here += __popc(there & ~used); });
     tell_all(counts, make_int2(warp_sum(free_here), 0), cluster);
     int2 before, total;
     sums_of(counts, cluster, before, total);
@@ -418,7 +421,7 @@ __global__ void __launch_bounds__(kThreads) k3da_pages_resize_kernel(const __gri
     long long next = before.x;  // the stretch's next free page is the next-th of all
     for (int base = mine.lo; base < mine.hi && next < needed; base += 128 * kAhead) {
         unsigned used[kAhead], there[kAhead];
-        look(b.refs, mine, base + 4 * lane, used, there);
+        look(b, mine, base + 4 * lane, used, there);
         int until[kAhead], all = 0;  // free pages of the steps so far
         __syncwarp();
 #pragma unroll
@@ -563,15 +566,15 @@ __global__ void __launch_bounds__(kThreads) k3da_pages_compact_kernel(const __gr
     const Stretch mine = stretch_of(b.num_pages, part_of(rank, warp, cluster), cluster * kWarps);
     int2 n = make_int2(0, 0), before, total;
     Seen seen;
-    look(b.refs, mine, mine.lo + 4 * (tid & 31), seen.used, seen.there);
-    walk(b.refs, mine, &seen, [&](int, unsigned used, unsigned) { n.x += __popc(used); });
+    look(b, mine, mine.lo + 4 * (tid & 31), seen.used, seen.there);
+    walk(b, mine, &seen, [&](int, unsigned used, unsigned) { n.x += __popc(used); });
     if (cluster > 1) cluster_wait();  // all of the cluster's CTAs run
     tell_all(counts[0], make_int2(warp_sum(n.x), 0), cluster);
     sums_of(counts[0], cluster, before, total);
     const int live = total.x;
     // Live ones at n and above, free ones below.
     n = make_int2(0, 0);
-    walk(b.refs, mine, &seen, [&](int page, unsigned used, unsigned there) {
+    walk(b, mine, &seen, [&](int page, unsigned used, unsigned there) {
         const unsigned high = from(page, live);
         n.x += __popc(used & high);
         n.y += __popc(there & ~used & ~high);
@@ -583,7 +586,7 @@ __global__ void __launch_bounds__(kThreads) k3da_pages_compact_kernel(const __gr
     const int moves = min(total.x, p.max_copies);
     int kth_high = total.x - 1 - before.x, kth_low = before.y;  // of the stretch's next one
     int32_t *const from_list = p.copies, *const to_list = p.copies + p.max_copies, *const tokens = to_list + p.max_copies;
-    walk(b.refs, mine, &seen, [&](int page, unsigned used, unsigned there) {
+    walk(b, mine, &seen, [&](int page, unsigned used, unsigned there) {
         const unsigned high = from(page, live), up = used & high, down = there & ~used & ~high;
         const int base = page - 4 * static_cast<int>(threadIdx.x & 31);
         if (base + 128 > live) {
@@ -629,7 +632,7 @@ __global__ void __launch_bounds__(kThreads) k3da_pages_compact_kernel(const __gr
         p.to[b.num_pages] = live;
         p.to[b.num_pages + 1] = moves;
     }
-    if (!p.rows_too || moves == 0) return;
+    if (!p.rows_too) return;
     __threadfence();
     __syncthreads();
     const int r = tid / b.page_stride, j = tid - r * b.page_stride;
@@ -637,7 +640,7 @@ __global__ void __launch_bounds__(kThreads) k3da_pages_compact_kernel(const __gr
     const int len = load_here(b.lens + r), page = load_here(b.page_table + tid);
     if (len < 0 || len > b.page_stride * kP) {
         if (j == 0) flag(b.status, K3DA_STATUS_BAD_LENGTH);
-    } else if (j < pages_for(len)) {
+    } else if (moves > 0 && j < pages_for(len)) {
         if (page < 0 || page >= b.num_pages) flag(b.status, K3DA_STATUS_BAD_PAGE);
         else if (page >= live) b.page_table[tid] = load_now(p.to + page);
     }
@@ -651,14 +654,13 @@ __global__ void __launch_bounds__(kRenameThreads) k3da_pages_rename_kernel(const
     wait_for_stream();
     const int len = load_here(b.lens + blockIdx.y);
     const int live = load_here(p.to + b.num_pages), moves = load_here(p.to + b.num_pages + 1);
+    const bool good = len >= 0 && len <= b.page_stride * kP;
+    if (!good && threadIdx.x == 0) flag(b.status, K3DA_STATUS_BAD_LENGTH);
     if (moves == 0) return;
     for (long long k = (static_cast<long long>(blockIdx.x) * gridDim.y + blockIdx.y) * kRenameThreads + threadIdx.x; k < moves;
          k += static_cast<long long>(gridDim.x) * gridDim.y * kRenameThreads)
         move_count(b, load_here(p.copies + k), load_here(p.copies + p.max_copies + k));
-    if (len < 0 || len > b.page_stride * kP) {
-        if (threadIdx.x == 0) flag(b.status, K3DA_STATUS_BAD_LENGTH);
-        return;
-    }
+    if (!good) return;
     int32_t *row = b.page_table + static_cast<long long>(blockIdx.y) * b.page_stride;
     const int held = pages_for(len);
     const int step = static_cast<int>(gridDim.x) * kRenameThreads;

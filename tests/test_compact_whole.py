@@ -1,5 +1,6 @@
-"""Pulling a pool together (GPU): the book stays whole if only the first of the
-call's kernels runs."""
+"""Pulling a pool together (GPU): what is violated is reported whether or not
+pages move, and the book stays whole if only the first of the call's kernels
+runs."""
 import ctypes
 import glob
 
@@ -11,6 +12,43 @@ import speculative_decoding_drafter_k3_gb300 as k3da
 from test_pages import Both, i32
 
 pytestmark = pytest.mark.gpu
+SIZES = [(4, 3, 30), (30, 100, 5000)]  # rows rewritten by the first kernel, and by a second one
+
+
+def compact(x, limit=8):
+    copies, num = torch.full((3, limit), 77, dtype=torch.int32, device="cuda"), i32([-1])
+    k3da.k3da_pages_compact(*x.t, copies, num, workspace=k3da.alloc_compact_workspace(len(x.b.refs)), status=x.status)
+    return int(num)
+
+
+@pytest.mark.parametrize("R,S,P", SIZES)
+@pytest.mark.parametrize("moves", [0, 1])
+def test_lengths_are_looked_at(R, S, P, moves):
+    x = Both(R, S, P)
+    x.resize([64] * R)
+    if moves:
+        x.resize([0] + [-1] * (R - 1))
+    for bad in (-1, S * 64 + 1):
+        x.t[1][2] = bad
+        compact(x)
+        x.flags(k3da.STATUS_BAD_LENGTH)
+        x.t[1][2] = 64
+        compact(x)
+        x.flags(0)
+
+
+@pytest.mark.parametrize("R,S,P", SIZES + [(2, 3, 140001)])
+def test_counts_below_zero_are_reported(R, S, P):
+    for page in (0, 1, P // 2, P - 1):
+        x = Both(R, S, P)
+        x.t[2][page] = -1
+        compact(x)
+        x.flags(k3da.STATUS_BAD_COUNT)
+        x = Both(R, S, P)
+        x.t[2][page] = -2 ** 31
+        k3da.k3da_pages_resize(*x.t, i32([64] + [0] * (R - 1)), x.copies, status=x.status)
+        x.flags(k3da.STATUS_BAD_COUNT)
+        assert int(x.t[2][page]) == -2 ** 31 and int(x.t[0][0, 0]) == (page == 0)
 
 
 def test_without_its_second_kernel_the_book_is_as_it_was():
