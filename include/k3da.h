@@ -466,7 +466,8 @@ int k3da_token_probs(float *probs, int64_t probs_row_stride, const void *logits,
 
 /*
  * k3da_verify -- keeps drafted tokens so that what comes out is distributed
- * as the target's own tokens, from given uniform numbers.  With request r's n
+ * as the target's own tokens (to the steps of uniform numbers: see below), from
+ * given uniform numbers.  With request r's n
  * rows at a = cu_seqlens[r], draft i (0 <= i < n - 1) is d = tokens[a + i + 1],
  * drawn from the distribution q of row a + i; the target's there is p.  It
  * stays if uniforms[a + i] * q(d) < p(d) (compared exactly), and the first
@@ -493,6 +494,12 @@ int k3da_token_probs(float *probs, int64_t probs_row_stride, const void *logits,
  * 0 where w is no number, p - q being rounded to fp32 once; the token is the
  * first whose running sum of W is above floor(sum W * floor(2^24 u) / 2^24).
  * Whole numbers, so the token does not depend on how the sum is split.
+ * How near that comes: a uniform number has 2^24 steps, so a word is drawn, and a
+ * draft kept, with its probability to 2^-24; a word whose share of the sum is
+ * below that may never be drawn, and over millions of words of small
+ * probability that adds up (a row of 3,000,000 equal ones: 0.04 in total variation).
+ * Cutting weights to 2^-40 loses vocab 2^-40 of the sum at most: nothing
+ * beside a sum of 1, but p - q may have a small one.
  * A draft outside [0, vocab) is rejected (BAD_TOKEN); a row without any
  * weight gives -1 (BAD_TOKEN); rows cu_seqlens[r] .. that do not lie in
  * [0, num_tokens] are left alone, with num_out 0 (BAD_LENGTH).

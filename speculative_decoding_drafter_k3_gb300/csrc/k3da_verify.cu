@@ -10,8 +10,11 @@
 // the total.  Running sums of rounded numbers depend on their order, and with
 // it the token would (in 0.4% of draws from 128,003 words in fp32); so weights are whole multiples of 2^-40 here, summed in
 // 64 bits: any split of a row over threads gives the same token.  A weight
-// below 2^-40 counts as nothing: a vocabulary of 2^18 such words loses less than
-// 2^-22 of the total.
+// below 2^-40 counts as nothing; a vocabulary of 2^18 words so loses less than
+// 2^-22 (of weights that add up to 1; of a difference p - q with a small sum that
+// is a larger part).  The share itself has 24 bits, what a uniform fp32 number
+// is sure to have: each word is met to 2^-24 of the total, and one of less may never
+// be drawn.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
