@@ -431,9 +431,9 @@ int k3da_chunk_attn(void *out, float *lse, const void *q, int64_t q_row_stride, 
 /* ------------------------------------------------------------------------
  * Around the drafts: probabilities of logits, and which drafts stay.  Packed
  * rows as above; the rows of request r's block are its known token and its
- * drafts, as k3da_chunk_attn takes them, and row i's logits are those of the
- * token behind it.  Any number of rows a request.  Memory, launches and the
- * rule on overlaps are those of the cache calls.
+ * drafts, as k3da_chunk_attn takes them, and the target's logits in row i are
+ * those of the token behind it.  Any number of rows a request.  Memory, launches
+ * and the rule on overlaps are those of the cache calls.
  */
 
 /* Type of the logits. */
@@ -483,9 +483,13 @@ int k3da_token_probs(float *probs, int64_t probs_row_stride, const void *logits,
  *   tokens       [num_tokens] int32 or int64 (token_dtype, a k3da_pos_dtype,
  *                out_tokens' too).
  *   target_probs [num_tokens, vocab] fp32 p, rows target_row_stride apart.
- *   draft_probs  [num_tokens, vocab] fp32 q, rows draft_row_stride apart; a
- *                request's last row is not used.  NULL: the drafts were
- *                certain, q is 1 at the draft and 0 elsewhere.
+ *   draft_probs  [num_tokens, vocab] fp32 q, rows draft_row_stride apart: row
+ *                i's is what token i + 1 was drawn from; a request's last row
+ *                is not used.  Of a drafter whose row i predicts token i
+ *                itself, pass the address of the second row (no row behind
+ *                the last token's is read).
+ *                NULL: the drafts were certain, q is 1 at the draft and 0
+ *                elsewhere.
  *   uniforms     [num_tokens] fp32 in [0, 1); a request's last one draws the
  *                token that follows.  Its first 24 binary places count.
  *   vocab, strides  as for k3da_token_probs.

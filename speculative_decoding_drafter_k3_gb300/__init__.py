@@ -636,7 +636,8 @@ def k3da_verify(out_tokens, num_out, tokens, target_probs, uniforms, cu_seqlens,
     """Which of the drafts ``tokens[cu[r] + 1:cu[r + 1]]`` stay, and the token
     that follows them, from ``uniforms`` [T] (C: k3da_verify).  ``target_probs``
     and ``draft_probs`` are [T, V] fp32, row i's those of the token behind row
-    i.  Returns ``out_tokens`` [T] and ``num_out`` [R]."""
+    i (of a drafter whose rows predict their own position: ``q[1:]`` of a ``q``
+    of one row more).  Returns ``out_tokens`` [T] and ``num_out`` [R]."""
     dev = target_probs.get_device()
     shape = target_probs.shape
     p, p_stride = _rows("target_probs", target_probs, dev, shape)

@@ -1,9 +1,12 @@
 """How near a draw comes to the distribution that it draws from, by the
-definition (CPU)."""
+definition (CPU); and a drafter whose rows predict their own position (GPU)."""
 import numpy as np
 import pytest
+import torch
 
+import speculative_decoding_drafter_k3_gb300 as k3da
 from draft_cases import draw, whole
+from test_verify import Blocks, i32
 
 STEPS = 2 ** 24
 
@@ -42,3 +45,17 @@ def test_words_below_a_step_may_never_be_drawn():
     w[0] = 2 ** 40 - 2 ** 27
     n = shares(w)
     assert set(n[1:].tolist()) <= {0, 1} and (n[1:] == 0).any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V", [41, 5003])
+def test_a_drafter_whose_rows_predict_their_own_position(V):
+    """Row i of such a drafter has the distribution of token i itself: its
+    probabilities are passed from the second row on, out of one row more."""
+    b = Blocks([6, 1, 0, 4, 3], V, 5)
+    own = torch.full((b.T + 1, V), 7.0, device="cuda")
+    own[1:] = b.q.cuda()
+    out, num = torch.full((b.T,), -7, dtype=torch.int32, device="cuda"), i32([-9] * 5)
+    k3da.k3da_verify(out, num, b.tokens.int().cuda(), b.p.cuda(), b.u.cuda(), i32(b.cu), draft_probs=own[1:])
+    want, counts = b.want()
+    assert (out.cpu().numpy() == want).all() and num.tolist() == counts
