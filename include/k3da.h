@@ -458,7 +458,13 @@ typedef enum { K3DA_LOGITS_BF16 = 0, K3DA_LOGITS_FP16 = 1, K3DA_LOGITS_FP32 = 2 
  * is not exact), the exponent E = (x - top) / tau is, and for 16-bit logits
  * 1 / tau; with n of these roundings a weight exp(E) is off by less than
  * (n |E| + 9) 2^-24 of itself.  (tau up to 2^120; above, 2^-18 is added.)  A
- * difference that passes fp32's range counts as infinite.  Sums are fp32.
+ * difference that passes fp32's range counts as infinite.  Sums are fp32, in
+ * an order that depends on vocab, on num_tokens and on the row's address modulo 32
+ * bytes: so may the last bits of a row's probabilities.  The same call gives the same
+ * bits, and equal logits of a row are equally probable.
+ *
+ * Up to K3DA_MAX_CHUNK_REQUESTS requests (k3da_verify takes more): temperatures
+ * of more than those take several calls.
  */
 int k3da_token_probs(float *probs, int64_t probs_row_stride, const void *logits, int logits_dtype,
                      int64_t logits_row_stride, int num_tokens, int vocab, const float *temperatures,
