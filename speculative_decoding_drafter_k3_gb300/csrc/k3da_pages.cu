@@ -266,7 +266,7 @@ int cluster_for(void (*kernel)(Params), int64_t num_pages, std::atomic<int> (&ru
 // cluster works out for itself what each request needs (a thread each); giving
 // back and looking for free pages is shared.  Bound by latency: a few bytes
 // a page and request, read one after the other.  1024 requests over 262,144
-// pages, 32,869 given back and 9,165 taken: 12.7 us (one CTA: 240); 8 requests that
+// pages, 32,869 given back and 9,165 taken: 12.8 us (one CTA: 240); 8 requests that
 // each grow by 8 tokens, 512 pages: 4.7.
 
 constexpr int kSlots = 2 * kMaxRequests;  // of the table of begun pages
@@ -531,8 +531,8 @@ __global__ void __launch_bounds__(kForkThreads) k3da_pages_fork_kernel(const __g
 // changes there: should its launch be refused, rows and counts still belong
 // together.)  Bound by latency: counts, n, places and moves follow one
 // another with a barrier between each.  262,144 pages, 23,666 moved,
-// 276,897 entries of 1024 rows looked at: 13.2 us (one CTA: 153; counts moved by the
-// first kernel: 14.0); 512 pages: 5.9.
+// 276,897 entries of 1024 rows looked at: 13.3 us (one CTA: 153; counts moved by the
+// first kernel: 14.0); 512 pages: 5.8.
 
 struct CompactParams {
     Book b;

@@ -55,7 +55,7 @@ __device__ __forceinline__ float load_here(const float *p) {
 // CTAs with one exchange.  Weights are formed twice, for the sum and for the
 // result: as fp32 they would take twice the registers, and CTAs of 256
 // threads, four on an SM, hide each other's waits (512 threads: 59 us instead of
-// 43, three on an SM 48).  301 rows of 128,003 in bf16: 43.5 us, 5.3 TB/s, 0.77 of
+// 43, three on an SM 48).  301 rows of 128,003 in bf16: 43.7 us, 5.2 TB/s, 0.77 of
 // what a copy gets; a CTA's 9.5 us are 2.9 of loading, 1.6 of arithmetic, 3 of
 // reducing and waiting for the cluster's others, 1.9 of storing.
 //
@@ -719,7 +719,7 @@ template <typename L>
 int launch_probs(ProbParams &prm, cudaStream_t st) {
     constexpr int kMost = 32 / Logits<L>::kWords;  // chunks that a thread holds
     const int chunks = (prm.V + 14) / 8;
-    if (chunks <= 2 * kFewThreads) {  // 8000 rows of 1000: 16.6 us, 34.8 with 256 threads
+    if (chunks <= 2 * kFewThreads) {  // 8000 rows of 1000 (one request): 16.8 us, 34.8 with 256 threads
         prm.cluster = 1;
         return launch_clusters(k3da_token_probs_kernel<L, 2, kFewThreads>, dim3(static_cast<unsigned>(prm.T)), 1, kFewThreads, st,
                                prm);
