@@ -151,11 +151,13 @@ struct Span {
     size_t bytes;
 };
 
-// One of the first `written` of n spans overlaps another of the n.
+// One of the first `written` of n spans, or the last (the status word, written
+// too), overlaps another of the n.
 inline bool written_overlap(const Span *spans, int written, int n) {
-    for (int i = 0; i < written; ++i)
-        for (int j = i + 1; j < n; ++j)
-            if (spans[i].at && spans[j].at && overlap(spans[i].at, spans[i].bytes, spans[j].at, spans[j].bytes)) return true;
+    for (int i = 0; i < n; ++i)
+        for (int j = i < written ? i + 1 : n - 1; j < n; ++j)
+            if (i != j && spans[i].at && spans[j].at && overlap(spans[i].at, spans[i].bytes, spans[j].at, spans[j].bytes))
+                return true;
     return false;
 }
 
