@@ -544,7 +544,7 @@ int k3da_verify(void *out_tokens, int32_t *num_out, const void *tokens, int toke
  * compact look at all lengths, and at all counts for those below 0; fork at its
  * requests' lengths; all of them at the entries that change hands or move (compact:
  * at all entries, if any page moves); and resize compares counts and holders
- * of pages that are given back or parted.  With a state
+ * of pages that are given back or that a growing request writes into.  With a state
  * that violates this, which pages are given is left open; nothing outside
  * the arrays is touched.
  *

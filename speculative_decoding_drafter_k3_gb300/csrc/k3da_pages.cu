@@ -374,6 +374,7 @@ __global__ void __launch_bounds__(kThreads) k3da_pages_resize_kernel(const __gri
     // write into it now, the first of them keeps it.
     if (begun >= 0) {
         count = load_now(b.refs + begun);
+        if (count < 1 && rank == 0) flag(b.status, K3DA_STATUS_BAD_COUNT);
         if (count < 2) begun = -1;
     }
     bool moves = begun >= 0;

@@ -1,5 +1,5 @@
 """Pulling a pool together (GPU): what is violated is reported whether or not
-pages move, and the book stays whole if only the first of the call's kernels
+pages move (counts by resize too), and the book stays whole if only the first of the call's kernels
 runs."""
 import ctypes
 import glob
@@ -49,6 +49,14 @@ def test_counts_below_zero_are_reported(R, S, P):
         k3da.k3da_pages_resize(*x.t, i32([64] + [0] * (R - 1)), x.copies, status=x.status)
         x.flags(k3da.STATUS_BAD_COUNT)
         assert int(x.t[2][page]) == -2 ** 31 and int(x.t[0][0, 0]) == (page == 0)
+
+
+def test_a_page_that_is_written_next_but_not_counted_is_reported():
+    x = Both(3, 4, 20)
+    x.resize([130, 70, 20])
+    x.t[2][int(x.t[0][1, 1])] = 0
+    k3da.k3da_pages_resize(*x.t, i32([-1, 71, 21]), x.copies, status=x.status)
+    x.flags(k3da.STATUS_BAD_COUNT)
 
 
 def test_without_its_second_kernel_the_book_is_as_it_was():
