@@ -454,14 +454,16 @@ typedef enum { K3DA_LOGITS_BF16 = 0, K3DA_LOGITS_FP16 = 1, K3DA_LOGITS_FP32 = 2 
  *
  * Logits that are -inf have probability 0; a row of nothing else is all 0.
  * Logits of +inf share the row.  A row with a NaN becomes NaN.  (All
- * zeros and NaN: BAD_TOKEN.)  Arithmetic is fp32: x - top is rounded (where it
- * is not exact), the exponent E = (x - top) / tau is, and for 16-bit logits
- * 1 / tau; with n of these roundings a weight exp(E) is off by less than
- * (n |E| + 9) 2^-24 of itself.  (tau up to 2^120; above, 2^-18 is added.)  A
- * difference that passes fp32's range counts as infinite.  Sums are fp32, in
- * an order that depends on vocab, on num_tokens and on the row's address modulo 32
- * bytes: so may the last bits of a row's probabilities.  The same call gives the same
- * bits, and equal logits of a row are equally probable.
+ * zeros and NaN: BAD_TOKEN.)
+ *
+ * Arithmetic is fp32: x - top is rounded (where it is not exact), the exponent
+ * E = (x - top) / tau is, and for 16-bit logits 1 / tau; with n of these
+ * roundings a weight exp(E) is off by less than (n |E| + 9) 2^-24 of itself.
+ * (tau up to 2^120; above, 2^-18 is added.)  A difference that passes fp32's
+ * range counts as infinite.  The order of the sums depends on vocab, logits_dtype
+ * and num_tokens, and on the address of probs' row modulo 32 bytes, and so may the
+ * last bits of a row.  The same call gives the same bits, and for tau above 0
+ * equal logits of a row have equal probabilities.
  *
  * Up to K3DA_MAX_CHUNK_REQUESTS requests (k3da_verify takes more): temperatures
  * of more than those take several calls.
@@ -492,10 +494,9 @@ int k3da_token_probs(float *probs, int64_t probs_row_stride, const void *logits,
  *   draft_probs  [num_tokens, vocab] fp32 q, rows draft_row_stride apart: row
  *                i's is what token i + 1 was drawn from; a request's last row
  *                is not used.  Of a drafter whose row i predicts token i
- *                itself, pass the address of the second row (no row behind
- *                the last token's is read).
- *                NULL: the drafts were certain, q is 1 at the draft and 0
- *                elsewhere.
+ *                itself, pass the address of the second of num_tokens + 1
+ *                rows.  NULL: the drafts were certain, q is 1 at the draft and
+ *                0 elsewhere.
  *   uniforms     [num_tokens] fp32 in [0, 1); a request's last one draws the
  *                token that follows.  Its first 24 binary places count.
  *   vocab, strides  as for k3da_token_probs.
@@ -542,10 +543,11 @@ int k3da_verify(void *out_tokens, int32_t *num_out, const void *tokens, int toke
  * BAD_PAGE (skipped), a count below the page's holders BAD_COUNT (below 0: the
  * page is never given).  Reported is what a call comes across: resize and
  * compact look at all lengths, and at all counts for those below 0; fork at its
- * requests' lengths; all of them at the entries that change hands or move (compact:
- * at all entries, if any page moves); and resize compares counts and holders
- * of pages that are given back or that a growing request writes into.  With a state
- * that violates this, which pages are given is left open; nothing outside
+ * requests' lengths; all of them at the entries that change hands or move
+ * (compact: at all entries, if any page moves); resize compares counts with
+ * the holders that it meets: who gives a page back, who writes into it next (a
+ * count of 0), and all who write into a page that is parted.  With a state that
+ * violates this, which pages are given is left open; nothing outside
  * the arrays is touched.
  *
  * `copies` is [3, n] int32: page from, page to, tokens (the first ones of the
